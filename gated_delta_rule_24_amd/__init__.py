@@ -9,6 +9,16 @@ be loaded, every call raises.
 
     o, S = chunk_fwd(q, k, v, log_alpha, beta, init_state=None, cu_seqlens=None)
     o    = decode_step(state, q, k, v, log_alpha, beta)      # state updated in place
+
+Next to the gated delta rule, with the same conventions: the elementwise gated
+linear recurrence, layer norm, and moves of resident states.
+
+    h, s = scan_fwd(x, log_alpha, init_state=None, cu_seqlens=None)
+    dx, dlog_alpha, d_init = scan_bwd(log_alpha, h, d_h, init_state=None, d_final=None, cu_seqlens=None)
+    h    = scan_step(state, x, log_alpha)                    # state updated in place
+    y, mean, rstd = layernorm_fwd(x, weight=None, bias=None)
+    dx, dweight, dbias = layernorm_bwd(dy, x, mean, rstd, weight=None)
+    state_move(state, src, dst)                              # state updated in place
 """
 from __future__ import annotations
 
@@ -19,7 +29,9 @@ from typing import Optional
 import torch
 
 __all__ = ["GdnError", "chunk_fwd", "chunk_fwd_noalloc", "decode_step", "chunk_bwd", "chunk_fwd_workspace_size",
-           "chunk_bwd_workspace_size", "chunk_fwd_check", "load", "lib_path", "profile", "CHUNK"]
+           "chunk_bwd_workspace_size", "chunk_fwd_check", "scan_fwd", "scan_bwd", "scan_step", "scan_workspace_size",
+           "layernorm_fwd", "layernorm_bwd", "layernorm_bwd_workspace_size", "state_move", "state_move_check", "load",
+           "lib_path", "profile", "CHUNK"]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CHUNK = 64
@@ -45,6 +57,12 @@ class ChunkDesc(ctypes.Structure):
                 ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
                 ("chunk", ctypes.c_int32), ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
                 ("flags", ctypes.c_int32)]
+
+
+class ScanDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("num_seqs", ctypes.c_int32), ("in_dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
 
 
 def lib_path() -> str:
@@ -83,6 +101,17 @@ def load():
     lib.gdn_chunk_fwd_check.argtypes = [vp, vp, ctypes.POINTER(i32)]
     lib.gdn_decode_step.restype = ctypes.c_int
     lib.gdn_decode_step.argtypes = [i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    i64, scan_desc = ctypes.c_int64, ctypes.POINTER(ScanDesc)
+    for name, args in {
+            "gdn_scan_workspace_size": [scan_desc, ctypes.POINTER(sz)],
+            "gdn_scan_fwd": [scan_desc] + [vp] * 7 + [sz, vp],
+            "gdn_scan_bwd": [scan_desc] + [vp] * 10 + [sz, vp],
+            "gdn_scan_step": [i32] * 5 + [vp] * 5,
+            "gdn_layernorm_fwd": [i64, i32, i32, i32, ctypes.c_float] + [vp] * 7,
+            "gdn_layernorm_bwd_workspace_size": [i64, i32, ctypes.POINTER(sz)],
+            "gdn_layernorm_bwd": [i64, i32, i32, i32] + [vp] * 9 + [sz, vp],
+            "gdn_state_move": [i32, i32, i64, i32] + [vp] * 5}.items():
+        getattr(lib, name).restype, getattr(lib, name).argtypes = ctypes.c_int, args
     lib.gdn_profile_enable.restype = ctypes.c_int
     lib.gdn_profile_enable.argtypes = [i32]
     lib.gdn_profile_count.restype = ctypes.c_int
@@ -313,6 +342,230 @@ def decode_step(state, q, k, v, log_alpha, beta, *, out_dtype=torch.float32, o=N
                                _ptr(state), _ptr(q), _ptr(k), _ptr(v),
                                _ptr(log_alpha), _ptr(beta), _ptr(o), _stream(dev)))
     return o
+
+
+# ---- gated linear recurrence, layer norm, state moves ------------------------------
+
+_FLOATS = tuple(_DT)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, device, *args):
+    """One library call with `device` current and its current stream as the last argument."""
+    f = getattr(load(), name)
+    if torch.cuda.current_device() == device.index:
+        status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status != 0:
+        _check(status)
+
+
+def _cuda(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} is on {t.device}, expected a GPU")
+    return t.device
+
+
+def _shaped(t, name, shape, dtypes, device):
+    _need(t, name, dtypes, device, len(shape))
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+
+
+def _workspace(workspace, size, device):
+    if workspace is None:
+        return torch.empty(size, dtype=torch.uint8, device=device), size
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def scan_workspace_size(B, T, D, num_seqs, in_dtype=torch.bfloat16, gate_dtype=torch.float32,
+                        out_dtype=torch.float32) -> int:
+    d = ScanDesc(B, T, D, num_seqs, _DT[in_dtype], _DT[gate_dtype], _DT[out_dtype], 0)
+    n = ctypes.c_size_t(0)
+    _check(load().gdn_scan_workspace_size(ctypes.byref(d), ctypes.byref(n)))
+    return int(n.value)
+
+
+def _scan_call(B, T, D, in_dtype, gate_dtype, out_dtype, cu_seqlens, workspace, device):
+    """Descriptor, number of sequences and workspace of a scan_fwd or scan_bwd call."""
+    if cu_seqlens is None:
+        N = B
+    else:
+        _need(cu_seqlens, "cu_seqlens", (torch.int32,), device, 1)
+        N = cu_seqlens.shape[0] - 1
+    desc = ScanDesc(B, T, D, N, _DT[in_dtype], _DT[gate_dtype], _DT[out_dtype], 0)
+    need = ctypes.c_size_t(0)
+    _check(load().gdn_scan_workspace_size(ctypes.byref(desc), ctypes.byref(need)))
+    return desc, N, *_workspace(workspace, need.value, device)
+
+
+def scan_fwd(x, log_alpha, init_state=None, cu_seqlens=None, *, out_dtype=torch.float32, h=None, final_state=True,
+             workspace=None):
+    """Gated linear recurrence h_t = exp(log_alpha_t) h_{t-1} + x_t per channel.
+
+    x [B,T,D], log_alpha [B,T,D] (each fp32 or one 16-bit type); init_state
+    [N,D] fp32 or None (zeros); cu_seqlens int32 [N+1] (packed batch, B == 1)
+    or None.  final_state: True (allocate), False/None (not returned) or a
+    tensor to write (it may be init_state itself).  Returns (h [B,T,D],
+    final_state [N,D] or None).
+    """
+    dev = _cuda(x, "x")
+    _need(x, "x", _FLOATS, dev, 3)
+    B, T, D = shape = tuple(x.shape)
+    _shaped(log_alpha, "log_alpha", shape, _FLOATS, dev)
+    if h is None:
+        h = torch.empty(shape, dtype=out_dtype, device=dev)
+    else:
+        _shaped(h, "h", shape, _FLOATS, dev)
+    desc, N, workspace, size = _scan_call(B, T, D, x.dtype, log_alpha.dtype, h.dtype, cu_seqlens, workspace, dev)
+    if init_state is not None:
+        _shaped(init_state, "init_state", (N, D), (torch.float32,), dev)
+    if final_state is True:
+        final_state = torch.empty((N, D), dtype=torch.float32, device=dev)
+    elif final_state is False:
+        final_state = None
+    elif final_state is not None:
+        _shaped(final_state, "final_state", (N, D), (torch.float32,), dev)
+    _call("gdn_scan_fwd", dev, desc, _addr(x), _addr(log_alpha), _addr(init_state), _addr(cu_seqlens), _addr(h),
+          _addr(final_state), _addr(workspace), size)
+    return h, final_state
+
+
+def scan_bwd(log_alpha, h, d_h, init_state=None, d_final=None, cu_seqlens=None, *, dx_dtype=torch.float32,
+             d_init=True, workspace=None):
+    """Gradients of scan_fwd's h and final state with respect to its inputs.
+
+    log_alpha, init_state, cu_seqlens as for scan_fwd; h is its output; d_h
+    [B,T,D] in h's dtype; d_final [N,D] fp32 or None (zeros).  dx_dtype: the
+    dtype of x.  d_init: True (allocate and return dL/d init_state) or False.
+    Returns (dx in dx_dtype, dlog_alpha in log_alpha's dtype, d_init or None).
+    """
+    dev = _cuda(h, "h")
+    _need(h, "h", _FLOATS, dev, 3)
+    B, T, D = shape = tuple(h.shape)
+    _shaped(log_alpha, "log_alpha", shape, _FLOATS, dev)
+    _shaped(d_h, "d_h", shape, (h.dtype,), dev)
+    dx = torch.empty(shape, dtype=dx_dtype, device=dev)
+    dla = torch.empty(shape, dtype=log_alpha.dtype, device=dev)
+    desc, N, workspace, size = _scan_call(B, T, D, dx_dtype, log_alpha.dtype, h.dtype, cu_seqlens, workspace, dev)
+    for name, t in (("init_state", init_state), ("d_final", d_final)):
+        if t is not None:
+            _shaped(t, name, (N, D), (torch.float32,), dev)
+    di = torch.empty((N, D), dtype=torch.float32, device=dev) if d_init else None
+    _call("gdn_scan_bwd", dev, desc, _addr(log_alpha), _addr(h), _addr(init_state), _addr(cu_seqlens), _addr(d_h),
+          _addr(d_final), _addr(dx), _addr(dla), _addr(di), _addr(workspace), size)
+    return dx, dla, di
+
+
+def scan_step(state, x, log_alpha, *, out_dtype=torch.float32, h=None):
+    """One token of the gated linear recurrence, in place on `state` [N,D]
+    fp32.  x, log_alpha [N,D].  Returns h [N,D], the new state in out_dtype."""
+    dev = _cuda(state, "state")
+    _need(state, "state", (torch.float32,), dev, 2)
+    shape = tuple(state.shape)
+    _shaped(x, "x", shape, _FLOATS, dev)
+    _shaped(log_alpha, "log_alpha", shape, _FLOATS, dev)
+    if h is None:
+        h = torch.empty(shape, dtype=out_dtype, device=dev)
+    else:
+        _shaped(h, "h", shape, _FLOATS, dev)
+    _call("gdn_scan_step", dev, *shape, _DT[x.dtype], _DT[log_alpha.dtype], _DT[h.dtype], _addr(state), _addr(x),
+          _addr(log_alpha), _addr(h))
+    return h
+
+
+def _rows(x, name):
+    dev = _cuda(x, name)
+    if x.dim() < 1:
+        raise ValueError(f"{name} must have at least one dim")
+    _need(x, name, _FLOATS, dev, x.dim())
+    return dev, x.shape[:-1].numel(), x.shape[-1]
+
+
+def layernorm_fwd(x, weight=None, bias=None, *, eps=1e-5, out_dtype=torch.float32, y=None, stats=True):
+    """Layer norm over the last dimension of x [..., D] (fp32/bf16/fp16);
+    weight, bias [D] fp32 or None (ones, zeros).  Returns (y [..., D], mean
+    [...], rstd [...]), the statistics fp32, or None both without `stats`."""
+    dev, rows, D = _rows(x, "x")
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _shaped(t, name, (D,), (torch.float32,), dev)
+    if y is None:
+        y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+    else:
+        _shaped(y, "y", tuple(x.shape), _FLOATS, dev)
+    mean = rstd = None
+    if stats:
+        mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) for _ in range(2))
+    _call("gdn_layernorm_fwd", dev, rows, D, _DT[x.dtype], _DT[y.dtype], eps, _addr(x), _addr(weight), _addr(bias),
+          _addr(y), _addr(mean), _addr(rstd))
+    return y, mean, rstd
+
+
+def layernorm_bwd_workspace_size(rows, dim) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().gdn_layernorm_bwd_workspace_size(rows, dim, ctypes.byref(n)))
+    return int(n.value)
+
+
+def layernorm_bwd(dy, x, mean, rstd, weight=None, *, dweight=True, dbias=True, workspace=None):
+    """Gradients of layernorm_fwd: dy [..., D] in y's dtype; x, weight as given
+    to it; mean, rstd [...] fp32 as it returned them.  Returns (dx in x's
+    dtype, dweight [D] fp32 or None, dbias [D] fp32 or None)."""
+    dev, rows, D = _rows(x, "x")
+    _shaped(dy, "dy", tuple(x.shape), _FLOATS, dev)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _shaped(t, name, tuple(x.shape[:-1]), (torch.float32,), dev)
+    if weight is not None:
+        _shaped(weight, "weight", (D,), (torch.float32,), dev)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dw, db = (torch.empty((D,), dtype=torch.float32, device=dev) if want else None for want in (dweight, dbias))
+    size = 0
+    if dweight or dbias:
+        workspace, size = _workspace(workspace, layernorm_bwd_workspace_size(rows, D), dev)
+    _call("gdn_layernorm_bwd", dev, rows, D, _DT[x.dtype], _DT[dy.dtype], _addr(dy), _addr(x), _addr(mean),
+          _addr(rstd), _addr(weight), _addr(dx), _addr(dw), _addr(db), _addr(workspace), size)
+    return dx, dw, db
+
+
+def state_move(state, src, dst, *, layers=False, status=None):
+    """Moves of resident states, in place: slot dst[m] of `state` gets what slot
+    src[m] held before the call, zeros where src[m] is -1.  `state` [N, ...]
+    is one layer's resident states (decode_step's, scan_step's), or with
+    `layers` [L, N, ...] several layers' that all move alike.  src, dst int32
+    [M] on the device, dst without repetition; bad indices leave the state as
+    it was, and state_move_check tells of them if `status` (int32 [2] on the
+    device) was given.  Forks, compacts, reorders and frees.  Returns state."""
+    dev = _cuda(state, "state")
+    lead = 2 if layers else 1
+    if state.dim() < lead + 1:
+        raise ValueError(f"state must have more than {lead} dims, got shape {tuple(state.shape)}")
+    if not state.is_contiguous():
+        raise ValueError("state must be contiguous")
+    _need(src, "src", (torch.int32,), dev, 1)
+    _shaped(dst, "dst", tuple(src.shape), (torch.int32,), dev)
+    if status is not None:
+        _shaped(status, "status", (2,), (torch.int32,), dev)
+    _call("gdn_state_move", dev, state.shape[0] if layers else 1, state.shape[lead - 1],
+          state.shape[lead:].numel() * state.element_size(), src.shape[0], _addr(state), _addr(src), _addr(dst),
+          _addr(status))
+    return state
+
+
+def state_move_check(status: torch.Tensor) -> int:
+    """Synchronise and return the code that state_move left in `status`: 0, or
+    1 for a source out of range, 2 for a destination out of range, 3 for a
+    destination given twice."""
+    return chunk_fwd_check(status)
 
 
 class profile:

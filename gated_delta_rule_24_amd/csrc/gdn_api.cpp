@@ -2,6 +2,7 @@
 // launch timing, error reporting.  Declarations and the full contract are in
 // include/gdn.h.  Every check runs before anything is enqueued.
 #include "gdn.h"
+#include "gdn_check.h"
 #include "gdn_launch.h"
 
 #include <hip/hip_runtime.h>
@@ -13,9 +14,9 @@
 #include <string>
 #include <vector>
 
-namespace {
+namespace gdn {
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
 
 gdn_status fail(gdn_status s, const char *fmt, ...) {
     char buf[512];
@@ -32,26 +33,24 @@ gdn_status ok() {
     return GDN_OK;
 }
 
-bool valid_dtype(int32_t d) { return d == GDN_FP32 || d == GDN_BF16 || d == GDN_FP16; }
-size_t dtype_size(int32_t d) { return d == GDN_FP32 ? 4 : 2; }
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-struct Range {
-    const char *name;
-    uintptr_t lo, hi;   // [lo, hi)
-};
-Range rng(const char *name, const void *p, size_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{name, lo, p ? lo + bytes : lo};
-}
-bool overlap(const Range &a, const Range &b) {
-    return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
-}
-
 gdn_status hip_fail(hipError_t e, const char *what) {
     return fail(GDN_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace gdn
+
+namespace {
+
+using gdn::aligned16;
+using gdn::aligned4;
+using gdn::dtype_size;
+using gdn::fail;
+using gdn::hip_fail;
+using gdn::ok;
+using gdn::overlap;
+using gdn::Range;
+using gdn::rng;
+using gdn::valid_dtype;
 
 // ---- launch timing ------------------------------------------------------------
 struct ProfRecord {
@@ -139,7 +138,7 @@ const char *gdn_status_string(gdn_status s) {
     return "GDN_ERR_UNKNOWN";
 }
 
-const char *gdn_last_error_message(void) { return g_last_error.c_str(); }
+const char *gdn_last_error_message(void) { return gdn::g_last_error.c_str(); }
 
 gdn_status gdn_chunk_fwd_workspace_size(const gdn_chunk_desc *desc, size_t *bytes) {
     if (!bytes) return fail(GDN_ERR_NULL, "bytes is NULL");

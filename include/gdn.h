@@ -23,7 +23,12 @@
  * device memory: it uses a scratch array of the library instead of a
  * workspace argument.
  *
- * Both return the same numbers as the recurrence up to floating-point
+ * Next to it, in the same conventions: the elementwise gated linear
+ * recurrence (gdn_scan_fwd, gdn_scan_bwd, gdn_scan_step), layer norm
+ * (gdn_layernorm_fwd, gdn_layernorm_bwd) and moves of resident states
+ * (gdn_state_move), described at their declarations.
+ *
+ * Both evaluations return the same numbers as the recurrence up to floating-point
  * rounding.  Chunked, single-step and save-then-resume evaluations agree
  * (tutorial: the three paths must line up; independent samples reset the
  * state, a continued request does not).
@@ -308,8 +313,9 @@ gdn_status gdn_chunk_bwd(const gdn_chunk_desc *desc,
                          hipStream_t stream);
 
 /*
- * Result of the device-side cu_seqlens check of the last gdn_chunk_fwd (or
- * packed gdn_chunk_bwd) that used `workspace`.  Synchronises `stream`, then writes 0 (valid) or a
+ * Result of the device-side check of the last gdn_chunk_fwd (or packed
+ * gdn_chunk_bwd, gdn_scan_fwd, gdn_scan_bwd) that used `workspace`, or of
+ * the gdn_state_move that wrote it as its status (codes there).  Synchronises `stream`, then writes 0 (valid) or a
  * non-zero code (1: cu[0] != 0, 2: decreasing offsets, 3: cu[N] != T) to
  * *code (host pointer).  Returns GDN_ERR_DEVICE_INPUT when the code is
  * non-zero, GDN_OK otherwise.
@@ -342,6 +348,215 @@ gdn_status gdn_decode_step(int32_t N, int32_t H, int32_t dk, int32_t dv,
                            const void *q, const void *k, const void *v,
                            const float *log_alpha, const float *beta,
                            void *o, hipStream_t stream);
+
+/*
+ * Gated linear recurrence: the elementwise sibling of the gated delta rule,
+ * with a state of one value per channel,
+ *
+ *     h_t = alpha_t h_{t-1} + x_t          alpha_t = exp(log_alpha_t)
+ *
+ * over the tokens t of a sequence, each channel on its own.
+ *   gdn_scan_fwd   -- whole sequences (prefill, training), optionally packed
+ *                     with cu_seqlens, from an initial state, returning the
+ *                     final state
+ *   gdn_scan_bwd   -- gradients of gdn_scan_fwd's outputs
+ *   gdn_scan_step  -- one token for a batch of resident states, in place
+ *
+ * Shape of a gdn_scan_fwd / gdn_scan_bwd call:
+ *   batch       B >= 1: batch rows.  Must be 1 when cu_seqlens is given.
+ *   seqlen      T >= 0: tokens per row (packed: total tokens); B * T < 2^30.
+ *   channels    D: 1..65536 (a layer with heads passes heads * head dim).
+ *   num_seqs    N: B without cu_seqlens; with it, cu_seqlens has N + 1
+ *               offsets.
+ *   in_dtype    dtype of x and of its gradient
+ *   gate_dtype  dtype of log_alpha and of its gradient
+ *   out_dtype   dtype of h and of its gradient
+ *               Each is FP32 or one 16-bit type; BF16 and FP16 do not mix in
+ *               one call (GDN_ERR_UNSUPPORTED).  States are fp32, and every
+ *               state, decay and carry is held in fp32 whatever the types;
+ *               an output is rounded once, to nearest, when it is stored.
+ *   flags       0.
+ */
+typedef struct {
+    int32_t batch;
+    int32_t seqlen;
+    int32_t channels;
+    int32_t num_seqs;
+    int32_t in_dtype;    /* gdn_dtype */
+    int32_t gate_dtype;  /* gdn_dtype */
+    int32_t out_dtype;   /* gdn_dtype */
+    int32_t flags;
+} gdn_scan_desc;
+
+/*
+ * Workspace for gdn_scan_fwd and gdn_scan_bwd, in bytes, written to *bytes
+ * (host pointer).  Depends only on the descriptor.  Need not be initialised;
+ * may be reused by later calls ordered after this one on the stream.
+ * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_UNSUPPORTED.
+ */
+gdn_status gdn_scan_workspace_size(const gdn_scan_desc *desc, size_t *bytes);
+
+/*
+ * Forward pass.
+ *
+ *   x            [B, T, D]  in_dtype
+ *   log_alpha    [B, T, D]  gate_dtype, <= 0 (not checked; a positive value
+ *                           is computed as given, -inf forgets everything)
+ *   init_state   [N, D]     fp32 or NULL (zeros)
+ *   cu_seqlens   int32 [N+1] or NULL, as for gdn_chunk_fwd: empty sequences
+ *                are allowed, a malformed array makes the kernels write
+ *                nothing and gdn_chunk_fwd_check(workspace, ...) reports it
+ *   h            [B, T, D]  out_dtype (written)
+ *   final_state  [N, D]     fp32 or NULL (not returned).  May be the same
+ *                           pointer as init_state (in-place continuation),
+ *                           not a partial overlap.
+ * Nothing of one sequence reaches another, not-a-number and infinite values
+ * included.  Equal calls give equal bits.
+ * x, log_alpha, h, the states and the workspace must be 16-byte aligned.
+ * h, final_state and the workspace must not overlap anything else
+ * (GDN_ERR_ALIAS).
+ * Errors: as gdn_chunk_fwd.
+ */
+gdn_status gdn_scan_fwd(const gdn_scan_desc *desc, const void *x, const void *log_alpha,
+                        const float *init_state, const int32_t *cu_seqlens,
+                        void *h, float *final_state,
+                        void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Backward pass: gradients of a loss with respect to x, log_alpha and the
+ * initial state, given those with respect to h and the final state.  With
+ * g_t the whole gradient of h_t and e_t = alpha_t g_t,
+ *     g_t = d_h_t + e_{t+1}     (d_h_L + d_final_state at a sequence's end)
+ *     dx_t = g_t     dlog_alpha_t = e_t h_{t-1}     d_init_state = e_1
+ *
+ *   log_alpha, init_state, cu_seqlens   as for gdn_scan_fwd
+ *   h              [B, T, D]  out_dtype, gdn_scan_fwd's output.  With a
+ *                             16-bit out_dtype its rounding (half a step of
+ *                             the type) carries over to dlog_alpha.
+ *   d_h            [B, T, D]  out_dtype
+ *   d_final_state  [N, D]     fp32 or NULL (zeros)
+ *   dx             [B, T, D]  in_dtype (written)
+ *   dlog_alpha     [B, T, D]  gate_dtype (written)
+ *   d_init_state   [N, D]     fp32 or NULL (not returned); with init_state
+ *                             NULL it is the gradient at a zero state.  Of an
+ *                             empty sequence it is d_final_state.
+ * The outputs must not overlap each other, any input or the workspace.
+ * Errors: as gdn_chunk_bwd.
+ */
+gdn_status gdn_scan_bwd(const gdn_scan_desc *desc, const void *log_alpha, const void *h,
+                        const float *init_state, const int32_t *cu_seqlens,
+                        const void *d_h, const float *d_final_state,
+                        void *dx, void *dlog_alpha, float *d_init_state,
+                        void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One token for N resident states, in place.
+ *
+ *   state      [N, D]  fp32, read and overwritten with h_t
+ *   x          [N, D]  in_dtype
+ *   log_alpha  [N, D]  gate_dtype
+ *   h          [N, D]  out_dtype (written), the new state rounded once
+ * D: 1..65536; types as for gdn_scan_fwd.  N * D < 2^40.  h and state must
+ * not overlap each other or an input.  N = 0 does nothing.
+ * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_ALIGN,
+ * GDN_ERR_UNSUPPORTED, GDN_ERR_ALIAS, GDN_ERR_HIP.
+ */
+gdn_status gdn_scan_step(int32_t N, int32_t D, int32_t in_dtype, int32_t gate_dtype, int32_t out_dtype,
+                         float *state, const void *x, const void *log_alpha, void *h, hipStream_t stream);
+
+/*
+ * Layer norm over the last dimension,
+ *     mean = sum_i x_i / D     rstd = 1 / sqrt(sum_i (x_i - mean)^2 / D + eps)
+ *     y_i = (x_i - mean) rstd weight_i + bias_i
+ * as it stands behind the recurrence (per head, D = dv) or in front of the
+ * block (D = model width).
+ *
+ *   rows       R >= 0, R < 2^31
+ *   dim        D: 1..16384
+ *   eps        finite and >= 0 (GDN_ERR_UNSUPPORTED otherwise)
+ *   x          [R, D]  in_dtype
+ *   weight     [D]     fp32 or NULL (ones)
+ *   bias       [D]     fp32 or NULL (zeros)
+ *   y          [R, D]  out_dtype (written)
+ *   mean, rstd [R]     fp32 (written) or both NULL (not returned)
+ * in_dtype and out_dtype: each FP32 or one 16-bit type, not BF16 with FP16.
+ * Statistics are fp32 sums of (x - mean) taken after the mean; y is rounded
+ * once.  A row's results depend on that row alone.
+ * x, y, weight and bias must be 16-byte aligned, mean and rstd 4-byte.  The
+ * outputs must not overlap each other or an input.
+ * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_ALIGN,
+ * GDN_ERR_UNSUPPORTED, GDN_ERR_ALIAS, GDN_ERR_HIP.
+ */
+gdn_status gdn_layernorm_fwd(int64_t rows, int32_t dim, int32_t in_dtype, int32_t out_dtype, float eps,
+                             const void *x, const float *weight, const float *bias,
+                             void *y, float *mean, float *rstd, hipStream_t stream);
+
+/*
+ * Workspace of gdn_layernorm_bwd in bytes, written to *bytes (host pointer).
+ * Need not be initialised.  Errors: GDN_ERR_NULL, GDN_ERR_SHAPE,
+ * GDN_ERR_UNSUPPORTED.
+ */
+gdn_status gdn_layernorm_bwd_workspace_size(int64_t rows, int32_t dim, size_t *bytes);
+
+/*
+ * Gradients of gdn_layernorm_fwd.  With xh = (x - mean) rstd and
+ * u = dy weight,
+ *     dx = rstd (u - sum(u) / D - xh sum(u xh) / D)
+ *     dweight = sum over rows of dy xh     dbias = sum over rows of dy
+ *
+ *   dy          [R, D]  out_dtype
+ *   x           [R, D]  in_dtype
+ *   mean, rstd  [R]     fp32, as gdn_layernorm_fwd gave them
+ *   weight      [D]     fp32 or NULL (ones)
+ *   dx          [R, D]  in_dtype (written)
+ *   dweight     [D]     fp32 or NULL (not returned), written, not added to
+ *   dbias       [D]     fp32 or NULL (not returned), written, not added to
+ *   workspace   at least gdn_layernorm_bwd_workspace_size bytes, 16-byte
+ *               aligned; may be NULL when neither dweight nor dbias is asked
+ *               for
+ * The sums over rows are taken in a fixed order: equal calls give equal
+ * bits.  With R = 0 dweight and dbias are zeros.
+ * The outputs must not overlap each other, any input or the workspace.
+ * Errors: those of gdn_layernorm_fwd and GDN_ERR_WORKSPACE.
+ */
+gdn_status gdn_layernorm_bwd(int64_t rows, int32_t dim, int32_t in_dtype, int32_t out_dtype,
+                             const void *dy, const void *x, const float *mean, const float *rstd,
+                             const float *weight, void *dx, float *dweight, float *dbias,
+                             void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Moves of resident states.  A page is the state of one sequence in one
+ * layer: one slot of gdn_decode_step's or gdn_scan_step's state, page_bytes
+ * long (fp32 [H, dv, dk]: 4 H dv dk).  For every layer l and every
+ * m < moves,
+ *     new[l, dst[m]] = old[l, src[m]]        zeros where src[m] = -1
+ * with every source read as it was before the call, so that one call
+ *   - forks a state (one source, many destinations),
+ *   - compacts a batch after sequences have ended (live states into holes),
+ *   - reorders or swaps states (cycles are fine),
+ *   - frees slots for new sequences (src = -1).
+ * Slots that are no destination keep their bytes.
+ *
+ *   layers      L >= 0
+ *   slots       P: 1..65536
+ *   page_bytes  a multiple of 4, >= 4
+ *   moves       M: 0..min(P, 4096)
+ *   state       [L, P, page_bytes], 16-byte aligned, updated in place
+ *   src         int32 [M], each -1 or a slot
+ *   dst         int32 [M], slots, no two alike
+ *   status      int32 [2] or NULL (written): {M, code}.  src and dst are
+ *               device data and are checked on the device: code 1 for a
+ *               source out of range, 2 for a destination out of range, 3 for
+ *               a destination given twice, 0 otherwise; where it is not 0
+ *               the call changes nothing else.  gdn_chunk_fwd_check(status,
+ *               ...) reads it.  src, dst, status: 4-byte aligned.
+ * src, dst and status must not overlap the state or status an index array.
+ * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_ALIGN, GDN_ERR_UNSUPPORTED,
+ * GDN_ERR_ALIAS, GDN_ERR_HIP.
+ */
+gdn_status gdn_state_move(int32_t layers, int32_t slots, int64_t page_bytes, int32_t moves,
+                          void *state, const int32_t *src, const int32_t *dst, int32_t *status,
+                          hipStream_t stream);
 
 /*
  * Per-kernel timing for measurement harnesses (host-side bookkeeping only;

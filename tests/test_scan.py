@@ -1,0 +1,336 @@
+"""Gated linear recurrence on the GPU against the fp64 oracle.
+
+Bounds.  In h_t = sum_j (prod_{j<i<=t} alpha_i) x_j each term meets at most
+t - j + 1 decays.  A decay costs its exp (argument rounding |l| u, the
+function 4 u) and a product u, or the same again where a kernel multiplies
+decays before it applies them; each joined partial sum costs u.  So with
+S_t = alpha_t S_{t-1} + |x_t| the error obeys
+E_t = alpha_t E_{t-1} + (8 + 4 |l_t|) u S_t + 40 u S_t at the end (joins), and
+the same holds for the reversed recurrence of the gradients.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_24_amd as gdn
+from oracle import operators as R
+
+from .op_util import DT, HALF, U, cu_tensor, dev, host, within
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [("fp32", "fp32", "fp32"), ("bf16", "fp32", "bf16"), ("bf16", "bf16", "bf16"), ("fp16", "fp16", "fp16"),
+         ("fp32", "bf16", "fp32"), ("bf16", "fp32", "fp32"), ("fp16", "fp32", "fp32"), ("fp32", "fp16", "fp16")]
+SHAPES = [  # B, T, D, cu
+    (1, 1, 1, None), (2, 3, 5, None), (3, 127, 33, None), (2, 128, 64, None), (1, 129, 65, None),
+    (2, 300, 130, None), (1, 1000, 24, None), (1, 2500, 8, None), (4, 515, 72, None), (130, 2, 16, None),
+    (1, 9, 20, [0, 3, 3, 4, 9]), (1, 700, 40, [0, 0, 1, 128, 256, 257, 640, 640, 700, 700]),
+    (1, 1200, 96, [0, 1000, 1200]), (1, 300, 6, list(range(0, 301))), (1, 1030, 64, [0, 513, 513, 514, 1030]),
+]
+
+
+def inputs(B, T, D, cu, types, seed=0, init=True):
+    """Inputs as the library gets them (fp64 copies of the rounded values beside them)."""
+    g = np.random.default_rng(seed)
+    N = B if cu is None else len(cu) - 1
+    t = dict(x=dev(g.standard_normal((B, T, D)), types[0]),
+             la=dev(-g.uniform(0.001, 0.1, (B, T, D)) * g.choice([1.0, 1.0, 30.0], (B, T, D)), types[1]),
+             init=dev(g.standard_normal((N, D))) if init else None,
+             dfin=dev(g.standard_normal((N, D))), dh=dev(g.standard_normal((B, T, D)), types[2]))
+    return t, {k: None if v is None else host(v) for k, v in t.items()}
+
+
+def bound_scan(mag, la, first, B, T, D, cu, reverse=False):
+    """E_t and the error of each sequence's last state (see above); mag: |x| or |dh|."""
+    mag, l = np.abs(mag).reshape(-1, D), np.asarray(la).reshape(-1, D)
+    a, E = np.exp(l), np.zeros_like(mag)
+    spans = R._spans(B, T, cu)
+    last = np.zeros((len(spans), D))
+    for n, (t0, t1) in enumerate(spans):
+        S = np.zeros(D) if first is None else np.abs(first[n])
+        e = np.zeros(D)
+        for t in (range(t1 - 1, t0 - 1, -1) if reverse else range(t0, t1)):
+            if reverse:       # g_t = dh_t + e_{t+1}; then e = a g
+                S = mag[t] + S
+                E[t] = e + 40 * U * S
+                S, e = a[t] * S, a[t] * (e + (8 + 4 * np.abs(l[t])) * U * S)
+            else:
+                S = a[t] * S + mag[t]
+                e = a[t] * e + (8 + 4 * np.abs(l[t])) * U * S
+                E[t] = e + 40 * U * S
+        last[n] = e + 40 * U * S
+    return E.reshape(B, T, D), last
+
+
+def check_fwd(B, T, D, cu, types, seed=0, init=True):
+    t, r = inputs(B, T, D, cu, types, seed, init)
+    h, fin = gdn.scan_fwd(t["x"], t["la"], t["init"], cu_tensor(cu), out_dtype=DT[types[2]])
+    want, wfin = R.scan(r["x"], r["la"], r["init"], cu)
+    E, last = bound_scan(r["x"], r["la"], r["init"], B, T, D, cu)
+    within(h, want, E, types[2], f"h {B, T, D} {types}")
+    within(fin, wfin, last, "fp32", "final state")
+    return t, r
+
+
+def check_bwd(B, T, D, cu, types, seed=0, init=True):
+    t, r = inputs(B, T, D, cu, types, seed, init)
+    h = dev(R.scan(r["x"], r["la"], r["init"], cu)[0], types[2])
+    hr = host(h)
+    dx, dl, di = gdn.scan_bwd(t["la"], h, t["dh"], t["init"], t["dfin"], cu_tensor(cu), dx_dtype=DT[types[0]])
+    wx, wl, wi = R.scan_bwd(r["la"], hr, r["dh"], r["init"], r["dfin"], cu)
+    E, last = bound_scan(r["dh"], r["la"], r["dfin"], B, T, D, cu, reverse=True)
+    within(dx, wx, E, types[0], f"dx {B, T, D} {types}")
+    # e_t = alpha_t g_t costs 8 + 4 |l| more steps of itself, its product with h_{t-1} one
+    a, past = np.exp(r["la"]), np.zeros((B * T, D))
+    for n, (t0, t1) in enumerate(R._spans(B, T, cu)):
+        past[t0 + 1:t1] = hr.reshape(-1, D)[t0:t1 - 1] if t1 > t0 else 0
+        if t1 > t0 and r["init"] is not None:
+            past[t0] = r["init"][n]
+    past = np.abs(past).reshape(B, T, D)
+    within(dl, wl, past * a * (E + (10 + 4 * np.abs(r["la"])) * U * np.abs(wx)), types[1], "dlog_alpha")
+    within(di, wi, last, "fp32", "d_init")
+
+
+@pytest.mark.parametrize("types", TYPES)
+def test_fwd_types(types):
+    check_fwd(2, 300, 72, None, types)
+    check_fwd(1, 200, 37, [0, 1, 1, 150, 200], types, seed=1)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_fwd_shapes(shape):
+    check_fwd(*shape, ("bf16", "fp32", "bf16"), init=False)
+    check_fwd(*shape, ("fp32", "fp32", "fp32"), seed=2)
+
+
+@pytest.mark.parametrize("types", TYPES)
+def test_bwd_types(types):
+    check_bwd(2, 300, 72, None, types)
+    check_bwd(1, 200, 37, [0, 1, 1, 150, 200], types, seed=1)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_bwd_shapes(shape):
+    check_bwd(*shape, ("bf16", "fp32", "bf16"), init=False)
+    check_bwd(*shape, ("fp32", "fp32", "fp32"), seed=2)
+
+
+def test_bwd_equals_differences():
+    """The gradients against central differences of the loss taken with scan_fwd itself.  In fp32 a difference
+    of losses of size L over a step of 2^-4 is off by about 2^-24 L 2^4 and the linear loss has no higher term in x
+    and init; log_alpha's third derivative adds step^2 / 6 of the terms' size."""
+    t, r = inputs(1, 40, 8, [0, 10, 10, 40], ("fp32",) * 3, seed=4)
+    cu = cu_tensor([0, 10, 10, 40])
+    h, _ = gdn.scan_fwd(t["x"], t["la"], t["init"], cu)
+    grads = gdn.scan_bwd(t["la"], h, t["dh"], t["init"], t["dfin"], cu)
+
+    def loss(v):
+        h, fin = gdn.scan_fwd(v["x"], v["la"], v["init"], cu)
+        return float((h.double() * t["dh"].double()).sum() + (fin.double() * t["dfin"].double()).sum())
+
+    size = float((h.double().abs() * t["dh"].double().abs()).sum()) + float(t["dfin"].double().abs().sum()) * 8
+    for name, got in zip(("x", "la", "init"), grads):
+        g = torch.Generator().manual_seed(1)
+        way = torch.randn(t[name].shape, generator=g).cuda()
+        step = 2.0 ** -4 if name != "la" else 2.0 ** -8
+        hi, lo = dict(t), dict(t)
+        hi[name], lo[name] = t[name] + step * way, t[name] - step * way
+        want = (loss(hi) - loss(lo)) / (2 * step)
+        have = float((got.double() * way.double()).sum())
+        room = size * (40 * U / step + (step * float(way.abs().max())) ** 2 * 40 * 40 / 6 * (name == "la"))
+        print(f"[differences] {name}: {have:.6g} against {want:.6g}, room {room:.3g}")
+        assert abs(have - want) <= room
+
+
+def test_zero_tokens_and_no_final():
+    init = torch.randn(3, 10, device="cuda")
+    x = torch.empty(3, 0, 10, device="cuda")
+    h, fin = gdn.scan_fwd(x, x, init)
+    assert h.shape == x.shape and torch.equal(fin, init)
+    assert torch.equal(gdn.scan_fwd(x, x)[1], torch.zeros_like(init))
+    dx, dl, di = gdn.scan_bwd(x, x, x, init, init)
+    assert torch.equal(di, init) and dx.shape == x.shape
+    x = torch.randn(2, 20, 10, device="cuda")
+    h, fin = gdn.scan_fwd(x, -x.abs(), final_state=False)
+    assert fin is None
+    assert torch.equal(h, gdn.scan_fwd(x, -x.abs())[0])
+    full, none = gdn.scan_bwd(-x.abs(), h, x), gdn.scan_bwd(-x.abs(), h, x, d_init=False)
+    assert none[2] is None and torch.equal(full[0], none[0]) and torch.equal(full[1], none[1])
+
+
+@pytest.mark.parametrize("D", [64, 37])
+def test_continuation_in_place(D):
+    """Two calls with the state carried in one buffer are one call (bounds of both sides)."""
+    t, r = inputs(2, 700, D, None, ("fp32",) * 3, seed=5)
+    state = t["init"].clone()
+    parts = [gdn.scan_fwd(t["x"][:, s].contiguous(), t["la"][:, s].contiguous(), state, final_state=state)[0]
+             for s in (slice(0, 331), slice(331, 700))]
+    want, wfin = R.scan(r["x"], r["la"], r["init"])
+    E, last = bound_scan(r["x"], r["la"], r["init"], 2, 700, D, None)
+    within(torch.cat(parts, 1), want, 2 * E, "fp32", "parts")
+    within(state, wfin, 2 * last, "fp32", "state")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_bad_values_stay_in_their_sequence(bad):
+    cu = [0, 5, 130, 131, 400, 400, 700]
+    t, _ = inputs(1, 700, 40, cu, ("fp32",) * 3, seed=6)
+    ref = gdn.scan_fwd(t["x"], t["la"], t["init"], cu_tensor(cu))
+    gref = gdn.scan_bwd(t["la"], ref[0], t["dh"], t["init"], t["dfin"], cu_tensor(cu))
+    for n in (0, 1, 3):
+        v = {k: s.clone() for k, s in t.items()}
+        v["x"][0, cu[n + 1] - 1] = bad
+        v["dh"][0, cu[n]] = bad
+        h, fin = gdn.scan_fwd(v["x"], v["la"], v["init"], cu_tensor(cu))
+        dx, dl, di = gdn.scan_bwd(v["la"], ref[0], v["dh"], v["init"], v["dfin"], cu_tensor(cu))
+        keep = torch.ones(700, dtype=torch.bool, device="cuda")
+        keep[cu[n]:cu[n + 1]] = False
+        others = [i for i in range(6) if i != n]
+        assert torch.equal(h[0, keep], ref[0][0, keep]) and torch.equal(fin[others], ref[1][others])
+        assert torch.equal(dx[0, keep], gref[0][0, keep]) and torch.equal(dl[0, keep], gref[1][0, keep])
+        assert torch.equal(di[others], gref[2][others])
+        assert not torch.isfinite(h[0, cu[n + 1] - 1]).any() and not torch.isfinite(dx[0, cu[n]]).any()
+
+
+def test_total_forgetting():
+    """log_alpha = -inf: h = x, and nothing comes back through it."""
+    x = torch.randn(1, 300, 64, device="cuda")
+    la = torch.full_like(x, -float("inf"))
+    init = torch.randn(1, 64, device="cuda")
+    h, fin = gdn.scan_fwd(x, la, init)
+    assert torch.equal(h, x) and torch.equal(fin, x[:, -1])
+    dx, dl, di = gdn.scan_bwd(la, h, x, init)
+    assert torch.equal(dx, x) and not dl.any() and not di.any()
+
+
+def test_no_decay_counts():
+    """log_alpha = 0: running sums of whole numbers are exact."""
+    x = torch.ones(1, 5000, 16, device="cuda")
+    h, fin = gdn.scan_fwd(x, torch.zeros_like(x))
+    assert torch.equal(h[0, :, 3], torch.arange(1.0, 5001, device="cuda")) and (fin == 5000).all()
+    dx, dl, di = gdn.scan_bwd(torch.zeros_like(x), h, x)
+    assert torch.equal(dx[0, :, 0], torch.arange(5000.0, 0, -1, device="cuda")) and (di == 5000).all()
+
+
+@pytest.mark.parametrize("cu,code", [([1, 5, 10], 1), ([0, 6, 5], 2), ([0, 5, 9], 3)])
+def test_malformed_offsets_write_nothing(cu, code):
+    x = torch.randn(1, 10, 8, device="cuda")
+    ws = torch.empty(gdn.scan_workspace_size(1, 10, 8, 2), dtype=torch.uint8, device="cuda")
+    h, fin = torch.full_like(x, 7.0), torch.full((2, 8), 7.0, device="cuda")
+    gdn.scan_fwd(x, -x.abs(), None, cu_tensor(cu), h=h, final_state=fin, workspace=ws)
+    assert gdn.chunk_fwd_check(ws) == code
+    assert (h == 7).all() and (fin == 7).all()
+    gdn.scan_fwd(x, -x.abs(), None, cu_tensor([0, 5, 10]), h=h, final_state=fin, workspace=ws)
+    assert gdn.chunk_fwd_check(ws) == 0 and (h != 7).all()
+    gdn.scan_bwd(-x.abs(), h, x, None, None, cu_tensor(cu), workspace=ws)
+    assert gdn.chunk_fwd_check(ws) == code
+
+
+def test_equal_calls_equal_bits_and_streams():
+    """Runs side by side on two streams, with workspaces of their own, give the bits of a run alone."""
+    t, _ = inputs(1, 4000, 512, [0, 700, 4000], ("bf16", "bf16", "bf16"), seed=7)
+    cu = cu_tensor([0, 700, 4000])
+    ref = gdn.scan_fwd(t["x"], t["la"], t["init"], cu, out_dtype=torch.bfloat16)
+    gref = gdn.scan_bwd(t["la"], ref[0], t["dh"], t["init"], t["dfin"], cu, dx_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for k in range(6):
+        with torch.cuda.stream(streams[k % 2]):
+            got.append((gdn.scan_fwd(t["x"], t["la"], t["init"], cu, out_dtype=torch.bfloat16),
+                        gdn.scan_bwd(t["la"], ref[0], t["dh"], t["init"], t["dfin"], cu, dx_dtype=torch.bfloat16)))
+    torch.cuda.synchronize()
+    for f, b in got:
+        assert all(torch.equal(p, q) for p, q in zip(f, ref)) and all(torch.equal(p, q) for p, q in zip(b, gref))
+
+
+def test_graph_replays():
+    """Captured calls, replayed on new inputs between eager work, equal the eager calls."""
+    t, _ = inputs(2, 900, 256, None, ("bf16", "fp32", "bf16"), seed=8)
+    h, fin = torch.empty(2, 900, 256, dtype=torch.bfloat16, device="cuda"), torch.empty(2, 256, device="cuda")
+    gdn.scan_fwd(t["x"], t["la"], t["init"], h=h, final_state=fin)
+    gdn.scan_bwd(t["la"], h, t["dh"], t["init"], t["dfin"])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.scan_fwd(t["x"], t["la"], t["init"], h=h, final_state=fin)
+        grads = gdn.scan_bwd(t["la"], h, t["dh"], t["init"], t["dfin"])
+    for k in range(4):
+        t["x"].normal_()
+        t["dh"].normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = gdn.scan_fwd(t["x"], t["la"], t["init"], out_dtype=torch.bfloat16)
+        assert torch.equal(eager[0], h) and torch.equal(eager[1], fin)
+        for p, q in zip(gdn.scan_bwd(t["la"], h, t["dh"], t["init"], t["dfin"]), grads):
+            assert torch.equal(p, q)
+
+
+def test_offsets_past_32_bits():
+    """Over 2^31 values a tensor: the last channels and tokens equal a small call's on the same channels."""
+    T, D = 33000, 65536
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.empty(1, T, D, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    la = torch.empty(1, T, D, dtype=torch.bfloat16, device="cuda").uniform_(-0.1, -0.001, generator=g)
+    h, fin = gdn.scan_fwd(x, la, out_dtype=torch.bfloat16)
+    at = slice(D - 64, D)
+    hs, fs = gdn.scan_fwd(x[..., at].contiguous(), la[..., at].contiguous(), out_dtype=torch.bfloat16)
+    assert torch.equal(h[..., at], hs) and torch.equal(fin[..., at], fs)
+    dx, dl, di = gdn.scan_bwd(la, h, x, dx_dtype=torch.bfloat16)
+    sx, sl, si = gdn.scan_bwd(la[..., at].contiguous(), hs, x[..., at].contiguous(), dx_dtype=torch.bfloat16)
+    assert torch.equal(dx[..., at], sx) and torch.equal(dl[..., at], sl) and torch.equal(di[..., at], si)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("N,D", [(1, 1), (3, 33), (5, 64), (256, 129), (17, 2048)])
+def test_step(N, D, types):
+    """One rounding each for exp's argument, exp (4), the product and the sum; in place, then the chain of steps
+    is the sequence."""
+    g = np.random.default_rng(N + D)
+    state, x = dev(g.standard_normal((N, D))), dev(g.standard_normal((N, D)), types[0])
+    la = dev(-g.uniform(0.001, 3.0, (N, D)), types[1])
+    s, xr, l = host(state), host(x), host(la)
+    keep = (x.clone(), la.clone())
+    h = gdn.scan_step(state, x, la, out_dtype=DT[types[2]])
+    want = np.exp(l) * s + xr
+    room = U * ((6 + np.abs(l)) * np.abs(np.exp(l) * s) + np.abs(want))
+    within(state, want, room, "fp32", f"step {N, D}")
+    assert torch.equal(h, state.to(h.dtype))
+    assert torch.equal(x, keep[0]) and torch.equal(la, keep[1])
+
+
+def test_steps_are_the_sequence():
+    t, r = inputs(3, 50, 40, None, ("bf16", "fp32", "fp32"), seed=11)
+    state = t["init"].clone()
+    hs = [gdn.scan_step(state, t["x"][:, k].contiguous(), t["la"][:, k].contiguous()) for k in range(50)]
+    want, wfin = R.scan(r["x"], r["la"], r["init"])
+    E, last = bound_scan(r["x"], r["la"], r["init"], 3, 50, 40, None)
+    within(torch.stack(hs, 1), want, E, "fp32", "steps")
+    within(state, wfin, last, "fp32", "state")
+    h, _ = gdn.scan_fwd(t["x"], t["la"], t["init"])
+    within(h, want, E, "fp32", "sequence")
+
+
+def test_refusals():
+    x = torch.randn(2, 10, 8, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        gdn.scan_fwd(x.transpose(1, 2), x)
+    with pytest.raises(ValueError, match="must be"):
+        gdn.scan_fwd(x, x[:, :5].contiguous())
+    with pytest.raises(ValueError, match="dtype"):
+        gdn.scan_fwd(x.double(), x)
+    with pytest.raises(ValueError, match="dtype"):
+        gdn.scan_bwd(x, x, x.bfloat16())
+    with pytest.raises(gdn.GdnError, match="mix"):
+        gdn.scan_fwd(x.bfloat16(), x.half())
+    with pytest.raises(gdn.GdnError, match="aligned"):
+        gdn.scan_fwd(x, x, h=torch.empty(2 * 10 * 8 + 1, device="cuda")[1:].view(2, 10, 8))
+    with pytest.raises(gdn.GdnError, match="batch == 1"):
+        gdn.scan_fwd(x, x, cu_seqlens=cu_tensor([0, 10, 20]))
+    with pytest.raises(gdn.GdnError, match="overlaps"):
+        gdn.scan_fwd(x, x, h=x)
+    with pytest.raises(gdn.GdnError, match="workspace"):
+        gdn.scan_fwd(x, x, workspace=torch.empty(1, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(gdn.GdnError):
+        gdn.scan_fwd(x[:1], x[:1], cu_seqlens=cu_tensor([]))
+    assert HALF["bf16"] == torch.finfo(torch.bfloat16).eps / 2
