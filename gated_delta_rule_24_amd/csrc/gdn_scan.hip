@@ -44,10 +44,17 @@
 
 namespace gdn {
 
-constexpr int kTc = 128;        // tokens of a tile
+#ifndef KNT
+#define KNT 256
+#define KTC 128
+#define KGRP 8
+#define KWAVES 4
+#endif
+constexpr int kTc = KTC;        // tokens of a tile
 constexpr int kCw = 64;         // channels of a tile
-constexpr int kElems = kTc * kCw / 256;   // elements per thread
-constexpr int kGroup = 8;       // tiles per group of a chain
+constexpr int kNt = KNT;        // threads of a block
+constexpr int kElems = kTc * kCw / kNt;   // elements per thread
+constexpr int kGroup = KGRP;       // tiles per group of a chain
 constexpr uint64_t kEmpty = ~0ull;
 constexpr int64_t kMaxBlocks = 1 << 22;
 constexpr int kPatience = 1 << 20;
@@ -63,8 +70,8 @@ ScanWorkspace scan_workspace_layout(int32_t B, int32_t T, int32_t D, int32_t N, 
     const bool chained = w.chunks > 1;
     const int64_t words = chained ? w.rows * w.tiles * kCw : 0;
     size_t at = 256;                                   // meta
-    w.off_tab = at;
-    at += packed ? up((size_t)(w.chunks + 1) * 4) : 0;
+    w.off_seq = at;
+    at += packed ? up((size_t)T * 4) : 0;
     w.off_ctr = at;
     at += chained ? up((size_t)w.rows * w.tiles * 4) : 0;
     w.off_agg = at;
@@ -76,43 +83,40 @@ ScanWorkspace scan_workspace_layout(int32_t B, int32_t T, int32_t D, int32_t N, 
 }
 
 // Empties the words, zeroes the counters; packed: checks cu_seqlens (codes as
-// in chunk_table_kernel) and finds, for each tile of tokens, the first offset
-// that is not before it.
-__global__ __launch_bounds__(256) void scan_setup_kernel(int N, int T, int nchunk, const int32_t *__restrict__ cu,
-                                                         int32_t *__restrict__ meta, int32_t *__restrict__ tab,
+// in chunk_table_kernel) and writes down each token's sequence.
+__global__ __launch_bounds__(256) void scan_setup_kernel(int N, int T, const int32_t *__restrict__ cu,
+                                                         int32_t *__restrict__ meta, int32_t *__restrict__ seq,
                                                          int32_t *__restrict__ ctr, int64_t nctr,
                                                          u32x4_t *__restrict__ words, int64_t nwords16) {
     const int64_t tid = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
     for (int64_t i = tid; i < nwords16; i += all) words[i] = u32x4_t{~0u, ~0u, ~0u, ~0u};
     for (int64_t i = tid; i < nctr; i += all) ctr[i] = 0;
-    if (cu) {
-        for (int64_t c = tid; c < nchunk; c += all) {
-            const int64_t t0 = c * kTc;
-            int lo = 0, hi = N;            // the first n with cu[n] >= t0 (N if there is none)
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (cu[mid] < t0) lo = mid + 1;
-                else hi = mid;
-            }
-            tab[c] = lo;
+    if (!cu) return;
+    for (int64_t t = tid; t < T; t += all) {
+        int lo = 1, hi = N;            // the first n >= 1 with cu[n] > t (N if there is none)
+        while (lo < hi) {
+            const int mid = lo + ((hi - lo) >> 1);
+            if (cu[mid] <= t) lo = mid + 1;
+            else hi = mid;
         }
-        if (blockIdx.x == 0) {
-            __shared__ int s_code;
-            if (threadIdx.x == 0) s_code = 0;
-            __syncthreads();
-            int code = 0;
-            for (int n = threadIdx.x; n <= N; n += 256) {
-                const int v = cu[n];
-                if (n == 0 && v != 0) code |= 1;
-                if (n > 0 && cu[n - 1] > v) code |= 2;
-                if (n == N && v != T) code |= 4;
-            }
-            if (code) atomicOr(&s_code, code);
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                meta[0] = nchunk;
-                meta[1] = (s_code & 1) ? 1 : ((s_code & 2) ? 2 : (s_code ? 3 : 0));
-            }
+        seq[t] = lo - 1;
+    }
+    if (blockIdx.x == 0) {
+        __shared__ int s_code;
+        if (threadIdx.x == 0) s_code = 0;
+        __syncthreads();
+        int code = 0;
+        for (int64_t n = threadIdx.x; n <= N; n += 256) {
+            const int v = cu[n];
+            if (n == 0 && v != 0) code |= 1;
+            if (n > 0 && cu[n - 1] > v) code |= 2;
+            if (n == N && v != T) code |= 4;
+        }
+        if (code) atomicOr(&s_code, code);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            meta[0] = T;
+            meta[1] = (s_code & 1) ? 1 : ((s_code & 2) ? 2 : (s_code ? 3 : 0));
         }
     }
 }
@@ -125,6 +129,12 @@ template <bool PACKED>
 __device__ __forceinline__ float apply(float A, float H, float s) {
     const float v = fmaf(A, s, H);
     return PACKED && forgets(A) ? H : v;
+}
+// (A, H) followed by (nA, nH).
+template <bool PACKED>
+__device__ __forceinline__ void join(float &A, float &H, float nA, float nH) {
+    H = apply<PACKED>(nA, nH, H);
+    A = PACKED && (forgets(nA) || forgets(A)) ? -0.f : A * nA;
 }
 // The word of a published pair.  H is not-a-number in one form only, so no
 // word equals kEmpty.
@@ -141,18 +151,68 @@ __device__ __forceinline__ uint64_t get(const uint64_t *p) {
 // exp(x): exp2's instruction on x log2(e).
 __device__ __forceinline__ float exp_gate(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
-// V consecutive elements as loaded.
+// V consecutive elements as loaded (16-bit types two to a register).  Values
+// are converted each time they are used: the registers that this saves let
+// one block more share a CU.
 template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T *p, T (&o)[V]) {
-    struct alignas(sizeof(T) * V) A {
-        T e[V];
-    };
-    const A a = *reinterpret_cast<const A *>(p);
+struct Held {
+    static constexpr int W = (V * (int)sizeof(T) + 3) / 4;
+    uint32_t w[W];
+    // element `off` of a uniform base (32-bit byte offsets: one scalar base for all of a thread's loads)
+    __device__ __forceinline__ void load(const T *base, uint32_t off) {
+        const char *p = reinterpret_cast<const char *>(base) + (uint32_t)(off * (uint32_t)sizeof(T));
+        struct alignas(sizeof(T) * V) A {
+            T e[V];
+        };
+        const A a = *reinterpret_cast<const A *>(p);
+        if constexpr (sizeof(A) < 4) {
+            w[0] = __builtin_bit_cast(uint16_t, a);
+        } else {
+            struct R {
+                uint32_t w[W];
+            };
+            const R r = __builtin_bit_cast(R, a);
 #pragma unroll
-    for (int j = 0; j < V; ++j) o[j] = a.e[j];
-}
+            for (int i = 0; i < W; ++i) w[i] = r.w[i];
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    // The registers as a new value: what was computed from them before is not kept for later.
+    __device__ __forceinline__ void touch() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) asm volatile("" : "+v"(w[i]));
+    }
+    __device__ __forceinline__ float get(int j) const {
+        if constexpr (std::is_same_v<T, float>)
+            return __uint_as_float(w[j]);
+        else if constexpr (std::is_same_v<T, bf16_t>)
+            return __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+        else
+            return (float)__builtin_bit_cast(_Float16, (uint16_t)(j & 1 ? w[j / 2] >> 16 : w[j / 2]));
+    }
+    __device__ __forceinline__ void set(int j, float v) {   // fp32 only
+        w[j] = __float_as_uint(v);
+    }
+};
+// A gate: log alpha as loaded; alpha itself takes the place of an fp32 one.
 template <typename T, int V>
-__device__ __forceinline__ void store_vec(T *p, const T (&v)[V]) {
+struct Gate : Held<T, V> {
+    __device__ __forceinline__ float first(int j) {
+        const float a = exp_gate(this->get(j));
+        if constexpr (std::is_same_v<T, float>) this->set(j, a);
+        return a;
+    }
+    __device__ __forceinline__ float again(int j) const {
+        if constexpr (std::is_same_v<T, float>) return this->get(j);
+        return exp_gate(this->get(j));
+    }
+};
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T *base, uint32_t off, const T (&v)[V]) {
+    char *p = reinterpret_cast<char *>(base) + (uint32_t)(off * (uint32_t)sizeof(T));
     struct alignas(sizeof(T) * V) A {
         T e[V];
     };
@@ -169,7 +229,7 @@ struct Chain {
     int64_t nchain, blocks;        // chains, tiles of all chains
     const int32_t *cu;
     int32_t *meta;
-    const int32_t *tab;
+    const int32_t *seq;
     int32_t *ctr;
     uint64_t *agg, *pre;
 };
@@ -182,35 +242,43 @@ template <bool PACKED>
 __device__ __forceinline__ float chain_state(const Chain &p, int64_t chain, int k, int c, float A, float H,
                                              float first) {
     if (p.nchunk == 1) return first;
-    const int64_t pitch = (int64_t)kCw;
     const int r = k / kGroup, s = k % kGroup;
-    uint64_t *agg = p.agg + (chain * p.nchunk + r * kGroup) * pitch + c;
-    uint64_t *pre = p.pre + (chain * ((p.nchunk + kGroup - 1) / kGroup) + r) * pitch + c;
+    uint64_t *agg = p.agg + (chain * p.nchunk + r * kGroup) * kCw + c;
+    uint64_t *pre = p.pre + (chain * ((p.nchunk + kGroup - 1) / kGroup) + r) * kCw + c;
     const bool more = k + 1 < p.nchunk;
-    if (more && s < kGroup - 1) put(agg + s * pitch, word(A, H));
-    float in = first;
-    if (k > 0) {
-        uint64_t w[kGroup];
-        for (int looks = 0;; ++looks) {
-            bool all = true;
+    if (more && s < kGroup - 1) put(agg + s * kCw, word(A, H));
+    // Look at all words once, then wait for each that is not there yet.  The
+    // maps of the group join first: what enters the group then takes one step
+    // to what leaves it.
+    uint64_t w[kGroup];
 #pragma unroll
-            for (int j = 0; j < kGroup - 1; ++j) w[j] = j < s ? get(agg + j * pitch) : 0;
-            w[kGroup - 1] = r > 0 ? get(pre) : 0;
-#pragma unroll
-            for (int j = 0; j < kGroup; ++j) all = all && w[j] != kEmpty;
-            if (__all(all)) break;
-            if (looks >= kPatience) {      // kEmpty's halves are not-a-number
+    for (int j = 0; j < kGroup - 1; ++j) w[j] = j < s ? get(agg + j * kCw) : 0;
+    w[kGroup - 1] = r > 0 ? get(pre) : 0;
+    int looks = 0;
+    auto wait = [&](uint64_t &v, const uint64_t *at) {
+        while (__any(v == kEmpty)) {
+            if (++looks > kPatience) {     // kEmpty's halves are not-a-number
                 p.meta[1] = 4;
                 break;
             }
-            __builtin_amdgcn_s_sleep(1);
+            __builtin_amdgcn_s_sleep(2);
+            v = get(at);
         }
-        if (r > 0) in = __uint_as_float((uint32_t)w[kGroup - 1]);
+    };
+    float gA = 1.f, gH = 0.f;
 #pragma unroll
-        for (int j = 0; j < kGroup - 1; ++j)
-            if (j < s) in = apply<PACKED>(__uint_as_float((uint32_t)(w[j] >> 32)), __uint_as_float((uint32_t)w[j]), in);
+    for (int j = 0; j < kGroup - 1; ++j)
+        if (j < s) {
+            wait(w[j], agg + j * kCw);
+            join<PACKED>(gA, gH, __uint_as_float((uint32_t)(w[j] >> 32)), __uint_as_float((uint32_t)w[j]));
+        }
+    float in = first;
+    if (r > 0) {
+        wait(w[kGroup - 1], pre);
+        in = __uint_as_float((uint32_t)w[kGroup - 1]);
     }
-    if (more && s == kGroup - 1) put(pre + pitch, word(0.f, apply<PACKED>(A, H, in)));
+    in = apply<PACKED>(gA, gH, in);
+    if (more && s == kGroup - 1) put(pre + kCw, word(0.f, apply<PACKED>(A, H, in)));
     return in;
 }
 
@@ -225,36 +293,46 @@ __device__ __forceinline__ int draw_place(const Chain &p, int64_t chain, int *s_
     if (p.nchunk <= 1) return 0;
     if (threadIdx.x == 0) *s_k = atomicAdd(&p.ctr[chain], 1);
     __syncthreads();
-    return *s_k;
+    return __builtin_amdgcn_readfirstlane(*s_k);
 }
 
-// Marks in LDS, for each token of tile [t0, t1), the sequence that starts or
-// ends there (-1: none), and runs f(n) for the empty sequences in it.
-template <typename F>
-__device__ __forceinline__ void mark_tokens(const Chain &p, int chunk, int t0, int t1, int *s_start, int *s_end, F f) {
-    for (int i = threadIdx.x; i < kTc; i += 256) s_start[i] = s_end[i] = -1;
-    __syncthreads();
-    for (int n = p.tab[chunk] + threadIdx.x; n <= p.N; n += 256) {
-        const int v = p.cu[n];
-        if (v > t1) break;
-        if (n < p.N) {
-            const bool empty = p.cu[n + 1] == v;
-            if (empty && (v < t1 || t1 == p.T)) f(n);
-            if (!empty && v < t1) s_start[v - t0] = n;
+// Bit i: token t0 + i of the thread's TT tokens is the first (last) of its
+// sequence.  s_seq[i]: the sequence of token i - 1 of the tile, -1 outside.
+template <int TT>
+__device__ __forceinline__ void edges(const int *s_seq, int t0, int len, uint32_t &starts, uint32_t &ends) {
+    starts = ends = 0;
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+        const int q = s_seq[t0 + i + 1];
+        if (t0 + i < len) {
+            starts |= q != s_seq[t0 + i] ? 1u << i : 0u;
+            ends |= q != s_seq[t0 + i + 2] ? 1u << i : 0u;
         }
-        if (n > 0 && v > t0 && p.cu[n - 1] < v) s_end[v - 1 - t0] = n - 1;
     }
-    __syncthreads();
+}
+// Loads what s_seq gets from this thread: token t0 - 1 + tid.
+__device__ __forceinline__ int load_seq(const Chain &p, int t0) {
+    const int64_t t = (int64_t)t0 - 1 + threadIdx.x;
+    return threadIdx.x < kTc + 2 && t >= 0 && t < p.T ? p.seq[t] : -1;
+}
+// What empty sequences end with (begin with, for the gradient) is what they
+// were given.  Rows of [N, D] are shared out over the blocks.
+__device__ __forceinline__ void hand_on(const Chain &p, const float *from, float *to) {
+    if (!to || to == from) return;
+    for (int64_t n = blockIdx.x; n < p.N; n += gridDim.x)
+        if (p.cu[n] == p.cu[n + 1])
+            for (int c = threadIdx.x; c < p.D; c += kNt) to[n * p.D + c] = from ? from[n * p.D + c] : 0.f;
 }
 
 template <typename x_t, typename l_t, typename h_t, int V, bool PACKED>
 __device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, const x_t *__restrict__ x,
-                                                       const l_t *__restrict__ la, const float *init, float *fin,
-                                                       h_t *__restrict__ h) {
-    constexpr int LPR = kCw / V, G = 256 / LPR, TT = kElems / V;
+                                              const l_t *__restrict__ la, const float *init, float *fin,
+                                              h_t *__restrict__ h) {
+    constexpr int LPR = kCw / V, G = kNt / LPR, TT = kElems / V;
     static_assert(G * TT == kTc, "the threads' tokens fill the tile");
+    static_assert(kNt >= kTc + 2, "one thread per entry of s_seq");
     __shared__ float sA[G][kCw], sH[G][kCw];
-    __shared__ int s_start[PACKED ? kTc : 1], s_end[PACKED ? kTc : 1], s_k;
+    __shared__ int s_seq[PACKED ? kTc + 2 : 1], s_k;
     const int k = draw_place(p, chain, &s_k);
     const int row = (int)quotient(chain, p.ntile), col0 = (int)(chain - (int64_t)row * p.ntile) * kCw;
     const int tid = threadIdx.x, lp = tid % LPR, g = tid / LPR;
@@ -264,76 +342,71 @@ __device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, con
     const int cc = live ? ch : 0;
     const int64_t base = ((int64_t)row * p.T + t0) * p.D;
 
-    x_t xr[TT][V];
-    l_t lr[TT][V];
+    const int seq = PACKED ? load_seq(p, t0) : 0;
+    Held<x_t, V> xr[TT];
+    Gate<l_t, V> lr[TT];
     if (len > 0) {
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
             const uint32_t off = (uint32_t)min(g * TT + i, len - 1) * (uint32_t)p.D + (uint32_t)cc;
-            load_vec<l_t, V>(la + base + off, lr[i]);
-            load_vec<x_t, V>(x + base + off, xr[i]);
+            lr[i].load(la + base, off);
+            xr[i].load(x + base, off);
         }
     }
-    uint32_t starts = 0;
+    uint32_t starts = 0, ends = 0;
     if constexpr (PACKED) {
-        mark_tokens(p, k, t0, t0 + len, s_start, s_end, [&](int n) {
-            if (fin && fin != init)
-                for (int c = col0; c < min(col0 + kCw, p.D); ++c)
-                    fin[(int64_t)n * p.D + c] = init ? init[(int64_t)n * p.D + c] : 0.f;
-        });
+        if (tid < kTc + 2) s_seq[tid] = seq;
+        __syncthreads();
+        edges<TT>(s_seq, g * TT, len, starts, ends);
     }
-    float a[TT][V], v[TT][V], A[V], H[V];
+    if (len < kTc) {                                  // tokens past the end change nothing
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+            if (g * TT + i >= len) {
+                lr[i].zero();
+                xr[i].zero();
+            }
+    }
+    // before a sequence's first token the state is its initial one
+    auto enter = [&](int i, float (&s)[V]) {
+        if constexpr (PACKED)
+            if (starts >> i & 1) {
+                const int64_t n = s_seq[g * TT + i + 1];
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[j] = init && live ? init[n * p.D + ch + j] : 0.f;
+            }
+    };
+    float A[V], H[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) A[j] = 1.f, H[j] = 0.f;
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
-        const bool in = g * TT + i < len;
+        enter(i, H);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            a[i][j] = in ? exp_gate(to_f32(lr[i][j])) : 1.f;
-            v[i][j] = in ? to_f32(xr[i][j]) : 0.f;
-        }
-        if constexpr (PACKED) {
-            const int n = s_start[g * TT + i];
-            if (n >= 0) {
-                starts |= 1u << i;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    if (init && live) v[i][j] = fmaf(a[i][j], init[(int64_t)n * p.D + ch + j], v[i][j]);
-                    A[j] = -0.f;
-                    H[j] = v[i][j];
-                }
-                continue;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            H[j] = fmaf(a[i][j], H[j], v[i][j]);
-            A[j] = PACKED && starts ? -0.f : A[j] * a[i][j];
+            const float a = lr[i].first(j);
+            H[j] = fmaf(a, H[j], xr[i].get(j));
+            A[j] *= a;
         }
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        sA[g][lp * V + j] = A[j];
+        sA[g][lp * V + j] = PACKED && starts ? -0.f : A[j];
         sH[g][lp * V + j] = H[j];
     }
     __syncthreads();
     if (tid < kCw) {                                  // one wave, a lane per channel of the tile
-        float ga[G], gh[G], bA = 1.f, bH = 0.f;
+        float bA = 1.f, bH = 0.f;
 #pragma unroll
-        for (int q = 0; q < G; ++q) {
-            ga[q] = sA[q][tid];
-            gh[q] = sH[q][tid];
-            bH = apply<PACKED>(ga[q], gh[q], bH);
-            bA = PACKED && (forgets(ga[q]) || forgets(bA)) ? -0.f : bA * ga[q];
-        }
+        for (int q = 0; q < G; ++q) join<PACKED>(bA, bH, sA[q][tid], sH[q][tid]);
         const bool on = col0 + tid < p.D;
         const int64_t sidx = (int64_t)row * p.D + col0 + tid;
         float s = chain_state<PACKED>(p, chain, k, tid, bA, bH, !PACKED && init && on ? init[sidx] : 0.f);
 #pragma unroll
         for (int q = 0; q < G; ++q) {                 // the state that enters each thread group
+            const float H = sH[q][tid];
             sH[q][tid] = s;
-            s = apply<PACKED>(ga[q], gh[q], s);
+            s = apply<PACKED>(sA[q][tid], H, s);
         }
         if (!PACKED && fin && on && k + 1 >= p.nchunk) fin[sidx] = s;
     }
@@ -343,45 +416,48 @@ __device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, con
 #pragma unroll
     for (int j = 0; j < V; ++j) s[j] = sH[g][lp * V + j];
 #pragma unroll
+    for (int i = 0; i < TT; ++i) lr[i].touch(), xr[i].touch();
+#pragma unroll
     for (int i = 0; i < TT; ++i) {
         const int t = g * TT + i;
         if (t >= len) break;
+        enter(i, s);
         h_t o[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float n = fmaf(a[i][j], s[j], v[i][j]);
-            s[j] = PACKED && (starts >> i & 1) ? v[i][j] : n;
+            s[j] = fmaf(lr[i].again(j), s[j], xr[i].get(j));
             o[j] = round_to<h_t>(s[j]);
         }
-        store_vec<h_t, V>(h + base + ((uint32_t)t * (uint32_t)p.D + (uint32_t)ch), o);
-        if constexpr (PACKED) {
-            if (fin && s_end[t] >= 0)
+        store_vec<h_t, V>(h + base, (uint32_t)t * (uint32_t)p.D + (uint32_t)ch, o);
+        if constexpr (PACKED)
+            if (fin && (ends >> i & 1))
 #pragma unroll
-                for (int j = 0; j < V; ++j) fin[(int64_t)s_end[t] * p.D + ch + j] = s[j];
-        }
+                for (int j = 0; j < V; ++j) fin[(int64_t)s_seq[t + 1] * p.D + ch + j] = s[j];
     }
 }
 
 template <typename x_t, typename l_t, typename h_t, int V, bool PACKED>
-__global__ __launch_bounds__(256) void scan_fwd_kernel(Chain p, const x_t *__restrict__ x, const l_t *__restrict__ la,
-                                                       const float *init, float *fin, h_t *__restrict__ h) {
+__global__ __launch_bounds__(kNt, KWAVES) void scan_fwd_kernel(Chain p, const x_t *__restrict__ x,
+                                                               const l_t *__restrict__ la, const float *init,
+                                                               float *fin, h_t *__restrict__ h) {
     if (PACKED && p.meta[1] != 0) return;
     if (!PACKED && blockIdx.x == 0 && threadIdx.x == 0) p.meta[0] = p.meta[1] = 0;
     for (int64_t b = blockIdx.x; b < p.blocks; b += gridDim.x) {
         scan_fwd_tile<x_t, l_t, h_t, V, PACKED>(p, modulo(b, p.nchain), x, la, init, fin, h);
         __syncthreads();   // the tile's LDS is no longer read
     }
+    if constexpr (PACKED) hand_on(p, init, fin);
 }
 
 template <typename x_t, typename l_t, typename h_t, int V, bool PACKED>
 __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, const l_t *__restrict__ la,
-                                                       const h_t *__restrict__ h, const float *__restrict__ init,
-                                                       const h_t *__restrict__ dh, const float *__restrict__ dfin,
-                                                       x_t *__restrict__ dx, l_t *__restrict__ dla,
-                                                       float *__restrict__ dinit) {
-    constexpr int LPR = kCw / V, G = 256 / LPR, TT = kElems / V;
+                                              const h_t *__restrict__ h, const float *__restrict__ init,
+                                              const h_t *__restrict__ dh, const float *__restrict__ dfin,
+                                              x_t *__restrict__ dx, l_t *__restrict__ dla,
+                                              float *__restrict__ dinit) {
+    constexpr int LPR = kCw / V, G = kNt / LPR, TT = kElems / V;
     __shared__ float sA[G][kCw], sH[G][kCw];
-    __shared__ int s_start[PACKED ? kTc : 1], s_end[PACKED ? kTc : 1], s_k;
+    __shared__ int s_seq[PACKED ? kTc + 2 : 1], s_k;
     const int k = draw_place(p, chain, &s_k);
     const int chunk = p.nchunk > 0 ? p.nchunk - 1 - k : 0;   // the chain runs from the last tile to the first
     const int row = (int)quotient(chain, p.ntile), col0 = (int)(chain - (int64_t)row * p.ntile) * kCw;
@@ -392,79 +468,81 @@ __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, con
     const int cc = live ? ch : 0;
     const int64_t base = ((int64_t)row * p.T + t0) * p.D;
 
-    h_t gr[TT][V], hr[TT][V];
-    l_t lr[TT][V];
+    const int seq = PACKED ? load_seq(p, t0) : 0;
+    Held<h_t, V> gr[TT], hr[TT];
+    Gate<l_t, V> lr[TT];
     if (len > 0) {
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
             const int t = min(g * TT + i, len - 1);
             const uint32_t off = (uint32_t)t * (uint32_t)p.D + (uint32_t)cc;
-            load_vec<l_t, V>(la + base + off, lr[i]);
-            load_vec<h_t, V>(dh + base + off, gr[i]);
-            // h of the token before; at the very first token of a row it is not used
-            load_vec<h_t, V>(h + base + (t0 + t > 0 ? (int64_t)off - p.D : (int64_t)off), hr[i]);
+            lr[i].load(la + base, off);
+            gr[i].load(dh + base, off);
+        }
+        // h of the token before; at the very first token of a row it is not used
+        const int back = t0 > 0 ? 0 : 1;
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            const int t = max(min(g * TT + i, len - 1) - back, 0);
+            hr[i].load(h + base - (1 - back) * (int64_t)p.D, (uint32_t)t * (uint32_t)p.D + (uint32_t)cc);
         }
     }
-    uint32_t ends = 0;
+    uint32_t starts = 0, ends = 0;
     if constexpr (PACKED) {
-        mark_tokens(p, chunk, t0, t0 + len, s_start, s_end, [&](int n) {
-            if (dinit)
-                for (int c = col0; c < min(col0 + kCw, p.D); ++c)
-                    dinit[(int64_t)n * p.D + c] = dfin ? dfin[(int64_t)n * p.D + c] : 0.f;
-        });
+        if (tid < kTc + 2) s_seq[tid] = seq;
+        __syncthreads();
+        edges<TT>(s_seq, g * TT, len, starts, ends);
+    } else if (t0 == 0 && g == 0) {
+        starts = 1;
     }
-    float a[TT][V], v[TT][V], A[V], H[V];
+    if (len < kTc) {
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+            if (g * TT + i >= len) {
+                lr[i].zero();
+                gr[i].zero();
+            }
+    }
+    // behind a sequence's last token the gradient is its final state's
+    auto enter = [&](int i, float (&e)[V]) {
+        if constexpr (PACKED)
+            if (ends >> i & 1) {
+                const int64_t n = s_seq[g * TT + i + 1];
+#pragma unroll
+                for (int j = 0; j < V; ++j) e[j] = dfin && live ? dfin[n * p.D + ch + j] : 0.f;
+            }
+    };
+    float A[V], H[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) A[j] = 1.f, H[j] = 0.f;
 #pragma unroll
     for (int i = TT - 1; i >= 0; --i) {
-        const bool in = g * TT + i < len;
+        enter(i, H);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            a[i][j] = in ? exp_gate(to_f32(lr[i][j])) : 1.f;
-            v[i][j] = in ? to_f32(gr[i][j]) : 0.f;
-        }
-        if constexpr (PACKED) {
-            const int n = s_end[g * TT + i];
-            if (n >= 0) {
-                ends |= 1u << i;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    if (dfin && live) v[i][j] += dfin[(int64_t)n * p.D + ch + j];
-                    A[j] = -0.f;
-                    H[j] = a[i][j] * v[i][j];
-                }
-                continue;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            H[j] = a[i][j] * (v[i][j] + H[j]);
-            A[j] = PACKED && ends ? -0.f : A[j] * a[i][j];
+            const float a = lr[i].first(j);
+            H[j] = a * (gr[i].get(j) + H[j]);
+            A[j] *= a;
         }
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        sA[g][lp * V + j] = A[j];
+        sA[g][lp * V + j] = PACKED && ends ? -0.f : A[j];
         sH[g][lp * V + j] = H[j];
     }
     __syncthreads();
     if (tid < kCw) {
-        float ga[G], gh[G], bA = 1.f, bH = 0.f;
+        float bA = 1.f, bH = 0.f;
 #pragma unroll
-        for (int q = G - 1; q >= 0; --q) {
-            ga[q] = sA[q][tid];
-            gh[q] = sH[q][tid];
-            bH = apply<PACKED>(ga[q], gh[q], bH);
-            bA = PACKED && (forgets(ga[q]) || forgets(bA)) ? -0.f : bA * ga[q];
-        }
+        for (int q = G - 1; q >= 0; --q) join<PACKED>(bA, bH, sA[q][tid], sH[q][tid]);
         const bool on = col0 + tid < p.D;
         const int64_t sidx = (int64_t)row * p.D + col0 + tid;
         float s = chain_state<PACKED>(p, chain, k, tid, bA, bH, !PACKED && dfin && on ? dfin[sidx] : 0.f);
 #pragma unroll
         for (int q = G - 1; q >= 0; --q) {
+            const float H = sH[q][tid];
             sH[q][tid] = s;
-            s = apply<PACKED>(ga[q], gh[q], s);
+            s = apply<PACKED>(sA[q][tid], H, s);
         }
         if (!PACKED && dinit && on && chunk == 0) dinit[sidx] = s;
     }
@@ -474,49 +552,49 @@ __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, con
 #pragma unroll
     for (int j = 0; j < V; ++j) e[j] = sH[g][lp * V + j];
 #pragma unroll
+    for (int i = 0; i < TT; ++i) lr[i].touch(), gr[i].touch(), hr[i].touch();
+#pragma unroll
     for (int i = TT - 1; i >= 0; --i) {
         const int t = g * TT + i;
         if (t >= len) continue;
-        int n = -1;
-        bool begin = !PACKED && t0 + t == 0;
-        if constexpr (PACKED) {
-            n = s_start[t];
-            begin = n >= 0;
-        }
+        enter(i, e);
+        const bool begin = starts >> i & 1;
+        const int64_t n = PACKED ? s_seq[t + 1] : row;
         x_t ox[V];
         l_t ol[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float q = PACKED && (ends >> i & 1) ? v[i][j] : v[i][j] + e[j];
-            e[j] = a[i][j] * q;
-            float past = to_f32(hr[i][j]);
-            if (begin) past = init ? init[(int64_t)(PACKED ? n : row) * p.D + ch + j] : 0.f;
+            const float q = gr[i].get(j) + e[j];
+            e[j] = lr[i].again(j) * q;
+            float past = hr[i].get(j);
+            if (begin) past = init ? init[n * p.D + ch + j] : 0.f;
             ox[j] = round_to<x_t>(q);
             ol[j] = round_to<l_t>(e[j] * past);
         }
         const uint32_t off = (uint32_t)t * (uint32_t)p.D + (uint32_t)ch;
-        store_vec<x_t, V>(dx + base + off, ox);
-        store_vec<l_t, V>(dla + base + off, ol);
-        if constexpr (PACKED) {
+        store_vec<x_t, V>(dx + base, off, ox);
+        store_vec<l_t, V>(dla + base, off, ol);
+        if constexpr (PACKED)
             if (dinit && begin)
 #pragma unroll
-                for (int j = 0; j < V; ++j) dinit[(int64_t)n * p.D + ch + j] = e[j];
-        }
+                for (int j = 0; j < V; ++j) dinit[n * p.D + ch + j] = e[j];
     }
 }
 
 template <typename x_t, typename l_t, typename h_t, int V, bool PACKED>
-__global__ __launch_bounds__(256) void scan_bwd_kernel(Chain p, const l_t *__restrict__ la,
-                                                       const h_t *__restrict__ h, const float *__restrict__ init,
-                                                       const h_t *__restrict__ dh, const float *__restrict__ dfin,
-                                                       x_t *__restrict__ dx, l_t *__restrict__ dla,
-                                                       float *__restrict__ dinit) {
+__global__ __launch_bounds__(kNt, KWAVES) void scan_bwd_kernel(Chain p, const l_t *__restrict__ la,
+                                                               const h_t *__restrict__ h,
+                                                               const float *__restrict__ init,
+                                                               const h_t *__restrict__ dh,
+                                                               const float *__restrict__ dfin, x_t *__restrict__ dx,
+                                                               l_t *__restrict__ dla, float *__restrict__ dinit) {
     if (PACKED && p.meta[1] != 0) return;
     if (!PACKED && blockIdx.x == 0 && threadIdx.x == 0) p.meta[0] = p.meta[1] = 0;
     for (int64_t b = blockIdx.x; b < p.blocks; b += gridDim.x) {
         scan_bwd_tile<x_t, l_t, h_t, V, PACKED>(p, modulo(b, p.nchain), la, h, init, dh, dfin, dx, dla, dinit);
         __syncthreads();   // the tile's LDS is no longer read
     }
+    if constexpr (PACKED) hand_on(p, dfin, dinit);
 }
 
 // Fills `c` and enqueues the setup kernel where the call needs one.
@@ -527,7 +605,7 @@ static hipError_t scan_setup(const ScanArgs &a, Chain &c, hipStream_t st) {
     c.T = a.T, c.D = a.D, c.N = a.N, c.nchunk = (int)w.chunks, c.ntile = (int)w.tiles;
     c.cu = a.cu_seqlens;
     c.meta = reinterpret_cast<int32_t *>(ws);
-    c.tab = reinterpret_cast<int32_t *>(ws + w.off_tab);
+    c.seq = reinterpret_cast<int32_t *>(ws + w.off_seq);
     c.ctr = reinterpret_cast<int32_t *>(ws + w.off_ctr);
     c.agg = reinterpret_cast<uint64_t *>(ws + w.off_agg);
     c.pre = reinterpret_cast<uint64_t *>(ws + w.off_pre);
@@ -535,12 +613,12 @@ static hipError_t scan_setup(const ScanArgs &a, Chain &c, hipStream_t st) {
     c.blocks = (w.chunks > 0 ? w.chunks : 1) * c.nchain;
     if (w.chunks <= 1 && !packed) return hipSuccess;
     const int64_t words16 = (int64_t)(w.total - w.off_agg) / 16;
-    int64_t blocks = (words16 / 4 + 255) / 256;
+    const int64_t work = words16 > (packed ? a.T : 0) ? words16 : a.T;
+    int64_t blocks = (work + 255) / 256;
     blocks = blocks < 1 ? 1 : (blocks > 2048 ? 2048 : blocks);
     ProfScope prof("gdn_scan_setup", st);
-    // an empty packed batch still has one tile: it hands on the states
-    scan_setup_kernel<<<(unsigned)blocks, 256, 0, st>>>(a.N, a.T, w.chunks > 0 ? (int)w.chunks : 1, a.cu_seqlens,
-                                                        c.meta, reinterpret_cast<int32_t *>(ws + w.off_tab), c.ctr,
+    scan_setup_kernel<<<(unsigned)blocks, 256, 0, st>>>(a.N, a.T, a.cu_seqlens, c.meta,
+                                                        reinterpret_cast<int32_t *>(ws + w.off_seq), c.ctr,
                                                         w.chunks > 1 ? c.nchain : 0,
                                                         reinterpret_cast<u32x4_t *>(ws + w.off_agg), words16);
     return hipGetLastError();
@@ -570,7 +648,7 @@ hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st) {
             using l_t = decltype(l);
             using h_t = decltype(h);
             scan_fwd_kernel<x_t, l_t, h_t, decltype(v)::value, decltype(packed)::value>
-                <<<blocks, 256, 0, st>>>(c, static_cast<const x_t *>(a.x),
+                <<<blocks, kNt, 0, st>>>(c, static_cast<const x_t *>(a.x),
                                                    static_cast<const l_t *>(a.log_alpha), a.init_state, a.final_state,
                                                    static_cast<h_t *>(a.h));
             return hipGetLastError();
@@ -590,7 +668,7 @@ hipError_t launch_scan_bwd(const ScanArgs &a, hipStream_t st) {
             using l_t = decltype(l);
             using h_t = decltype(h);
             scan_bwd_kernel<x_t, l_t, h_t, decltype(v)::value, decltype(packed)::value>
-                <<<blocks, 256, 0, st>>>(c, static_cast<const l_t *>(a.log_alpha),
+                <<<blocks, kNt, 0, st>>>(c, static_cast<const l_t *>(a.log_alpha),
                                                    static_cast<const h_t *>(a.h), a.init_state,
                                                    static_cast<const h_t *>(a.d_h), a.d_final,
                                                    static_cast<x_t *>(a.dx), static_cast<l_t *>(a.dlog_alpha),
