@@ -42,24 +42,27 @@
 #include "gdn_ops.h"
 #include "gdn_types.h"
 
+#include <algorithm>
+
 namespace gdn {
 
-#ifndef KNT
-#define KNT 256
-#define KTC 128
-#define KGRP 8
-#define KWAVES 4
+#ifndef CW
+#define CW 128
+#define NTH 512
+#define EL 32
+#define WV 4
+#define NTL 1
 #endif
-constexpr int kTc = KTC;        // tokens of a tile
-constexpr int kCw = 64;         // channels of a tile
-constexpr int kNt = KNT;        // threads of a block
-constexpr int kElems = kTc * kCw / kNt;   // elements per thread
-constexpr int kGroup = KGRP;       // tiles per group of a chain
+constexpr int kCw = CW;         // channels of a tile
+constexpr int kNt = NTH;        // threads of a block
+constexpr int kElems = EL;      // elements per thread
+constexpr int kTc = kNt * kElems / kCw;   // tokens of a tile
+constexpr int kGroup = 8;       // tiles per group of a chain, and groups per section
 constexpr uint64_t kEmpty = ~0ull;
-constexpr int64_t kMaxBlocks = 1 << 22;
+constexpr int64_t kMaxGridX = 1 << 20;
 constexpr int kPatience = 1 << 20;
 
-static int64_t scan_tiles(int64_t n, int w) { return (n + w - 1) / w; }
+static int64_t scan_tiles(int64_t n, int64_t w) { return (n + w - 1) / w; }
 
 ScanWorkspace scan_workspace_layout(int32_t B, int32_t T, int32_t D, int32_t N, bool packed) {
     ScanWorkspace w;
@@ -72,25 +75,35 @@ ScanWorkspace scan_workspace_layout(int32_t B, int32_t T, int32_t D, int32_t N, 
     size_t at = 256;                                   // meta
     w.off_seq = at;
     at += packed ? up((size_t)T * 4) : 0;
+    w.off_init = at;
+    at += packed ? up((size_t)N * D * 4) : 0;
     w.off_ctr = at;
     at += chained ? up((size_t)w.rows * w.tiles * 4) : 0;
     w.off_agg = at;
     at += up((size_t)words * w.chunks * 8);
-    w.off_pre = at;
+    w.off_grp = at;
     at += up((size_t)words * scan_tiles(w.chunks, kGroup) * 8);
+    w.off_pre = at;
+    at += up((size_t)words * scan_tiles(w.chunks, kGroup * kGroup) * 8);
     w.total = at;
     return w;
 }
 
 // Empties the words, zeroes the counters; packed: checks cu_seqlens (codes as
-// in chunk_table_kernel) and writes down each token's sequence.
+// in chunk_table_kernel) and writes down each token's sequence; copies the
+// initial states where the final ones will be written over them (`keep`: a
+// tile reads an initial state twice, and by the second time the sequence may
+// have ended in another block).
 __global__ __launch_bounds__(256) void scan_setup_kernel(int N, int T, const int32_t *__restrict__ cu,
                                                          int32_t *__restrict__ meta, int32_t *__restrict__ seq,
                                                          int32_t *__restrict__ ctr, int64_t nctr,
-                                                         u32x4_t *__restrict__ words, int64_t nwords16) {
+                                                         u32x4_t *__restrict__ words, int64_t nwords16,
+                                                         const float *__restrict__ init, float *__restrict__ keep,
+                                                         int64_t nkeep) {
     const int64_t tid = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
     for (int64_t i = tid; i < nwords16; i += all) words[i] = u32x4_t{~0u, ~0u, ~0u, ~0u};
     for (int64_t i = tid; i < nctr; i += all) ctr[i] = 0;
+    for (int64_t i = tid; i < nkeep; i += all) keep[i] = init[i];
     if (!cu) return;
     for (int64_t t = tid; t < T; t += all) {
         int lo = 1, hi = N;            // the first n >= 1 with cu[n] > t (N if there is none)
@@ -151,6 +164,25 @@ __device__ __forceinline__ uint64_t get(const uint64_t *p) {
 // exp(x): exp2's instruction on x log2(e).
 __device__ __forceinline__ float exp_gate(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+// Every element is used once: loads and stores that leave no trace in the caches.
+template <typename R>
+__device__ __forceinline__ R stream_load(const char *p) {
+#if NTL & 1
+    return __builtin_nontemporal_load(reinterpret_cast<const R *>(p));
+#else
+    return *reinterpret_cast<const R *>(p);
+#endif
+}
+template <typename R>
+__device__ __forceinline__ void stream_store(char *p, R r) {
+#if NTL & 2
+    __builtin_nontemporal_store(r, reinterpret_cast<R *>(p));
+#else
+    *reinterpret_cast<R *>(p) = r;
+#endif
+}
+
 // V consecutive elements as loaded (16-bit types two to a register).  Values
 // are converted each time they are used: the registers that this saves let
 // one block more share a CU.
@@ -161,20 +193,20 @@ struct Held {
     // element `off` of a uniform base (32-bit byte offsets: one scalar base for all of a thread's loads)
     __device__ __forceinline__ void load(const T *base, uint32_t off) {
         const char *p = reinterpret_cast<const char *>(base) + (uint32_t)(off * (uint32_t)sizeof(T));
-        struct alignas(sizeof(T) * V) A {
-            T e[V];
-        };
-        const A a = *reinterpret_cast<const A *>(p);
-        if constexpr (sizeof(A) < 4) {
-            w[0] = __builtin_bit_cast(uint16_t, a);
-        } else {
-            struct R {
-                uint32_t w[W];
-            };
-            const R r = __builtin_bit_cast(R, a);
+        constexpr int B = V * (int)sizeof(T);
+        if constexpr (B == 2)
+            w[0] = stream_load<uint16_t>(p);
+        else if constexpr (B == 4)
+            w[0] = stream_load<uint32_t>(p);
+        else if constexpr (B == 8)
+            take(stream_load<u32x2_t>(p));
+        else
+            take(stream_load<u32x4_t>(p));
+    }
+    template <typename R>
+    __device__ __forceinline__ void take(R r) {
 #pragma unroll
-            for (int i = 0; i < W; ++i) w[i] = r.w[i];
-        }
+        for (int i = 0; i < W; ++i) w[i] = r[i];
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -213,13 +245,20 @@ struct Gate : Held<T, V> {
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T *base, uint32_t off, const T (&v)[V]) {
     char *p = reinterpret_cast<char *>(base) + (uint32_t)(off * (uint32_t)sizeof(T));
-    struct alignas(sizeof(T) * V) A {
+    constexpr int B = V * (int)sizeof(T);
+    struct A {
         T e[V];
-    };
-    A a;
+    } a;
 #pragma unroll
     for (int j = 0; j < V; ++j) a.e[j] = v[j];
-    *reinterpret_cast<A *>(p) = a;
+    if constexpr (B == 2)
+        stream_store(p, __builtin_bit_cast(uint16_t, a));
+    else if constexpr (B == 4)
+        stream_store(p, __builtin_bit_cast(uint32_t, a));
+    else if constexpr (B == 8)
+        stream_store(p, __builtin_bit_cast(u32x2_t, a));
+    else
+        stream_store(p, __builtin_bit_cast(u32x4_t, a));
 }
 
 // ---- the chain --------------------------------------------------------------------
@@ -231,7 +270,7 @@ struct Chain {
     int32_t *meta;
     const int32_t *seq;
     int32_t *ctr;
-    uint64_t *agg, *pre;
+    uint64_t *agg, *grp, *pre;
 };
 
 // The state entering tile `k` (its place in the chain) for column `c`, from
@@ -242,18 +281,16 @@ template <bool PACKED>
 __device__ __forceinline__ float chain_state(const Chain &p, int64_t chain, int k, int c, float A, float H,
                                              float first) {
     if (p.nchunk == 1) return first;
-    const int r = k / kGroup, s = k % kGroup;
-    uint64_t *agg = p.agg + (chain * p.nchunk + r * kGroup) * kCw + c;
-    uint64_t *pre = p.pre + (chain * ((p.nchunk + kGroup - 1) / kGroup) + r) * kCw + c;
+    constexpr int kG = kGroup;
+    const int s = k % kG, r = k / kG % kG, R = k / (kG * kG);
+    uint64_t *agg = p.agg + (chain * p.nchunk + (k - s)) * kCw + c;
+    uint64_t *grp = p.grp + (chain * ((p.nchunk + kG - 1) / kG) + R * kG) * kCw + c;
+    uint64_t *pre = p.pre + (chain * ((p.nchunk + kG * kG - 1) / (kG * kG)) + R) * kCw + c;
     const bool more = k + 1 < p.nchunk;
-    if (more && s < kGroup - 1) put(agg + s * kCw, word(A, H));
-    // Look at all words once, then wait for each that is not there yet.  The
-    // maps of the group join first: what enters the group then takes one step
-    // to what leaves it.
-    uint64_t w[kGroup];
-#pragma unroll
-    for (int j = 0; j < kGroup - 1; ++j) w[j] = j < s ? get(agg + j * kCw) : 0;
-    w[kGroup - 1] = r > 0 ? get(pre) : 0;
+    if (more && s < kG - 1) put(agg + s * kCw, word(A, H));
+    // Look at the words of a kind once, then wait for each that is not there
+    // yet.
+    uint64_t w[kG - 1];
     int looks = 0;
     auto wait = [&](uint64_t &v, const uint64_t *at) {
         while (__any(v == kEmpty)) {
@@ -265,20 +302,36 @@ __device__ __forceinline__ float chain_state(const Chain &p, int64_t chain, int 
             v = get(at);
         }
     };
-    float gA = 1.f, gH = 0.f;
+    auto upper = [](uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); };
+    auto lower = [](uint64_t v) { return __uint_as_float((uint32_t)v); };
+    auto join_words = [&](float &mA, float &mH, const uint64_t *at, int n) {
 #pragma unroll
-    for (int j = 0; j < kGroup - 1; ++j)
-        if (j < s) {
-            wait(w[j], agg + j * kCw);
-            join<PACKED>(gA, gH, __uint_as_float((uint32_t)(w[j] >> 32)), __uint_as_float((uint32_t)w[j]));
-        }
-    float in = first;
-    if (r > 0) {
-        wait(w[kGroup - 1], pre);
-        in = __uint_as_float((uint32_t)w[kGroup - 1]);
+        for (int j = 0; j < kG - 1; ++j) w[j] = j < n ? get(at + j * kCw) : 0;
+#pragma unroll
+        for (int j = 0; j < kG - 1; ++j)
+            if (j < n) {
+                wait(w[j], at + j * kCw);
+                join<PACKED>(mA, mH, upper(w[j]), lower(w[j]));
+            }
+    };
+    float gA = 1.f, gH = 0.f;
+    join_words(gA, gH, agg, s);
+    if (more && s == kG - 1 && r < kG - 1) {
+        float lA = gA, lH = gH;
+        join<PACKED>(lA, lH, A, H);
+        put(grp + r * kCw, word(lA, lH));
     }
-    in = apply<PACKED>(gA, gH, in);
-    if (more && s == kGroup - 1) put(pre + kCw, word(0.f, apply<PACKED>(A, H, in)));
+    float sA = 1.f, sH = 0.f;
+    join_words(sA, sH, grp, r);
+    join<PACKED>(sA, sH, gA, gH);
+    float in = first;
+    if (R > 0) {
+        uint64_t u = get(pre);
+        wait(u, pre);
+        in = lower(u);
+    }
+    in = apply<PACKED>(sA, sH, in);
+    if (more && s == kG - 1 && r == kG - 1) put(pre + kCw, word(0.f, apply<PACKED>(A, H, in)));
     return in;
 }
 
@@ -288,12 +341,19 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 }
 __device__ __forceinline__ int64_t modulo(int64_t a, int64_t b) { return a - quotient(a, b) * b; }
 
-// The place of the block's next tile in its chain.
-__device__ __forceinline__ int draw_place(const Chain &p, int64_t chain, int *s_k) {
-    if (p.nchunk <= 1) return 0;
-    if (threadIdx.x == 0) *s_k = atomicAdd(&p.ctr[chain], 1);
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(*s_k);
+// This block's chain and its place there; false past the last tile.
+__device__ __forceinline__ bool draw_tile(const Chain &p, int64_t &chain, int &k) {
+    __shared__ int s_k;
+    const int64_t b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (b >= p.blocks) return false;
+    chain = modulo(b, p.nchain);
+    k = 0;
+    if (p.nchunk > 1) {
+        if (threadIdx.x == 0) s_k = atomicAdd(&p.ctr[chain], 1);
+        __syncthreads();
+        k = __builtin_amdgcn_readfirstlane(s_k);
+    }
+    return true;
 }
 
 // Bit i: token t0 + i of the thread's TT tokens is the first (last) of its
@@ -319,21 +379,20 @@ __device__ __forceinline__ int load_seq(const Chain &p, int t0) {
 // were given.  Rows of [N, D] are shared out over the blocks.
 __device__ __forceinline__ void hand_on(const Chain &p, const float *from, float *to) {
     if (!to || to == from) return;
-    for (int64_t n = blockIdx.x; n < p.N; n += gridDim.x)
+    for (int64_t n = (int64_t)blockIdx.y * gridDim.x + blockIdx.x; n < p.N; n += (int64_t)gridDim.x * gridDim.y)
         if (p.cu[n] == p.cu[n + 1])
             for (int c = threadIdx.x; c < p.D; c += kNt) to[n * p.D + c] = from ? from[n * p.D + c] : 0.f;
 }
 
 template <typename x_t, typename l_t, typename h_t, int V, bool PACKED>
-__device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, const x_t *__restrict__ x,
+__device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, int k, const x_t *__restrict__ x,
                                               const l_t *__restrict__ la, const float *init, float *fin,
                                               h_t *__restrict__ h) {
     constexpr int LPR = kCw / V, G = kNt / LPR, TT = kElems / V;
     static_assert(G * TT == kTc, "the threads' tokens fill the tile");
     static_assert(kNt >= kTc + 2, "one thread per entry of s_seq");
     __shared__ float sA[G][kCw], sH[G][kCw];
-    __shared__ int s_seq[PACKED ? kTc + 2 : 1], s_k;
-    const int k = draw_place(p, chain, &s_k);
+    __shared__ int s_seq[PACKED ? kTc + 2 : 1];
     const int row = (int)quotient(chain, p.ntile), col0 = (int)(chain - (int64_t)row * p.ntile) * kCw;
     const int tid = threadIdx.x, lp = tid % LPR, g = tid / LPR;
     const int t0 = k * kTc, len = min(kTc, p.T - t0);
@@ -401,7 +460,11 @@ __device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, con
         for (int q = 0; q < G; ++q) join<PACKED>(bA, bH, sA[q][tid], sH[q][tid]);
         const bool on = col0 + tid < p.D;
         const int64_t sidx = (int64_t)row * p.D + col0 + tid;
-        float s = chain_state<PACKED>(p, chain, k, tid, bA, bH, !PACKED && init && on ? init[sidx] : 0.f);
+        float s = !PACKED && init && on ? init[sidx] : 0.f;
+        // the final states may go where the initial ones are: this one is here before anything is published that
+        // lets another block write them
+        asm volatile("" : "+v"(s));
+        s = chain_state<PACKED>(p, chain, k, tid, bA, bH, s);
 #pragma unroll
         for (int q = 0; q < G; ++q) {                 // the state that enters each thread group
             const float H = sH[q][tid];
@@ -437,28 +500,26 @@ __device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, con
 }
 
 template <typename x_t, typename l_t, typename h_t, int V, bool PACKED>
-__global__ __launch_bounds__(kNt, KWAVES) void scan_fwd_kernel(Chain p, const x_t *__restrict__ x,
+__global__ __launch_bounds__(kNt, WV) void scan_fwd_kernel(Chain p, const x_t *__restrict__ x,
                                                                const l_t *__restrict__ la, const float *init,
                                                                float *fin, h_t *__restrict__ h) {
     if (PACKED && p.meta[1] != 0) return;
-    if (!PACKED && blockIdx.x == 0 && threadIdx.x == 0) p.meta[0] = p.meta[1] = 0;
-    for (int64_t b = blockIdx.x; b < p.blocks; b += gridDim.x) {
-        scan_fwd_tile<x_t, l_t, h_t, V, PACKED>(p, modulo(b, p.nchain), x, la, init, fin, h);
-        __syncthreads();   // the tile's LDS is no longer read
-    }
+    if (!PACKED && blockIdx.x + blockIdx.y == 0 && threadIdx.x == 0) p.meta[0] = p.meta[1] = 0;
+    int64_t chain;
+    int k;
+    if (draw_tile(p, chain, k)) scan_fwd_tile<x_t, l_t, h_t, V, PACKED>(p, chain, k, x, la, init, fin, h);
     if constexpr (PACKED) hand_on(p, init, fin);
 }
 
 template <typename x_t, typename l_t, typename h_t, int V, bool PACKED>
-__device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, const l_t *__restrict__ la,
+__device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, int k, const l_t *__restrict__ la,
                                               const h_t *__restrict__ h, const float *__restrict__ init,
                                               const h_t *__restrict__ dh, const float *__restrict__ dfin,
                                               x_t *__restrict__ dx, l_t *__restrict__ dla,
                                               float *__restrict__ dinit) {
     constexpr int LPR = kCw / V, G = kNt / LPR, TT = kElems / V;
     __shared__ float sA[G][kCw], sH[G][kCw];
-    __shared__ int s_seq[PACKED ? kTc + 2 : 1], s_k;
-    const int k = draw_place(p, chain, &s_k);
+    __shared__ int s_seq[PACKED ? kTc + 2 : 1];
     const int chunk = p.nchunk > 0 ? p.nchunk - 1 - k : 0;   // the chain runs from the last tile to the first
     const int row = (int)quotient(chain, p.ntile), col0 = (int)(chain - (int64_t)row * p.ntile) * kCw;
     const int tid = threadIdx.x, lp = tid % LPR, g = tid / LPR;
@@ -537,7 +598,10 @@ __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, con
         for (int q = G - 1; q >= 0; --q) join<PACKED>(bA, bH, sA[q][tid], sH[q][tid]);
         const bool on = col0 + tid < p.D;
         const int64_t sidx = (int64_t)row * p.D + col0 + tid;
-        float s = chain_state<PACKED>(p, chain, k, tid, bA, bH, !PACKED && dfin && on ? dfin[sidx] : 0.f);
+        float s = !PACKED && dfin && on ? dfin[sidx] : 0.f;
+        // (as in the forward pass)
+        asm volatile("" : "+v"(s));
+        s = chain_state<PACKED>(p, chain, k, tid, bA, bH, s);
 #pragma unroll
         for (int q = G - 1; q >= 0; --q) {
             const float H = sH[q][tid];
@@ -582,23 +646,23 @@ __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, con
 }
 
 template <typename x_t, typename l_t, typename h_t, int V, bool PACKED>
-__global__ __launch_bounds__(kNt, KWAVES) void scan_bwd_kernel(Chain p, const l_t *__restrict__ la,
+__global__ __launch_bounds__(kNt, WV) void scan_bwd_kernel(Chain p, const l_t *__restrict__ la,
                                                                const h_t *__restrict__ h,
                                                                const float *__restrict__ init,
                                                                const h_t *__restrict__ dh,
                                                                const float *__restrict__ dfin, x_t *__restrict__ dx,
                                                                l_t *__restrict__ dla, float *__restrict__ dinit) {
     if (PACKED && p.meta[1] != 0) return;
-    if (!PACKED && blockIdx.x == 0 && threadIdx.x == 0) p.meta[0] = p.meta[1] = 0;
-    for (int64_t b = blockIdx.x; b < p.blocks; b += gridDim.x) {
-        scan_bwd_tile<x_t, l_t, h_t, V, PACKED>(p, modulo(b, p.nchain), la, h, init, dh, dfin, dx, dla, dinit);
-        __syncthreads();   // the tile's LDS is no longer read
-    }
+    if (!PACKED && blockIdx.x + blockIdx.y == 0 && threadIdx.x == 0) p.meta[0] = p.meta[1] = 0;
+    int64_t chain;
+    int k;
+    if (draw_tile(p, chain, k)) scan_bwd_tile<x_t, l_t, h_t, V, PACKED>(p, chain, k, la, h, init, dh, dfin, dx, dla, dinit);
     if constexpr (PACKED) hand_on(p, dfin, dinit);
 }
 
 // Fills `c` and enqueues the setup kernel where the call needs one.
-static hipError_t scan_setup(const ScanArgs &a, Chain &c, hipStream_t st) {
+// `init`: the initial states that the kernel reads.
+static hipError_t scan_setup(const ScanArgs &a, Chain &c, const float *&init, hipStream_t st) {
     const bool packed = a.cu_seqlens != nullptr;
     const auto w = scan_workspace_layout(a.B, a.T, a.D, a.N, packed);
     char *ws = static_cast<char *>(a.workspace);
@@ -608,19 +672,26 @@ static hipError_t scan_setup(const ScanArgs &a, Chain &c, hipStream_t st) {
     c.seq = reinterpret_cast<int32_t *>(ws + w.off_seq);
     c.ctr = reinterpret_cast<int32_t *>(ws + w.off_ctr);
     c.agg = reinterpret_cast<uint64_t *>(ws + w.off_agg);
+    c.grp = reinterpret_cast<uint64_t *>(ws + w.off_grp);
     c.pre = reinterpret_cast<uint64_t *>(ws + w.off_pre);
     c.nchain = w.rows * w.tiles;
     c.blocks = (w.chunks > 0 ? w.chunks : 1) * c.nchain;
+    init = a.init_state;
     if (w.chunks <= 1 && !packed) return hipSuccess;
+    float *keep = reinterpret_cast<float *>(ws + w.off_init);
+    const bool over = packed && init && init == a.final_state;
+    if (over) init = keep;
     const int64_t words16 = (int64_t)(w.total - w.off_agg) / 16;
-    const int64_t work = words16 > (packed ? a.T : 0) ? words16 : a.T;
+    const int64_t other = over ? std::max<int64_t>(a.T, (int64_t)a.N * a.D) : packed ? a.T : 0;
+    const int64_t work = std::max(words16, other);
     int64_t blocks = (work + 255) / 256;
     blocks = blocks < 1 ? 1 : (blocks > 2048 ? 2048 : blocks);
     ProfScope prof("gdn_scan_setup", st);
     scan_setup_kernel<<<(unsigned)blocks, 256, 0, st>>>(a.N, a.T, a.cu_seqlens, c.meta,
                                                         reinterpret_cast<int32_t *>(ws + w.off_seq), c.ctr,
                                                         w.chunks > 1 ? c.nchain : 0,
-                                                        reinterpret_cast<u32x4_t *>(ws + w.off_agg), words16);
+                                                        reinterpret_cast<u32x4_t *>(ws + w.off_agg), words16,
+                                                        a.init_state, keep, over ? (int64_t)a.N * a.D : 0);
     return hipGetLastError();
 }
 
@@ -638,9 +709,10 @@ static hipError_t with_shape(const ScanArgs &a, F f) {
 
 hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st) {
     Chain c;
-    hipError_t e = scan_setup(a, c, st);
+    const float *init;
+    hipError_t e = scan_setup(a, c, init, st);
     if (e != hipSuccess) return e;
-    const unsigned blocks = (unsigned)(c.blocks < kMaxBlocks ? c.blocks : kMaxBlocks);
+    const dim3 blocks((unsigned)std::min(c.blocks, kMaxGridX), (unsigned)scan_tiles(c.blocks, kMaxGridX));
     ProfScope prof("gdn_scan_fwd", st);
     return with_types(a.in_dtype, a.gate_dtype, a.out_dtype, [&](auto x, auto l, auto h) {
         return with_shape(a, [&](auto v, auto packed) {
@@ -649,7 +721,7 @@ hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st) {
             using h_t = decltype(h);
             scan_fwd_kernel<x_t, l_t, h_t, decltype(v)::value, decltype(packed)::value>
                 <<<blocks, kNt, 0, st>>>(c, static_cast<const x_t *>(a.x),
-                                                   static_cast<const l_t *>(a.log_alpha), a.init_state, a.final_state,
+                                                   static_cast<const l_t *>(a.log_alpha), init, a.final_state,
                                                    static_cast<h_t *>(a.h));
             return hipGetLastError();
         });
@@ -658,9 +730,10 @@ hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st) {
 
 hipError_t launch_scan_bwd(const ScanArgs &a, hipStream_t st) {
     Chain c;
-    hipError_t e = scan_setup(a, c, st);
+    const float *init;
+    hipError_t e = scan_setup(a, c, init, st);
     if (e != hipSuccess) return e;
-    const unsigned blocks = (unsigned)(c.blocks < kMaxBlocks ? c.blocks : kMaxBlocks);
+    const dim3 blocks((unsigned)std::min(c.blocks, kMaxGridX), (unsigned)scan_tiles(c.blocks, kMaxGridX));
     ProfScope prof("gdn_scan_bwd", st);
     return with_types(a.in_dtype, a.gate_dtype, a.out_dtype, [&](auto x, auto l, auto h) {
         return with_shape(a, [&](auto v, auto packed) {
@@ -669,7 +742,7 @@ hipError_t launch_scan_bwd(const ScanArgs &a, hipStream_t st) {
             using h_t = decltype(h);
             scan_bwd_kernel<x_t, l_t, h_t, decltype(v)::value, decltype(packed)::value>
                 <<<blocks, kNt, 0, st>>>(c, static_cast<const l_t *>(a.log_alpha),
-                                                   static_cast<const h_t *>(a.h), a.init_state,
+                                                   static_cast<const h_t *>(a.h), init,
                                                    static_cast<const h_t *>(a.d_h), a.d_final,
                                                    static_cast<x_t *>(a.dx), static_cast<l_t *>(a.dlog_alpha),
                                                    a.d_init);

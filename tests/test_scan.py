@@ -171,6 +171,18 @@ def test_continuation_in_place(D):
     within(state, wfin, 2 * last, "fp32", "state")
 
 
+def test_packed_continuation_in_place():
+    """The final states over the initial ones, many sequences of all lengths: the bits of separate buffers."""
+    g = np.random.default_rng(12)
+    cu = np.concatenate([[0], np.sort(g.integers(0, 6001, 200)), [6001]]).tolist()
+    t, _ = inputs(1, 6001, 192, cu, ("bf16", "bf16", "fp32"), seed=12)
+    ref = gdn.scan_fwd(t["x"], t["la"], t["init"], cu_tensor(cu))
+    for _ in range(3):
+        state = t["init"].clone()
+        h, fin = gdn.scan_fwd(t["x"], t["la"], state, cu_tensor(cu), final_state=state)
+        assert torch.equal(h, ref[0]) and torch.equal(state, ref[1])
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_bad_values_stay_in_their_sequence(bad):
     cu = [0, 5, 130, 131, 400, 400, 700]
