@@ -355,12 +355,12 @@ def _addr(t: Optional[torch.Tensor]):
 
 def _call(name, device, *args):
     """One library call with `device` current and its current stream as the last argument."""
-    f = getattr(load(), name)
-    if torch.cuda.current_device() == device.index:
-        status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = getattr(_lib or load(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+            status = getattr(load(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
     if status != 0:
         _check(status)
 
@@ -368,15 +368,17 @@ def _call(name, device, *args):
 def _cuda(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} is on {t.device}, expected a GPU")
     return t.device
 
 
 def _shaped(t, name, shape, dtypes, device):
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.is_contiguous() \
+            and t.device == device:
+        return
     _need(t, name, dtypes, device, len(shape))
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
 
 
 def _workspace(workspace, size, device):

@@ -4,10 +4,13 @@
 //
 // A row belongs to L lanes (a power of two): part of a wave for short rows,
 // so that a wave takes several, or whole waves that join through LDS.  Every
-// lane holds K groups of 8 elements.  Where D is a multiple of 8 a group is 8
-// neighbours, loaded as one or two 16-byte vectors; otherwise rows do not
-// start on a vector and a group is 8 elements L apart, so that lanes still
-// load neighbours.
+// lane holds K groups of 8 neighbouring elements, loaded as one or two 16-byte
+// vectors.  Where D is no multiple of 8 the vectors are not aligned (the
+// hardware takes them as they are) and the row's last group starts earlier, so
+// that it ends with the row: the elements that it shares with the group before
+// count once and are written twice, with the same bits.  Rows of less than 8
+// elements go one by one.  A block walks over rows a grid apart and has the loads of its
+// next rows in flight while it works on a row.
 //
 // The gradients of weight and bias are sums over rows.  A block walks over
 // rows a grid apart and keeps its columns' sums in registers, its row groups
@@ -21,70 +24,118 @@
 namespace gdn {
 
 // Layout of one row over a block.
-template <int L_, int K_, int NT_, bool VEC_>
+template <int L_, int K_, int NT_, bool WHOLE_>
 struct RowShape {
     static constexpr int L = L_;         // lanes per row
     static constexpr int K = K_;         // groups of 8 elements per lane
     static constexpr int NT = NT_;       // threads of the block
-    static constexpr bool VEC = VEC_;
+    static constexpr bool WHOLE = WHOLE_;   // D is a multiple of 8
     static constexpr int ROWS = NT / L;  // rows of a block at a time
     static constexpr int E = 8 * K;      // elements per lane
-    // column of element e of group k for lane l
-    __device__ __forceinline__ static int col(int l, int k, int e) {
-        return VEC ? (k * L + l) * 8 + e : (k * 8 + e) * L + l;
+    // first column of group k of lane l, and where it is loaded from
+    __device__ __forceinline__ static int col(int l, int k) { return (k * L + l) * 8; }
+    __device__ __forceinline__ static int from(int l, int k, int D) {
+        return WHOLE ? col(l, k) : max(min(col(l, k), D - 8), 0);
+    }
+    // whether element e of the group, at column from() + e, counts for this lane
+    __device__ __forceinline__ static bool counts(int l, int k, int e, int D) {
+        const int c = col(l, k);
+        return WHOLE ? c < D : c < D && from(l, k, D) + e >= c && e < D;
     }
 };
 
-// Elements of a row that lane l holds, as fp32; 0 past the row's end.
-template <typename S, typename T>
-__device__ __forceinline__ void load_row(const T *__restrict__ row, int D, int l, float (&v)[S::E]) {
+typedef u32x4_t loose4_t __attribute__((aligned(2)));   // 16 bytes on any element
+
+// 8 elements as loaded.
+template <typename T>
+struct Raw {
+    static constexpr int W = (int)sizeof(T) / 2;   // 16-byte vectors
+    u32x4_t w[W];
+    __device__ __forceinline__ float get(int e) const {
+        if constexpr (std::is_same_v<T, float>)
+            return __uint_as_float(w[e / 4][e % 4]);
+        else if constexpr (std::is_same_v<T, bf16_t>)
+            return __uint_as_float(e & 1 ? w[0][e / 2] & 0xFFFF0000u : w[0][e / 2] << 16);
+        else
+            return (float)__builtin_bit_cast(_Float16, (uint16_t)(e & 1 ? w[0][e / 2] >> 16 : w[0][e / 2]));
+    }
+    __device__ __forceinline__ void put(int e, T v) {
+        if constexpr (std::is_same_v<T, float>) {
+            w[e / 4][e % 4] = __float_as_uint(v);
+        } else {
+            const uint32_t b = __builtin_bit_cast(uint16_t, v);
+            w[0][e / 2] = e & 1 ? (w[0][e / 2] & 0xFFFFu) | b << 16 : (w[0][e / 2] & 0xFFFF0000u) | b;
+        }
+    }
+};
+// The groups of lane l of a row; 0 past the row's end.  STREAM: the loads leave
+// no trace in the caches, as the stores do.  Measured, 262144 x 128 and 16384 x
+// 2048: stores so, forward 30.5 -> 26.6 us at 2048; loads so, backward 42 -> 40
+// us, but forward 26.6 -> 30.5 us.
+template <typename S, bool STREAM, typename T>
+__device__ __forceinline__ void load_raw(const T *__restrict__ row, int D, int l, Raw<T> (&v)[S::K]) {
 #pragma unroll
     for (int k = 0; k < S::K; ++k) {
-        if constexpr (S::VEC) {
-            const int c = S::col(l, k, 0);
-            float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (c < D) load8_f32(row + c, o);
+        const T *from = row + S::from(l, k, D);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[8 * k + e] = o[e];
+        for (int i = 0; i < Raw<T>::W; ++i) v[k].w[i] = u32x4_t{0u, 0u, 0u, 0u};
+        if (S::col(l, k) >= D) continue;
+        if (S::WHOLE || D >= 8) {
+#pragma unroll
+            for (int i = 0; i < Raw<T>::W; ++i) {
+                const char *p = reinterpret_cast<const char *>(from) + 16 * i;
+                if constexpr (!S::WHOLE)
+                    v[k].w[i] = *reinterpret_cast<const loose4_t *>(p);
+                else if constexpr (STREAM)
+                    v[k].w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(p));
+                else
+                    v[k].w[i] = *reinterpret_cast<const u32x4_t *>(p);
+            }
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = S::col(l, k, e);
-                v[8 * k + e] = c < D ? to_f32(row[c]) : 0.f;
-            }
+            for (int e = 0; e < 7; ++e)
+                if (e < D) v[k].put(e, from[e]);
         }
     }
 }
-template <typename T>
-__device__ __forceinline__ void store8(T *p, const float (&v)[8]) {
-    if constexpr (std::is_same_v<T, float>) {
-        reinterpret_cast<float4_t *>(p)[0] = float4_t{v[0], v[1], v[2], v[3]};
-        reinterpret_cast<float4_t *>(p)[1] = float4_t{v[4], v[5], v[6], v[7]};
-    } else {
-        struct alignas(16) O {
-            T e[8];
-        } o;
+template <typename S, typename T>
+__device__ __forceinline__ void unpack(const Raw<T> (&r)[S::K], float (&v)[S::E]) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o.e[e] = round_to<T>(v[e]);
-        *reinterpret_cast<O *>(p) = o;
-    }
+    for (int k = 0; k < S::K; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[8 * k + e] = r[k].get(e);
+}
+// fp32 parameters of a lane's groups.
+template <typename S>
+__device__ __forceinline__ void load_param(const float *__restrict__ p, int D, int l, float (&v)[S::E]) {
+    Raw<float> r[S::K];
+    load_raw<S, false>(p, D, l, r);
+    unpack<S>(r, v);
 }
 template <typename S, typename T>
 __device__ __forceinline__ void store_row(T *__restrict__ row, int D, int l, const float (&v)[S::E]) {
 #pragma unroll
     for (int k = 0; k < S::K; ++k) {
-        if constexpr (S::VEC) {
-            const int c = S::col(l, k, 0);
-            float o[8];
+        if (S::col(l, k) >= D) continue;
+        T *to = row + S::from(l, k, D);
+        Raw<T> r;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = v[8 * k + e];
-            if (c < D) store8(row + c, o);
+        for (int i = 0; i < Raw<T>::W; ++i) r.w[i] = u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.put(e, round_to<T>(v[8 * k + e]));
+        if (S::WHOLE || D >= 8) {
+#pragma unroll
+            for (int i = 0; i < Raw<T>::W; ++i) {
+                char *p = reinterpret_cast<char *>(to) + 16 * i;
+                if constexpr (S::WHOLE)
+                    __builtin_nontemporal_store(r.w[i], reinterpret_cast<u32x4_t *>(p));
+                else
+                    *reinterpret_cast<loose4_t *>(p) = r.w[i];
+            }
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = S::col(l, k, e);
-                if (c < D) row[c] = round_to<T>(v[8 * k + e]);
-            }
+            for (int e = 0; e < 7; ++e)
+                if (e < D) to[e] = round_to<T>(v[8 * k + e]);
         }
     }
 }
@@ -119,17 +170,23 @@ __global__ __launch_bounds__(S::NT) void layernorm_fwd_kernel(int64_t rows, int 
     __shared__ float s[S::NT / 64][2];
     const int l = threadIdx.x % S::L, g = threadIdx.x / S::L;
     float wv[S::E], bv[S::E];
-    if (w) load_row<S>(w, D, l, wv);
-    if (b) load_row<S>(b, D, l, bv);
+    if (w) load_param<S>(w, D, l, wv);
+    if (b) load_param<S>(b, D, l, bv);
+    Raw<x_t> raw[S::K];
+    auto load = [&](int64_t r0) { load_raw<S, false>(x + min(r0 + g, rows - 1) * D, D, l, raw); };
+    load((int64_t)blockIdx.x * S::ROWS);
     const float n = (float)D;
     for (int64_t r0 = (int64_t)blockIdx.x * S::ROWS; r0 < rows; r0 += (int64_t)gridDim.x * S::ROWS) {
         const int64_t r = r0 + g;
         const bool on = r < rows;
         float v[S::E];
-        load_row<S>(x + (on ? r : 0) * D, D, l, v);
+        unpack<S>(raw, v);
+        if (r0 + (int64_t)gridDim.x * S::ROWS < rows) load(r0 + (int64_t)gridDim.x * S::ROWS);
         float m = 0.f, q = 0.f, none = 0.f;
 #pragma unroll
-        for (int e = 0; e < S::E; ++e) m += v[e];
+        for (int k = 0; k < S::K; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m += S::WHOLE || S::counts(l, k, e, D) ? v[8 * k + e] : 0.f;
         row_sum2<S>(m, none, s);
         m /= n;
 #pragma unroll
@@ -137,8 +194,8 @@ __global__ __launch_bounds__(S::NT) void layernorm_fwd_kernel(int64_t rows, int 
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float &c = v[8 * k + e];
-                c = S::col(l, k, S::VEC ? 0 : e) < D ? c - m : 0.f;
-                q = fmaf(c, c, q);
+                c -= m;
+                q = S::counts(l, k, e, D) ? fmaf(c, c, q) : q;
             }
         row_sum2<S>(q, none, s);
         q = 1.f / sqrtf(q / n + eps);
@@ -169,30 +226,46 @@ __global__ __launch_bounds__(S::NT) void layernorm_bwd_kernel(int64_t rows, int 
     __shared__ float s[S::NT / 64][2];
     const int l = threadIdx.x % S::L, g = threadIdx.x / S::L;
     float wv[S::E], aw[S::E], ab[S::E];
-    if (w) load_row<S>(w, D, l, wv);
+    if (w) load_param<S>(w, D, l, wv);
+    Raw<y_t> ry[S::K];
+    Raw<x_t> rx[S::K];
+    float rm, rq;
+    auto load = [&](int64_t r0) {
+        const int64_t r = min(r0 + g, rows - 1);
+        load_raw<S, true>(dy + r * D, D, l, ry);
+        load_raw<S, true>(x + r * D, D, l, rx);
+        rm = mean[r];
+        rq = rstd[r];
+    };
+    load((int64_t)blockIdx.x * S::ROWS);
 #pragma unroll
     for (int e = 0; e < S::E; ++e) aw[e] = ab[e] = 0.f;
     const float n = (float)D;
     for (int64_t r0 = (int64_t)blockIdx.x * S::ROWS; r0 < rows; r0 += (int64_t)gridDim.x * S::ROWS) {
         const int64_t r = r0 + g;
         const bool on = r < rows;
-        const int64_t rr = on ? r : 0;
         float u[S::E], c[S::E];
-        load_row<S>(dy + rr * D, D, l, u);
-        load_row<S>(x + rr * D, D, l, c);
-        const float m = mean[rr], q = rstd[rr];
+        unpack<S>(ry, u);
+        unpack<S>(rx, c);
+        const float m = rm, q = rq;
+        if (r0 + (int64_t)gridDim.x * S::ROWS < rows) load(r0 + (int64_t)gridDim.x * S::ROWS);
         float c1 = 0.f, c2 = 0.f;
 #pragma unroll
-        for (int e = 0; e < S::E; ++e) {
-            c[e] = (c[e] - m) * q;                  // past the row's end u = 0, so c counts for nothing there
-            if (SUMS && on) {
-                aw[e] = fmaf(u[e], c[e], aw[e]);
-                ab[e] += u[e];
+        for (int k = 0; k < S::K; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int e = 8 * k + i;
+                c[e] = (c[e] - m) * q;
+                if (SUMS && on && S::counts(l, k, i, D)) {
+                    aw[e] = fmaf(u[e], c[e], aw[e]);
+                    ab[e] += u[e];
+                }
+                if (w) u[e] *= wv[e];
+                if (S::counts(l, k, i, D)) {
+                    c1 += u[e];
+                    c2 = fmaf(u[e], c[e], c2);
+                }
             }
-            if (w) u[e] *= wv[e];
-            c1 += u[e];
-            c2 = fmaf(u[e], c[e], c2);
-        }
         row_sum2<S>(c1, c2, s);
         c1 /= n;
         c2 /= n;
@@ -208,8 +281,8 @@ __global__ __launch_bounds__(S::NT) void layernorm_bwd_kernel(int64_t rows, int 
             for (int k = 0; k < S::K; ++k)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int col = S::col(l, k, e);
-                    if (col < D) line[col] = aw[8 * k + e], line[D + col] = ab[8 * k + e];
+                    const int col = S::from(l, k, D) + e;
+                    if (S::counts(l, k, e, D)) line[col] = aw[8 * k + e], line[D + col] = ab[8 * k + e];
                 }
         } else {
             __shared__ float sw[S::NT][9], sb[S::NT][9];
@@ -220,8 +293,8 @@ __global__ __launch_bounds__(S::NT) void layernorm_bwd_kernel(int64_t rows, int 
                 for (int e = 0; e < 8; ++e) sw[threadIdx.x][e] = aw[8 * k + e], sb[threadIdx.x][e] = ab[8 * k + e];
                 __syncthreads();
                 for (int i = threadIdx.x; i < S::L * 8; i += S::NT) {
-                    const int il = i >> 3, e = i & 7, col = S::col(il, k, e);
-                    if (col >= D) continue;
+                    const int il = i >> 3, e = i & 7, col = S::from(il, k, D) + e;
+                    if (!S::counts(il, k, e, D)) continue;
                     float tw = 0.f, tb = 0.f;
 #pragma unroll 8
                     for (int q = 0; q < S::ROWS; ++q) tw += sw[q * S::L + il][e], tb += sb[q * S::L + il][e];
@@ -260,33 +333,39 @@ __global__ __launch_bounds__(1024) void layernorm_sums_kernel(int lines, int D, 
 
 // f(RowShape{}) with the layout for D: as many lanes as 8 elements each need,
 // up to a wave; longer rows take 16 elements a lane, then more waves.
-template <bool VEC, typename F>
+template <bool WHOLE, int NT, typename F>
 static hipError_t with_row_shape_of(int D, F f) {
-    if (D <= 64) return f(RowShape<8, 1, 256, VEC>{});
-    if (D <= 128) return f(RowShape<16, 1, 256, VEC>{});
-    if (D <= 256) return f(RowShape<32, 1, 256, VEC>{});
-    if (D <= 512) return f(RowShape<64, 1, 256, VEC>{});
-    if (D <= 1024) return f(RowShape<64, 2, 256, VEC>{});
-    if (D <= 2048) return f(RowShape<128, 2, 256, VEC>{});
-    if (D <= 4096) return f(RowShape<256, 2, 256, VEC>{});
-    if (D <= 8192) return f(RowShape<512, 2, 512, VEC>{});
-    return f(RowShape<1024, 2, 1024, VEC>{});
+    if (D <= 64) return f(RowShape<8, 1, NT, WHOLE>{});
+    if (D <= 128) return f(RowShape<16, 1, NT, WHOLE>{});
+    if (D <= 256) return f(RowShape<32, 1, NT, WHOLE>{});
+    if (D <= 512) return f(RowShape<64, 1, NT, WHOLE>{});
+    if (D <= 1024) return f(RowShape<64, 2, NT, WHOLE>{});
+    if (D <= 2048) return f(RowShape<128, 2, NT, WHOLE>{});
+    if (D <= 4096) return f(RowShape<256, 2, NT, WHOLE>{});
+    if (D <= 8192) return f(RowShape<512, 2, 512, WHOLE>{});
+    return f(RowShape<1024, 2, 1024, WHOLE>{});
 }
-template <typename F>
+template <int NT, typename F>
 static hipError_t with_row_shape(int D, F f) {
-    return D % 8 == 0 ? with_row_shape_of<true>(D, f) : with_row_shape_of<false>(D, f);
+    return D % 8 == 0 ? with_row_shape_of<true, NT>(D, f) : with_row_shape_of<false, NT>(D, f);
 }
+
+// Threads of a block.  Measured at 262144 x 128 and 4093 x 1001 (backward):
+// 512 threads, two blocks a CU, 40 and 18 us; 256 threads 46 and 25; 1024
+// threads as 512.
+constexpr int kFwdThreads = 256, kBwdThreads = 512;
+constexpr int64_t kFwdBlocks = 8192;   // more only load the parameters again
 
 // Blocks of the backward kernel, and so lines of partial sums.
 static int64_t bwd_blocks(int64_t rows, int rows_per_block, int threads) {
-    const int64_t most = 256 * (1024 / threads);      // about 1024 threads on each of 256 CUs
+    const int64_t most = 256 * (1024 / threads);   // 1024 threads on each of 256 CUs
     const int64_t need = (rows + rows_per_block - 1) / rows_per_block;
     return need < most ? need : most;
 }
 
 size_t layernorm_bwd_workspace(int64_t rows, int32_t dim) {
     int64_t lines = 0;
-    with_row_shape(dim, [&](auto s) {
+    with_row_shape<kBwdThreads>(dim, [&](auto s) {
         using S = decltype(s);
         lines = bwd_blocks(rows, S::ROWS, S::NT);
         return hipSuccess;
@@ -299,10 +378,10 @@ hipError_t launch_layernorm_fwd(const NormArgs &a, hipStream_t st) {
     return with_types(a.in_dtype, a.out_dtype, a.in_dtype, [&](auto x, auto y, auto) {
         using x_t = decltype(x);
         using y_t = decltype(y);
-        return with_row_shape(a.dim, [&](auto s) {
+        return with_row_shape<kFwdThreads>(a.dim, [&](auto s) {
             using S = decltype(s);
             const int64_t need = (a.rows + S::ROWS - 1) / S::ROWS;
-            const unsigned blocks = (unsigned)(need < (1 << 20) ? need : (1 << 20));
+            const unsigned blocks = (unsigned)(need < kFwdBlocks ? need : kFwdBlocks);
             layernorm_fwd_kernel<S, x_t, y_t><<<blocks, S::NT, 0, st>>>(
                 a.rows, a.dim, a.eps, static_cast<const x_t *>(a.x), a.weight, a.bias, static_cast<y_t *>(a.y),
                 a.mean, a.rstd);
@@ -321,7 +400,7 @@ hipError_t launch_layernorm_bwd(const NormArgs &a, hipStream_t st) {
         e = with_types(a.in_dtype, a.out_dtype, a.in_dtype, [&](auto x, auto y, auto) {
             using x_t = decltype(x);
             using y_t = decltype(y);
-            return with_row_shape(a.dim, [&](auto s) {
+            return with_row_shape<kBwdThreads>(a.dim, [&](auto s) {
                 using S = decltype(s);
                 blocks = bwd_blocks(a.rows, S::ROWS, S::NT);
                 auto go = [&](auto *kernel) {
