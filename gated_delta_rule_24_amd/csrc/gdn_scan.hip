@@ -64,6 +64,12 @@ constexpr int kPatience = 1 << 20;
 
 static int64_t scan_tiles(int64_t n, int64_t w) { return (n + w - 1) / w; }
 
+// Whether final states over the initial ones make the kernels read a copy:
+// a packed tile reads an initial state twice, and by the second time the
+// sequence may have ended in another block; where D is no multiple of 4 two
+// blocks read the channels that they share.
+static bool keeps_init(bool packed, int32_t D) { return packed || D % 4 != 0; }
+
 ScanWorkspace scan_workspace_layout(int32_t B, int32_t T, int32_t D, int32_t N, bool packed) {
     ScanWorkspace w;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -76,7 +82,7 @@ ScanWorkspace scan_workspace_layout(int32_t B, int32_t T, int32_t D, int32_t N, 
     w.off_seq = at;
     at += packed ? up((size_t)T * 4) : 0;
     w.off_init = at;
-    at += packed ? up((size_t)N * D * 4) : 0;
+    at += keeps_init(packed, D) ? up((size_t)N * D * 4) : 0;
     w.off_ctr = at;
     at += chained ? up((size_t)w.rows * w.tiles * 4) : 0;
     w.off_agg = at;
@@ -91,9 +97,7 @@ ScanWorkspace scan_workspace_layout(int32_t B, int32_t T, int32_t D, int32_t N, 
 
 // Empties the words, zeroes the counters; packed: checks cu_seqlens (codes as
 // in chunk_table_kernel) and writes down each token's sequence; copies the
-// initial states where the final ones will be written over them (`keep`: a
-// tile reads an initial state twice, and by the second time the sequence may
-// have ended in another block).
+// initial states where need be (keeps_init).
 __global__ __launch_bounds__(256) void scan_setup_kernel(int N, int T, const int32_t *__restrict__ cu,
                                                          int32_t *__restrict__ meta, int32_t *__restrict__ seq,
                                                          int32_t *__restrict__ ctr, int64_t nctr,
@@ -165,6 +169,10 @@ __device__ __forceinline__ uint64_t get(const uint64_t *p) {
 __device__ __forceinline__ float exp_gate(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+// the same on any element's address (rows of D elements start anywhere)
+typedef uint32_t loose1_t __attribute__((aligned(2)));
+typedef u32x2_t loose2_t __attribute__((aligned(2)));
+typedef u32x4_t loose4_t __attribute__((aligned(2)));
 // Every element is used once: loads and stores that leave no trace in the caches.
 template <typename R>
 __device__ __forceinline__ R stream_load(const char *p) {
@@ -197,11 +205,11 @@ struct Held {
         if constexpr (B == 2)
             w[0] = stream_load<uint16_t>(p);
         else if constexpr (B == 4)
-            w[0] = stream_load<uint32_t>(p);
+            w[0] = stream_load<loose1_t>(p);
         else if constexpr (B == 8)
-            take(stream_load<u32x2_t>(p));
+            take(stream_load<loose2_t>(p));
         else
-            take(stream_load<u32x4_t>(p));
+            take(stream_load<loose4_t>(p));
     }
     template <typename R>
     __device__ __forceinline__ void take(R r) {
@@ -254,11 +262,11 @@ __device__ __forceinline__ void store_vec(T *base, uint32_t off, const T (&v)[V]
     if constexpr (B == 2)
         stream_store(p, __builtin_bit_cast(uint16_t, a));
     else if constexpr (B == 4)
-        stream_store(p, __builtin_bit_cast(uint32_t, a));
+        stream_store<loose1_t>(p, __builtin_bit_cast(uint32_t, a));
     else if constexpr (B == 8)
-        stream_store(p, __builtin_bit_cast(u32x2_t, a));
+        stream_store<loose2_t>(p, __builtin_bit_cast(u32x2_t, a));
     else
-        stream_store(p, __builtin_bit_cast(u32x4_t, a));
+        stream_store<loose4_t>(p, __builtin_bit_cast(u32x4_t, a));
 }
 
 // ---- the chain --------------------------------------------------------------------
@@ -396,9 +404,10 @@ __device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, int
     const int row = (int)quotient(chain, p.ntile), col0 = (int)(chain - (int64_t)row * p.ntile) * kCw;
     const int tid = threadIdx.x, lp = tid % LPR, g = tid / LPR;
     const int t0 = k * kTc, len = min(kTc, p.T - t0);
-    const int ch = col0 + lp * V;
-    const bool live = ch < p.D;                       // V divides D: all of a thread's channels or none
-    const int cc = live ? ch : 0;
+    // a row's last thread ends with the row: the channels that it shares with
+    // the thread before it are computed and written twice, with the same bits
+    const bool live = col0 + lp * V < p.D;
+    const int ch = min(col0 + lp * V, p.D - V);
     const int64_t base = ((int64_t)row * p.T + t0) * p.D;
 
     const int seq = PACKED ? load_seq(p, t0) : 0;
@@ -407,11 +416,15 @@ __device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, int
     if (len > 0) {
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
-            const uint32_t off = (uint32_t)min(g * TT + i, len - 1) * (uint32_t)p.D + (uint32_t)cc;
+            const uint32_t off = (uint32_t)min(g * TT + i, len - 1) * (uint32_t)p.D + (uint32_t)ch;
             lr[i].load(la + base, off);
             xr[i].load(x + base, off);
         }
     }
+    // the state that enters the chain, for one channel of the tile
+    const int wcol = col0 + tid / V * V;
+    const int64_t wch = (int64_t)row * p.D + min(wcol, p.D - V) + tid % V;
+    float edge = !PACKED && init && tid < kCw && wcol < p.D ? init[wch] : 0.f;
     uint32_t starts = 0, ends = 0;
     if constexpr (PACKED) {
         if (tid < kTc + 2) s_seq[tid] = seq;
@@ -453,25 +466,22 @@ __device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, int
         sA[g][lp * V + j] = PACKED && starts ? -0.f : A[j];
         sH[g][lp * V + j] = H[j];
     }
+    // The final state may go where the initial one is: it is here before
+    // anything is published or written.
+    asm volatile("" : "+v"(edge));
     __syncthreads();
     if (tid < kCw) {                                  // one wave, a lane per channel of the tile
         float bA = 1.f, bH = 0.f;
 #pragma unroll
         for (int q = 0; q < G; ++q) join<PACKED>(bA, bH, sA[q][tid], sH[q][tid]);
-        const bool on = col0 + tid < p.D;
-        const int64_t sidx = (int64_t)row * p.D + col0 + tid;
-        float s = !PACKED && init && on ? init[sidx] : 0.f;
-        // the final states may go where the initial ones are: this one is here before anything is published that
-        // lets another block write them
-        asm volatile("" : "+v"(s));
-        s = chain_state<PACKED>(p, chain, k, tid, bA, bH, s);
+        float s = chain_state<PACKED>(p, chain, k, tid, bA, bH, edge);
 #pragma unroll
         for (int q = 0; q < G; ++q) {                 // the state that enters each thread group
             const float H = sH[q][tid];
             sH[q][tid] = s;
             s = apply<PACKED>(sA[q][tid], H, s);
         }
-        if (!PACKED && fin && on && k + 1 >= p.nchunk) fin[sidx] = s;
+        if (!PACKED && fin && wcol < p.D && k + 1 >= p.nchunk) fin[wch] = s;
     }
     __syncthreads();
     if (!live) return;
@@ -524,9 +534,8 @@ __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, int
     const int row = (int)quotient(chain, p.ntile), col0 = (int)(chain - (int64_t)row * p.ntile) * kCw;
     const int tid = threadIdx.x, lp = tid % LPR, g = tid / LPR;
     const int t0 = chunk * kTc, len = min(kTc, p.T - t0);
-    const int ch = col0 + lp * V;
-    const bool live = ch < p.D;
-    const int cc = live ? ch : 0;
+    const bool live = col0 + lp * V < p.D;
+    const int ch = min(col0 + lp * V, p.D - V);
     const int64_t base = ((int64_t)row * p.T + t0) * p.D;
 
     const int seq = PACKED ? load_seq(p, t0) : 0;
@@ -536,7 +545,7 @@ __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, int
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
             const int t = min(g * TT + i, len - 1);
-            const uint32_t off = (uint32_t)t * (uint32_t)p.D + (uint32_t)cc;
+            const uint32_t off = (uint32_t)t * (uint32_t)p.D + (uint32_t)ch;
             lr[i].load(la + base, off);
             gr[i].load(dh + base, off);
         }
@@ -545,9 +554,12 @@ __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, int
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
             const int t = max(min(g * TT + i, len - 1) - back, 0);
-            hr[i].load(h + base - (1 - back) * (int64_t)p.D, (uint32_t)t * (uint32_t)p.D + (uint32_t)cc);
+            hr[i].load(h + base - (1 - back) * (int64_t)p.D, (uint32_t)t * (uint32_t)p.D + (uint32_t)ch);
         }
     }
+    const int wcol = col0 + tid / V * V;
+    const int64_t wch = (int64_t)row * p.D + min(wcol, p.D - V) + tid % V;
+    float edge = !PACKED && dfin && tid < kCw && wcol < p.D ? dfin[wch] : 0.f;
     uint32_t starts = 0, ends = 0;
     if constexpr (PACKED) {
         if (tid < kTc + 2) s_seq[tid] = seq;
@@ -591,24 +603,20 @@ __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, int
         sA[g][lp * V + j] = PACKED && ends ? -0.f : A[j];
         sH[g][lp * V + j] = H[j];
     }
+    asm volatile("" : "+v"(edge));
     __syncthreads();
     if (tid < kCw) {
         float bA = 1.f, bH = 0.f;
 #pragma unroll
         for (int q = G - 1; q >= 0; --q) join<PACKED>(bA, bH, sA[q][tid], sH[q][tid]);
-        const bool on = col0 + tid < p.D;
-        const int64_t sidx = (int64_t)row * p.D + col0 + tid;
-        float s = !PACKED && dfin && on ? dfin[sidx] : 0.f;
-        // (as in the forward pass)
-        asm volatile("" : "+v"(s));
-        s = chain_state<PACKED>(p, chain, k, tid, bA, bH, s);
+        float s = chain_state<PACKED>(p, chain, k, tid, bA, bH, edge);
 #pragma unroll
         for (int q = G - 1; q >= 0; --q) {
             const float H = sH[q][tid];
             sH[q][tid] = s;
             s = apply<PACKED>(sA[q][tid], H, s);
         }
-        if (!PACKED && dinit && on && chunk == 0) dinit[sidx] = s;
+        if (!PACKED && dinit && wcol < p.D && chunk == 0) dinit[wch] = s;
     }
     __syncthreads();
     if (!live) return;
@@ -677,12 +685,12 @@ static hipError_t scan_setup(const ScanArgs &a, Chain &c, const float *&init, hi
     c.nchain = w.rows * w.tiles;
     c.blocks = (w.chunks > 0 ? w.chunks : 1) * c.nchain;
     init = a.init_state;
-    if (w.chunks <= 1 && !packed) return hipSuccess;
     float *keep = reinterpret_cast<float *>(ws + w.off_init);
-    const bool over = packed && init && init == a.final_state;
+    const bool over = keeps_init(packed, a.D) && init && init == a.final_state;
     if (over) init = keep;
+    if (w.chunks <= 1 && !packed && !over) return hipSuccess;
     const int64_t words16 = (int64_t)(w.total - w.off_agg) / 16;
-    const int64_t other = over ? std::max<int64_t>(a.T, (int64_t)a.N * a.D) : packed ? a.T : 0;
+    const int64_t other = std::max<int64_t>(over ? (int64_t)a.N * a.D : 0, packed ? a.T : 0);
     const int64_t work = std::max(words16, other);
     int64_t blocks = (work + 255) / 256;
     blocks = blocks < 1 ? 1 : (blocks > 2048 ? 2048 : blocks);
@@ -695,8 +703,8 @@ static hipError_t scan_setup(const ScanArgs &a, Chain &c, const float *&init, hi
     return hipGetLastError();
 }
 
-// Loads of 4 channels where every row starts on one (D a multiple of 4), of
-// one otherwise.
+// Loads of 4 channels, of one where there are fewer.  Rows start on any
+// element: the vectors need no alignment beyond the element's.
 template <typename F>
 static hipError_t with_shape(const ScanArgs &a, F f) {
     using std::integral_constant;
@@ -704,7 +712,7 @@ static hipError_t with_shape(const ScanArgs &a, F f) {
     auto vec = [&](auto v) {
         return packed ? f(v, integral_constant<bool, true>{}) : f(v, integral_constant<bool, false>{});
     };
-    return a.D % 4 == 0 ? vec(integral_constant<int, 4>{}) : vec(integral_constant<int, 1>{});
+    return a.D >= 4 ? vec(integral_constant<int, 4>{}) : vec(integral_constant<int, 1>{});
 }
 
 hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st) {
@@ -753,28 +761,48 @@ hipError_t launch_scan_bwd(const ScanArgs &a, hipStream_t st) {
 
 // ---- single step -----------------------------------------------------------------
 
+// Four elements a thread (the arrays are dense and 16-byte aligned).  At 256 x
+// 2048 the call is bound by its launch.
 template <typename x_t, typename l_t, typename h_t>
 __global__ __launch_bounds__(256) void scan_step_kernel(int64_t n, float *__restrict__ state,
                                                         const x_t *__restrict__ x, const l_t *__restrict__ la,
                                                         h_t *__restrict__ h) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const float s = fmaf(exp_gate(to_f32(la[i])), state[i], to_f32(x[i]));
-        state[i] = s;
-        h[i] = round_to<h_t>(s);
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
+        if (i + 4 <= n) {
+            Held<x_t, 4> xr;
+            Held<l_t, 4> lr;
+            lr.load(la + i, 0);
+            xr.load(x + i, 0);
+            float4_t s = *reinterpret_cast<const float4_t *>(state + i);
+            h_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[j] = fmaf(exp_gate(lr.get(j)), s[j], xr.get(j));
+                o[j] = round_to<h_t>(s[j]);
+            }
+            *reinterpret_cast<float4_t *>(state + i) = s;
+            store_vec<h_t, 4>(h + i, 0, o);
+        } else {
+            for (int64_t e = i; e < n; ++e) {
+                const float s = fmaf(exp_gate(to_f32(la[e])), state[e], to_f32(x[e]));
+                state[e] = s;
+                h[e] = round_to<h_t>(s);
+            }
+        }
     }
 }
 
 hipError_t launch_scan_step(const ScanStepArgs &a, hipStream_t st) {
     const int64_t n = (int64_t)a.N * a.D;
-    const int64_t blocks = (n + 255) / 256;
+    const unsigned blocks = (unsigned)std::min<int64_t>(scan_tiles(n, 1024), 1 << 20);
     ProfScope prof("gdn_scan_step", st);
     return with_types(a.in_dtype, a.gate_dtype, a.out_dtype, [&](auto x, auto l, auto h) {
         using x_t = decltype(x);
         using l_t = decltype(l);
         using h_t = decltype(h);
-        scan_step_kernel<x_t, l_t, h_t><<<(unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)), 256, 0, st>>>(
-            n, a.state, static_cast<const x_t *>(a.x), static_cast<const l_t *>(a.log_alpha),
-            static_cast<h_t *>(a.h));
+        scan_step_kernel<x_t, l_t, h_t><<<blocks, 256, 0, st>>>(n, a.state, static_cast<const x_t *>(a.x),
+                                                                static_cast<const l_t *>(a.log_alpha),
+                                                                static_cast<h_t *>(a.h));
         return hipGetLastError();
     });
 }
