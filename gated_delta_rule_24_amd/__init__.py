@@ -23,6 +23,7 @@ linear recurrence, layer norm, and moves of resident states.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -391,10 +392,16 @@ def _workspace(workspace, size, device):
 
 def scan_workspace_size(B, T, D, num_seqs, in_dtype=torch.bfloat16, gate_dtype=torch.float32,
                         out_dtype=torch.float32) -> int:
-    d = ScanDesc(B, T, D, num_seqs, _DT[in_dtype], _DT[gate_dtype], _DT[out_dtype], 0)
+    return _scan_desc(B, T, D, num_seqs, in_dtype, gate_dtype, out_dtype)[1]
+
+
+@functools.lru_cache(maxsize=256)
+def _scan_desc(B, T, D, N, in_dtype, gate_dtype, out_dtype):
+    """Descriptor of these sizes and types, and its workspace size."""
+    d = ScanDesc(B, T, D, N, _DT[in_dtype], _DT[gate_dtype], _DT[out_dtype], 0)
     n = ctypes.c_size_t(0)
     _check(load().gdn_scan_workspace_size(ctypes.byref(d), ctypes.byref(n)))
-    return int(n.value)
+    return d, int(n.value)
 
 
 def _scan_call(B, T, D, in_dtype, gate_dtype, out_dtype, cu_seqlens, workspace, device):
@@ -404,10 +411,8 @@ def _scan_call(B, T, D, in_dtype, gate_dtype, out_dtype, cu_seqlens, workspace, 
     else:
         _need(cu_seqlens, "cu_seqlens", (torch.int32,), device, 1)
         N = cu_seqlens.shape[0] - 1
-    desc = ScanDesc(B, T, D, N, _DT[in_dtype], _DT[gate_dtype], _DT[out_dtype], 0)
-    need = ctypes.c_size_t(0)
-    _check(load().gdn_scan_workspace_size(ctypes.byref(desc), ctypes.byref(need)))
-    return desc, N, *_workspace(workspace, need.value, device)
+    desc, need = _scan_desc(B, T, D, N, in_dtype, gate_dtype, out_dtype)
+    return desc, N, *_workspace(workspace, need, device)
 
 
 def scan_fwd(x, log_alpha, init_state=None, cu_seqlens=None, *, out_dtype=torch.float32, h=None, final_state=True,
@@ -513,6 +518,7 @@ def layernorm_fwd(x, weight=None, bias=None, *, eps=1e-5, out_dtype=torch.float3
     return y, mean, rstd
 
 
+@functools.lru_cache(maxsize=256)
 def layernorm_bwd_workspace_size(rows, dim) -> int:
     n = ctypes.c_size_t(0)
     _check(load().gdn_layernorm_bwd_workspace_size(rows, dim, ctypes.byref(n)))

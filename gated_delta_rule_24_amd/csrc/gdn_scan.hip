@@ -46,17 +46,10 @@
 
 namespace gdn {
 
-#ifndef CW
-#define CW 128
-#define NTH 512
-#define EL 32
-#define WV 4
-#define NTL 1
-#endif
-constexpr int kCw = CW;         // channels of a tile
-constexpr int kNt = NTH;        // threads of a block
-constexpr int kElems = EL;      // elements per thread
-constexpr int kTc = kNt * kElems / kCw;   // tokens of a tile
+constexpr int kCw = 128;        // channels of a tile
+constexpr int kNt = 512;        // threads of a block
+constexpr int kElems = 32;      // elements per thread
+constexpr int kTc = kNt * kElems / kCw;   // tokens of a tile: 128
 constexpr int kGroup = 8;       // tiles per group of a chain, and groups per section
 constexpr uint64_t kEmpty = ~0ull;
 constexpr int64_t kMaxGridX = 1 << 20;
@@ -176,19 +169,11 @@ typedef u32x4_t loose4_t __attribute__((aligned(2)));
 // Every element is used once: loads and stores that leave no trace in the caches.
 template <typename R>
 __device__ __forceinline__ R stream_load(const char *p) {
-#if NTL & 1
     return __builtin_nontemporal_load(reinterpret_cast<const R *>(p));
-#else
-    return *reinterpret_cast<const R *>(p);
-#endif
 }
 template <typename R>
 __device__ __forceinline__ void stream_store(char *p, R r) {
-#if NTL & 2
     __builtin_nontemporal_store(r, reinterpret_cast<R *>(p));
-#else
-    *reinterpret_cast<R *>(p) = r;
-#endif
 }
 
 // V consecutive elements as loaded (16-bit types two to a register).  Values
@@ -510,7 +495,7 @@ __device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, int
 }
 
 template <typename x_t, typename l_t, typename h_t, int V, bool PACKED>
-__global__ __launch_bounds__(kNt, WV) void scan_fwd_kernel(Chain p, const x_t *__restrict__ x,
+__global__ __launch_bounds__(kNt, 4) void scan_fwd_kernel(Chain p, const x_t *__restrict__ x,
                                                                const l_t *__restrict__ la, const float *init,
                                                                float *fin, h_t *__restrict__ h) {
     if (PACKED && p.meta[1] != 0) return;
@@ -654,7 +639,7 @@ __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, int
 }
 
 template <typename x_t, typename l_t, typename h_t, int V, bool PACKED>
-__global__ __launch_bounds__(kNt, WV) void scan_bwd_kernel(Chain p, const l_t *__restrict__ la,
+__global__ __launch_bounds__(kNt, 4) void scan_bwd_kernel(Chain p, const l_t *__restrict__ la,
                                                                const h_t *__restrict__ h,
                                                                const float *__restrict__ init,
                                                                const h_t *__restrict__ dh,
