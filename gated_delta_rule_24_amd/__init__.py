@@ -350,6 +350,12 @@ def decode_step(state, q, k, v, log_alpha, beta, *, out_dtype=torch.float32, o=N
 _FLOATS = tuple(_DT)
 
 
+def _code(dtype):
+    if dtype not in _DT:
+        raise ValueError(f"dtype {dtype} is not one of {_FLOATS}")
+    return _DT[dtype]
+
+
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -398,7 +404,7 @@ def scan_workspace_size(B, T, D, num_seqs, in_dtype=torch.bfloat16, gate_dtype=t
 @functools.lru_cache(maxsize=256)
 def _scan_desc(B, T, D, N, in_dtype, gate_dtype, out_dtype):
     """Descriptor of these sizes and types, and its workspace size."""
-    d = ScanDesc(B, T, D, N, _DT[in_dtype], _DT[gate_dtype], _DT[out_dtype], 0)
+    d = ScanDesc(B, T, D, N, _code(in_dtype), _code(gate_dtype), _code(out_dtype), 0)
     n = ctypes.c_size_t(0)
     _check(load().gdn_scan_workspace_size(ctypes.byref(d), ctypes.byref(n)))
     return d, int(n.value)
@@ -485,7 +491,7 @@ def scan_step(state, x, log_alpha, *, out_dtype=torch.float32, h=None):
         h = torch.empty(shape, dtype=out_dtype, device=dev)
     else:
         _shaped(h, "h", shape, _FLOATS, dev)
-    _call("gdn_scan_step", dev, *shape, _DT[x.dtype], _DT[log_alpha.dtype], _DT[h.dtype], _addr(state), _addr(x),
+    _call("gdn_scan_step", dev, *shape, _DT[x.dtype], _DT[log_alpha.dtype], _code(h.dtype), _addr(state), _addr(x),
           _addr(log_alpha), _addr(h))
     return h
 
@@ -513,7 +519,7 @@ def layernorm_fwd(x, weight=None, bias=None, *, eps=1e-5, out_dtype=torch.float3
     mean = rstd = None
     if stats:
         mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) for _ in range(2))
-    _call("gdn_layernorm_fwd", dev, rows, D, _DT[x.dtype], _DT[y.dtype], eps, _addr(x), _addr(weight), _addr(bias),
+    _call("gdn_layernorm_fwd", dev, rows, D, _DT[x.dtype], _code(y.dtype), eps, _addr(x), _addr(weight), _addr(bias),
           _addr(y), _addr(mean), _addr(rstd))
     return y, mean, rstd
 

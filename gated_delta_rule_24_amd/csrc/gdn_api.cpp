@@ -345,7 +345,7 @@ gdn_status gdn_chunk_fwd_check(const void *workspace, hipStream_t stream, int32_
     e = hipMemcpy(meta, workspace, sizeof(meta), hipMemcpyDeviceToHost);
     if (e != hipSuccess) return hip_fail(e, "hipMemcpy");
     *code = meta[1];
-    if (meta[1] != 0) return fail(GDN_ERR_DEVICE_INPUT, "cu_seqlens rejected on the device (code %d)", meta[1]);
+    if (meta[1] != 0) return fail(GDN_ERR_DEVICE_INPUT, "cu_seqlens or indices rejected on the device (code %d)", meta[1]);
     return ok();
 }
 

@@ -27,7 +27,7 @@ struct ScanArgs {
 // Workspace carve-up of one scan call (byte offsets).
 struct ScanWorkspace {
     int64_t rows, chunks, tiles;   // chains = rows * tiles of channels, chunks = tiles of tokens per chain
-    size_t off_seq, off_init, off_ctr, off_agg, off_grp, off_pre;
+    size_t off_seq, off_init, off_agg, off_grp, off_pre;
     size_t total;
 };
 ScanWorkspace scan_workspace_layout(int32_t B, int32_t T, int32_t D, int32_t N, bool packed);

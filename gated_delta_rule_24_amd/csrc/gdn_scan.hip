@@ -4,30 +4,43 @@
 //
 // Sequences in one pass.  Tokens compose as affine maps h -> A h + H:
 //   (A1, H1) then (A2, H2)  =  (A1 A2, A2 H1 + H2).
-// A block takes a tile of kTc tokens x 64 channels, reads it once into
+// A block takes a tile of 128 tokens x 128 channels, reads it once into
 // registers, forms its threads' maps, joins them in LDS, gets the state that
 // enters the tile, runs the recurrence from the registers and writes the
 // result: every tensor crosses HBM once, whatever the length.  The state that
 // enters a tile comes from the tiles before it in the same chain (batch row
-// and channel tile):
-//   - each tile publishes its own map (agg) as soon as it has it;
-//   - a chain's tiles form groups of kGroup; the last tile of a group
-//     publishes the state that leaves the group (pre);
-//   - a tile takes the state that enters its group and applies the maps of
-//     the tiles before it in the group, in order.  The order of every sum is
-//     fixed, so equal calls give equal bits, and only one hand-over per
-//     kGroup tiles is serial.
+// and channel tile).  A chain's tiles form groups of kGroup, its groups
+// sections of kGroup:
+//   - a tile publishes its own map (agg) as soon as it has it;
+//   - the last tile of a group publishes the group's map (grp), the last of a
+//     section the state that leaves it (pre);
+//   - a tile joins the maps of the groups before its own in the section and
+//     of the tiles before it in the group, in order, and applies them to the
+//     state that entered the section.
+// The order of every sum is fixed, so equal calls give equal bits, and only
+// one hand-over per 64 tiles is serial.
 // Every published value is one 8-byte word, written and read by relaxed
 // device-scope atomics, so a word is whole or not there: scan_setup_kernel
 // fills the words with kEmpty, which no published word equals (not-a-number
 // is published in one form).  No fence is needed, as nothing but the word
 // itself is handed over.
-// Every wait ends: a block draws its place in its chain from the chain's
-// counter when it turns to a tile, so it waits only for tiles that were begun
-// before its own, and the first of a chain waits for none.  Should two calls
-// run on one workspace at once, against the contract, a wait gives up after
-// kPatience looks (about a second; a wait in earnest takes microseconds): the
-// state is then not-a-number and the workspace's code 4.
+// Every wait ends, in whatever order the blocks run: tiles are given to blocks
+// in the order of their chain, so the tiles before a block's own have as a
+// rule begun before it; but a block that has looked `patience` times for
+// words (about 4 ms) waits no longer and works out the maps of all tiles before
+// its own itself, in the same order of sums.
+//
+// Measured (MI355X, a large copy reaches 5.4 TB/s): 4 x 4096 x 2048 from bf16
+// with fp32 gates 55 us (4.9 TB/s), its gradient 91 us (5.2), 32768 x 4096 in
+// fp16 backward 247 us (5.4), 50408 packed tokens x 2048 in bf16 135 us (4.6).
+// Tiles are 256 bytes a row because a plain copy in tiles of 128 tokens runs at
+// 4.9 TB/s with rows of 128 bytes, 5.5 with 256, 6.0 with 512; 256 channels in
+// blocks of 512 threads leave 64 tokens a tile and twice the words (prefill 59
+// us).  Loads and stores that pass the caches by save 7%.  What is left is a
+// block's life: one load latency and one or two hand-overs per tile with three
+// (16-bit operands) or two blocks a CU to cover them.  Drawing a tile's place
+// from a counter instead costs 2-7%; keeping blocks on their CUs with the next
+// tile's loads in flight leaves the words too late (75 us for prefill).
 //
 // The gradient is the same recurrence backwards in e_t = alpha_t g_t,
 //   g_t = dh_t + e_{t+1},  e_t = alpha_t g_t,
@@ -42,7 +55,13 @@
 #include "gdn_ops.h"
 #include "gdn_types.h"
 
+#include <stdlib.h>
+
 #include <algorithm>
+
+// Products and sums are fused only where fmaf says so: the same recurrence is
+// written in unrolled and in plain loops, whose bits have to agree.
+#pragma clang fp contract(off)
 
 namespace gdn {
 
@@ -53,15 +72,15 @@ constexpr int kTc = kNt * kElems / kCw;   // tokens of a tile: 128
 constexpr int kGroup = 8;       // tiles per group of a chain, and groups per section
 constexpr uint64_t kEmpty = ~0ull;
 constexpr int64_t kMaxGridX = 1 << 20;
-constexpr int kPatience = 1 << 20;
+constexpr int kPatience = 4096; // looks at a word before a block helps itself
 
 static int64_t scan_tiles(int64_t n, int64_t w) { return (n + w - 1) / w; }
 
 // Whether final states over the initial ones make the kernels read a copy:
-// a packed tile reads an initial state twice, and by the second time the
-// sequence may have ended in another block; where D is no multiple of 4 two
-// blocks read the channels that they share.
-static bool keeps_init(bool packed, int32_t D) { return packed || D % 4 != 0; }
+// initial states are read by more than one block, or twice, and the sequence
+// may have ended in another block by then.  Only single tiles of whole vectors
+// are safe.
+static bool keeps_init(bool packed, int32_t D, int64_t chunks) { return packed || D % 4 != 0 || chunks > 1; }
 
 ScanWorkspace scan_workspace_layout(int32_t B, int32_t T, int32_t D, int32_t N, bool packed) {
     ScanWorkspace w;
@@ -75,9 +94,7 @@ ScanWorkspace scan_workspace_layout(int32_t B, int32_t T, int32_t D, int32_t N, 
     w.off_seq = at;
     at += packed ? up((size_t)T * 4) : 0;
     w.off_init = at;
-    at += keeps_init(packed, D) ? up((size_t)N * D * 4) : 0;
-    w.off_ctr = at;
-    at += chained ? up((size_t)w.rows * w.tiles * 4) : 0;
+    at += keeps_init(packed, D, w.chunks) ? up((size_t)N * D * 4) : 0;
     w.off_agg = at;
     at += up((size_t)words * w.chunks * 8);
     w.off_grp = at;
@@ -88,18 +105,16 @@ ScanWorkspace scan_workspace_layout(int32_t B, int32_t T, int32_t D, int32_t N, 
     return w;
 }
 
-// Empties the words, zeroes the counters; packed: checks cu_seqlens (codes as
+// Empties the words; packed: checks cu_seqlens (codes as
 // in chunk_table_kernel) and writes down each token's sequence; copies the
 // initial states where need be (keeps_init).
 __global__ __launch_bounds__(256) void scan_setup_kernel(int N, int T, const int32_t *__restrict__ cu,
                                                          int32_t *__restrict__ meta, int32_t *__restrict__ seq,
-                                                         int32_t *__restrict__ ctr, int64_t nctr,
                                                          u32x4_t *__restrict__ words, int64_t nwords16,
                                                          const float *__restrict__ init, float *__restrict__ keep,
                                                          int64_t nkeep) {
     const int64_t tid = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
     for (int64_t i = tid; i < nwords16; i += all) words[i] = u32x4_t{~0u, ~0u, ~0u, ~0u};
-    for (int64_t i = tid; i < nctr; i += all) ctr[i] = 0;
     for (int64_t i = tid; i < nkeep; i += all) keep[i] = init[i];
     if (!cu) return;
     for (int64_t t = tid; t < T; t += all) {
@@ -262,18 +277,18 @@ struct Chain {
     const int32_t *cu;
     int32_t *meta;
     const int32_t *seq;
-    int32_t *ctr;
+    int patience;
     uint64_t *agg, *grp, *pre;
 };
 
 // The state entering tile `k` (its place in the chain) for column `c`, from
-// the tile's own map: waits for the tiles before it and publishes what the
-// tiles after it need.  Returns the state that enters; `first` is the state
-// that enters the chain.
-template <bool PACKED>
+// the tile's own map (A, H).  Publishes what the tiles after it need and waits
+// for the tiles before it; where a word does not come, map(j, A, H) works out
+// the map of tile j.  `first` is the state that enters the chain.
+template <bool PACKED, typename F>
 __device__ __forceinline__ float chain_state(const Chain &p, int64_t chain, int k, int c, float A, float H,
-                                             float first) {
-    if (p.nchunk == 1) return first;
+                                             float first, F map) {
+    if (p.nchunk <= 1) return first;
     constexpr int kG = kGroup;
     const int s = k % kG, r = k / kG % kG, R = k / (kG * kG);
     uint64_t *agg = p.agg + (chain * p.nchunk + (k - s)) * kCw + c;
@@ -281,14 +296,12 @@ __device__ __forceinline__ float chain_state(const Chain &p, int64_t chain, int 
     uint64_t *pre = p.pre + (chain * ((p.nchunk + kG * kG - 1) / (kG * kG)) + R) * kCw + c;
     const bool more = k + 1 < p.nchunk;
     if (more && s < kG - 1) put(agg + s * kCw, word(A, H));
-    // Look at the words of a kind once, then wait for each that is not there
-    // yet.
-    uint64_t w[kG - 1];
     int looks = 0;
+    bool late = false;
     auto wait = [&](uint64_t &v, const uint64_t *at) {
-        while (__any(v == kEmpty)) {
-            if (++looks > kPatience) {     // kEmpty's halves are not-a-number
-                p.meta[1] = 4;
+        while (!late && __any(v == kEmpty)) {
+            if (++looks > p.patience) {
+                late = true;
                 break;
             }
             __builtin_amdgcn_s_sleep(2);
@@ -297,7 +310,10 @@ __device__ __forceinline__ float chain_state(const Chain &p, int64_t chain, int 
     };
     auto upper = [](uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); };
     auto lower = [](uint64_t v) { return __uint_as_float((uint32_t)v); };
+    // Look at the words of a kind once, then wait for each that is not there
+    // yet.
     auto join_words = [&](float &mA, float &mH, const uint64_t *at, int n) {
+        uint64_t w[kG - 1];
 #pragma unroll
         for (int j = 0; j < kG - 1; ++j) w[j] = j < n ? get(at + j * kCw) : 0;
 #pragma unroll
@@ -307,22 +323,45 @@ __device__ __forceinline__ float chain_state(const Chain &p, int64_t chain, int 
                 join<PACKED>(mA, mH, upper(w[j]), lower(w[j]));
             }
     };
-    float gA = 1.f, gH = 0.f;
-    join_words(gA, gH, agg, s);
-    if (more && s == kG - 1 && r < kG - 1) {
+    // joined: the tiles before this one in its group, the groups before that
+    // in its section; in: the state that enters the section
+    float gA = 1.f, gH = 0.f, sA = 1.f, sH = 0.f, in = first;
+    auto publish_group = [&] {
         float lA = gA, lH = gH;
         join<PACKED>(lA, lH, A, H);
-        put(grp + r * kCw, word(lA, lH));
+        if (more && s == kG - 1 && r < kG - 1) put(grp + r * kCw, word(lA, lH));
+    };
+    join_words(gA, gH, agg, s);
+    if (!late) {
+        publish_group();
+        join_words(sA, sH, grp, r);
+        if (R > 0) {
+            uint64_t u = get(pre);
+            wait(u, pre);
+            in = lower(u);
+        }
     }
-    float sA = 1.f, sH = 0.f;
-    join_words(sA, sH, grp, r);
+    if (late) {
+        gA = sA = 1.f, gH = sH = 0.f, in = first;
+        for (int j = 0; j < k; ++j) {
+            float tA, tH, eA = sA, eH = sH;
+            map(j, tA, tH);
+            join<PACKED>(eA, eH, gA, gH);
+            const float out = apply<PACKED>(tA, tH, apply<PACKED>(eA, eH, in));
+            join<PACKED>(gA, gH, tA, tH);
+            if (j % kG == kG - 1) {
+                if (j / kG % kG == kG - 1) {
+                    in = out;
+                    sA = 1.f, sH = 0.f;
+                } else {
+                    join<PACKED>(sA, sH, gA, gH);
+                }
+                gA = 1.f, gH = 0.f;
+            }
+        }
+        publish_group();
+    }
     join<PACKED>(sA, sH, gA, gH);
-    float in = first;
-    if (R > 0) {
-        uint64_t u = get(pre);
-        wait(u, pre);
-        in = lower(u);
-    }
     in = apply<PACKED>(sA, sH, in);
     if (more && s == kG - 1 && r == kG - 1) put(pre + kCw, word(0.f, apply<PACKED>(A, H, in)));
     return in;
@@ -335,18 +374,21 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 __device__ __forceinline__ int64_t modulo(int64_t a, int64_t b) { return a - quotient(a, b) * b; }
 
 // This block's chain and its place there; false past the last tile.
-__device__ __forceinline__ bool draw_tile(const Chain &p, int64_t &chain, int &k) {
-    __shared__ int s_k;
+__device__ __forceinline__ bool take_tile(const Chain &p, int64_t &chain, int &k) {
     const int64_t b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     if (b >= p.blocks) return false;
-    chain = modulo(b, p.nchain);
-    k = 0;
-    if (p.nchunk > 1) {
-        if (threadIdx.x == 0) s_k = atomicAdd(&p.ctr[chain], 1);
-        __syncthreads();
-        k = __builtin_amdgcn_readfirstlane(s_k);
-    }
+    k = (int)quotient(b, p.nchain);
+    chain = b - k * p.nchain;
     return true;
+}
+
+// Waves per SIMD that a kernel's registers should leave room for.  A thread's
+// operands take kElems / 4 times (registers for 4 values) each; with three
+// blocks a CU instead of two, packed 16-bit calls take 135 us instead of 145.
+template <int V, typename... T>
+constexpr int min_waves() {
+    const int held = kElems / V * (... + Held<T, V>::W);
+    return held <= 32 ? 6 : 4;
 }
 
 // Bit i: token t0 + i of the thread's TT tokens is the first (last) of its
@@ -455,11 +497,33 @@ __device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, int
     // anything is published or written.
     asm volatile("" : "+v"(edge));
     __syncthreads();
-    if (tid < kCw) {                                  // one wave, a lane per channel of the tile
+    if (tid < kCw) {                                  // the first waves, a lane per channel of the tile
         float bA = 1.f, bH = 0.f;
 #pragma unroll
         for (int q = 0; q < G; ++q) join<PACKED>(bA, bH, sA[q][tid], sH[q][tid]);
-        float s = chain_state<PACKED>(p, chain, k, tid, bA, bH, edge);
+        // a tile before this one, token by token
+        auto map = [&](int tile, float &tA, float &tH) {
+            const int64_t at = (int64_t)row * p.T + (int64_t)tile * kTc;
+            const int c = (int)(wch - (int64_t)row * p.D);
+            tA = 1.f, tH = 0.f;
+#pragma nounroll
+            for (int q = 0; q < G; ++q) {
+                float mA = 1.f, mH = 0.f;
+                bool forget = false;
+#pragma nounroll
+                for (int64_t t = at + q * TT; t < at + (q + 1) * TT; ++t) {
+                    if (PACKED && (t == 0 || p.seq[t - 1] != p.seq[t])) {
+                        mH = init ? init[(int64_t)p.seq[t] * p.D + c] : 0.f;
+                        forget = true;
+                    }
+                    const float a = exp_gate(to_f32(la[t * p.D + c]));
+                    mH = fmaf(a, mH, to_f32(x[t * p.D + c]));
+                    mA *= a;
+                }
+                join<PACKED>(tA, tH, PACKED && forget ? -0.f : mA, mH);
+            }
+        };
+        float s = chain_state<PACKED>(p, chain, k, tid, bA, bH, edge, map);
 #pragma unroll
         for (int q = 0; q < G; ++q) {                 // the state that enters each thread group
             const float H = sH[q][tid];
@@ -495,14 +559,14 @@ __device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, int
 }
 
 template <typename x_t, typename l_t, typename h_t, int V, bool PACKED>
-__global__ __launch_bounds__(kNt, 4) void scan_fwd_kernel(Chain p, const x_t *__restrict__ x,
+__global__ __launch_bounds__(kNt, (min_waves<V, x_t, l_t>())) void scan_fwd_kernel(Chain p, const x_t *__restrict__ x,
                                                                const l_t *__restrict__ la, const float *init,
                                                                float *fin, h_t *__restrict__ h) {
     if (PACKED && p.meta[1] != 0) return;
     if (!PACKED && blockIdx.x + blockIdx.y == 0 && threadIdx.x == 0) p.meta[0] = p.meta[1] = 0;
     int64_t chain;
     int k;
-    if (draw_tile(p, chain, k)) scan_fwd_tile<x_t, l_t, h_t, V, PACKED>(p, chain, k, x, la, init, fin, h);
+    if (take_tile(p, chain, k)) scan_fwd_tile<x_t, l_t, h_t, V, PACKED>(p, chain, k, x, la, init, fin, h);
     if constexpr (PACKED) hand_on(p, init, fin);
 }
 
@@ -594,7 +658,30 @@ __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, int
         float bA = 1.f, bH = 0.f;
 #pragma unroll
         for (int q = G - 1; q >= 0; --q) join<PACKED>(bA, bH, sA[q][tid], sH[q][tid]);
-        float s = chain_state<PACKED>(p, chain, k, tid, bA, bH, edge);
+        // a tile after this one, token by token
+        auto map = [&](int tile, float &tA, float &tH) {
+            const int from = (p.nchunk - 1 - tile) * kTc, to = min(from + kTc, p.T);
+            const int c = (int)(wch - (int64_t)row * p.D);
+            tA = 1.f, tH = 0.f;
+#pragma nounroll
+            for (int q = G - 1; q >= 0; --q) {
+                float mA = 1.f, mH = 0.f;
+                bool forget = false;
+#pragma nounroll
+                for (int i = min(from + (q + 1) * TT, to) - 1; i >= from + q * TT; --i) {
+                    const int64_t t = (int64_t)row * p.T + i;
+                    if (PACKED && (i == p.T - 1 || p.seq[i + 1] != p.seq[i])) {
+                        mH = dfin ? dfin[(int64_t)p.seq[i] * p.D + c] : 0.f;
+                        forget = true;
+                    }
+                    const float a = exp_gate(to_f32(la[t * p.D + c]));
+                    mH = a * (to_f32(dh[t * p.D + c]) + mH);
+                    mA *= a;
+                }
+                join<PACKED>(tA, tH, PACKED && forget ? -0.f : mA, mH);
+            }
+        };
+        float s = chain_state<PACKED>(p, chain, k, tid, bA, bH, edge, map);
 #pragma unroll
         for (int q = G - 1; q >= 0; --q) {
             const float H = sH[q][tid];
@@ -639,7 +726,7 @@ __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, int
 }
 
 template <typename x_t, typename l_t, typename h_t, int V, bool PACKED>
-__global__ __launch_bounds__(kNt, 4) void scan_bwd_kernel(Chain p, const l_t *__restrict__ la,
+__global__ __launch_bounds__(kNt, (min_waves<V, l_t, h_t, h_t>())) void scan_bwd_kernel(Chain p, const l_t *__restrict__ la,
                                                                const h_t *__restrict__ h,
                                                                const float *__restrict__ init,
                                                                const h_t *__restrict__ dh,
@@ -649,8 +736,13 @@ __global__ __launch_bounds__(kNt, 4) void scan_bwd_kernel(Chain p, const l_t *__
     if (!PACKED && blockIdx.x + blockIdx.y == 0 && threadIdx.x == 0) p.meta[0] = p.meta[1] = 0;
     int64_t chain;
     int k;
-    if (draw_tile(p, chain, k)) scan_bwd_tile<x_t, l_t, h_t, V, PACKED>(p, chain, k, la, h, init, dh, dfin, dx, dla, dinit);
+    if (take_tile(p, chain, k)) scan_bwd_tile<x_t, l_t, h_t, V, PACKED>(p, chain, k, la, h, init, dh, dfin, dx, dla, dinit);
     if constexpr (PACKED) hand_on(p, dfin, dinit);
+}
+
+static int scan_patience() {
+    const char *s = getenv("GDN_SCAN_PATIENCE");
+    return s && *s ? std::max(atoi(s), 0) : kPatience;
 }
 
 // Fills `c` and enqueues the setup kernel where the call needs one.
@@ -663,7 +755,7 @@ static hipError_t scan_setup(const ScanArgs &a, Chain &c, const float *&init, hi
     c.cu = a.cu_seqlens;
     c.meta = reinterpret_cast<int32_t *>(ws);
     c.seq = reinterpret_cast<int32_t *>(ws + w.off_seq);
-    c.ctr = reinterpret_cast<int32_t *>(ws + w.off_ctr);
+    c.patience = scan_patience();
     c.agg = reinterpret_cast<uint64_t *>(ws + w.off_agg);
     c.grp = reinterpret_cast<uint64_t *>(ws + w.off_grp);
     c.pre = reinterpret_cast<uint64_t *>(ws + w.off_pre);
@@ -671,7 +763,7 @@ static hipError_t scan_setup(const ScanArgs &a, Chain &c, const float *&init, hi
     c.blocks = (w.chunks > 0 ? w.chunks : 1) * c.nchain;
     init = a.init_state;
     float *keep = reinterpret_cast<float *>(ws + w.off_init);
-    const bool over = keeps_init(packed, a.D) && init && init == a.final_state;
+    const bool over = keeps_init(packed, a.D, w.chunks) && init && init == a.final_state;
     if (over) init = keep;
     if (w.chunks <= 1 && !packed && !over) return hipSuccess;
     const int64_t words16 = (int64_t)(w.total - w.off_agg) / 16;
@@ -681,8 +773,7 @@ static hipError_t scan_setup(const ScanArgs &a, Chain &c, const float *&init, hi
     blocks = blocks < 1 ? 1 : (blocks > 2048 ? 2048 : blocks);
     ProfScope prof("gdn_scan_setup", st);
     scan_setup_kernel<<<(unsigned)blocks, 256, 0, st>>>(a.N, a.T, a.cu_seqlens, c.meta,
-                                                        reinterpret_cast<int32_t *>(ws + w.off_seq), c.ctr,
-                                                        w.chunks > 1 ? c.nchain : 0,
+                                                        reinterpret_cast<int32_t *>(ws + w.off_seq),
                                                         reinterpret_cast<u32x4_t *>(ws + w.off_agg), words16,
                                                         a.init_state, keep, over ? (int64_t)a.N * a.D : 0);
     return hipGetLastError();

@@ -411,7 +411,11 @@ gdn_status gdn_scan_workspace_size(const gdn_scan_desc *desc, size_t *bytes);
  *                           pointer as init_state (in-place continuation),
  *                           not a partial overlap.
  * Nothing of one sequence reaches another, not-a-number and infinite values
- * included.  Equal calls give equal bits.
+ * included.  Equal calls give equal bits.  Long sequences are cut into tiles
+ * whose blocks hand states on through the workspace; the environment variable
+ * GDN_SCAN_PATIENCE, read at every call, sets how often a block looks for
+ * another's word before it works the state out itself, with the same bits
+ * (default 4096, about 4 ms; 0 makes every block do so where it can).
  * x, log_alpha, h, the states and the workspace must be 16-byte aligned.
  * h, final_state and the workspace must not overlap anything else
  * (GDN_ERR_ALIAS).

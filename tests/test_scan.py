@@ -251,6 +251,24 @@ def test_malformed_offsets_write_nothing(cu, code):
     assert gdn.chunk_fwd_check(ws) == code
 
 
+@pytest.mark.parametrize("types", [("bf16", "bf16", "bf16"), ("bf16", "fp32", "fp32")])
+@pytest.mark.parametrize("D", [3, 40, 130])
+def test_blocks_that_wait_for_none(monkeypatch, D, types):
+    """Without patience the blocks work out the states before their tiles themselves: the same bits, over more
+    than a section of tiles (64 x 128 tokens), in one sequence, packed and in place."""
+    T = 128 * 70 + 5
+    for cu in (None, [0, 100, 100, 128, 5000, 5001, T]):
+        t, _ = inputs(1, T, D, cu, types, seed=D)
+        runs = []
+        for patience in ("4096", "0"):
+            monkeypatch.setenv("GDN_SCAN_PATIENCE", patience)
+            state = t["init"].clone()
+            h, fin = gdn.scan_fwd(t["x"], t["la"], state, cu_tensor(cu), out_dtype=DT[types[2]], final_state=state)
+            runs.append((h, fin) + gdn.scan_bwd(t["la"], h, t["dh"], t["init"], t["dfin"], cu_tensor(cu),
+                                                dx_dtype=DT[types[0]]))
+        assert all(torch.equal(p, q) for p, q in zip(*runs))
+
+
 def test_equal_calls_equal_bits_and_streams():
     """Runs side by side on two streams, with workspaces of their own, give the bits of a run alone."""
     t, _ = inputs(1, 4000, 512, [0, 700, 4000], ("bf16", "bf16", "bf16"), seed=7)
