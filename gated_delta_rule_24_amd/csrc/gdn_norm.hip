@@ -21,6 +21,8 @@
 #include "gdn_ops.h"
 #include "gdn_types.h"
 
+#include <algorithm>
+
 namespace gdn {
 
 // Layout of one row over a block.
@@ -215,8 +217,8 @@ __global__ __launch_bounds__(S::NT) void layernorm_fwd_kernel(int64_t rows, int 
     }
 }
 
-// SUMS: also the block's line of partial sums, part[block][2][D].
-template <typename S, typename x_t, typename y_t, bool SUMS>
+// part: the block's line of partial sums goes to part[block][2][D]; NULL: none.
+template <typename S, typename x_t, typename y_t>
 __global__ __launch_bounds__(S::NT) void layernorm_bwd_kernel(int64_t rows, int D, const y_t *__restrict__ dy,
                                                               const x_t *__restrict__ x,
                                                               const float *__restrict__ mean,
@@ -225,6 +227,8 @@ __global__ __launch_bounds__(S::NT) void layernorm_bwd_kernel(int64_t rows, int 
                                                               float *__restrict__ part) {
     __shared__ float s[S::NT / 64][2];
     const int l = threadIdx.x % S::L, g = threadIdx.x / S::L;
+    // the widest rows' sums leave no registers for a second row
+    constexpr bool AHEAD = S::NT < 1024 || S::K == 1;
     float wv[S::E], aw[S::E], ab[S::E];
     if (w) load_param<S>(w, D, l, wv);
     Raw<y_t> ry[S::K];
@@ -248,7 +252,8 @@ __global__ __launch_bounds__(S::NT) void layernorm_bwd_kernel(int64_t rows, int 
         unpack<S>(ry, u);
         unpack<S>(rx, c);
         const float m = rm, q = rq;
-        if (r0 + (int64_t)gridDim.x * S::ROWS < rows) load(r0 + (int64_t)gridDim.x * S::ROWS);
+        const bool more = r0 + (int64_t)gridDim.x * S::ROWS < rows;
+        if (AHEAD && more) load(r0 + (int64_t)gridDim.x * S::ROWS);
         float c1 = 0.f, c2 = 0.f;
 #pragma unroll
         for (int k = 0; k < S::K; ++k)
@@ -256,7 +261,7 @@ __global__ __launch_bounds__(S::NT) void layernorm_bwd_kernel(int64_t rows, int 
             for (int i = 0; i < 8; ++i) {
                 const int e = 8 * k + i;
                 c[e] = (c[e] - m) * q;
-                if (SUMS && on && S::counts(l, k, i, D)) {
+                if (on && S::counts(l, k, i, D)) {
                     aw[e] = fmaf(u[e], c[e], aw[e]);
                     ab[e] += u[e];
                 }
@@ -272,8 +277,9 @@ __global__ __launch_bounds__(S::NT) void layernorm_bwd_kernel(int64_t rows, int 
 #pragma unroll
         for (int e = 0; e < S::E; ++e) u[e] = q * (u[e] - c1 - c[e] * c2);
         if (on) store_row<S>(dx + r * D, D, l, u);
+        if (!AHEAD && more) load(r0 + (int64_t)gridDim.x * S::ROWS);
     }
-    if constexpr (SUMS) {
+    if (part) {
         // the block's row groups join, a part of the columns at a time
         float *line = part + (int64_t)blockIdx.x * 2 * D;
         if constexpr (S::ROWS == 1) {
@@ -306,19 +312,21 @@ __global__ __launch_bounds__(S::NT) void layernorm_bwd_kernel(int64_t rows, int 
     }
 }
 
-// Adds the lines: 16 columns of the 2 D (weight's, then bias's) by 16 lanes,
-// 64 groups of lines that join in LDS.
+// Adds the lines: COLS columns of the 2 D (weight's, then bias's) by as many
+// lanes, 1024 / COLS groups of lines that join in LDS.
+template <int COLS>
 __global__ __launch_bounds__(1024) void layernorm_sums_kernel(int lines, int D, const float *__restrict__ part,
                                                               float *__restrict__ dw, float *__restrict__ db) {
-    __shared__ float s[64][17];
-    const int c = threadIdx.x & 15, g = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
+    constexpr int G = 1024 / COLS;
+    __shared__ float s[G][COLS + 1];
+    const int c = threadIdx.x % COLS, g = threadIdx.x / COLS, col = blockIdx.x * COLS + c;
     float a = 0.f;
     if (col < 2 * D)
-#pragma unroll 4
-        for (int i = g; i < lines; i += 64) a += part[(int64_t)i * 2 * D + col];
+#pragma unroll 8
+        for (int i = g; i < lines; i += G) a += part[(int64_t)i * 2 * D + col];
     s[g][c] = a;
     __syncthreads();
-    for (int n = 32; n >= 1; n >>= 1) {
+    for (int n = G / 2; n >= 1; n >>= 1) {
         if (g < n) s[g][c] += s[g + n][c];
         __syncthreads();
     }
@@ -331,23 +339,39 @@ __global__ __launch_bounds__(1024) void layernorm_sums_kernel(int lines, int D, 
     }
 }
 
-// f(RowShape{}) with the layout for D: as many lanes as 8 elements each need,
-// up to a wave; longer rows take 16 elements a lane, then more waves.
-template <bool WHOLE, int NT, typename F>
+// f(RowShape{}) with the layout for D: 8 elements a lane up to a wave, then two
+// or three groups a lane, then more waves; three groups where two would leave
+// more than a third of the lanes without any.  The backward pass holds five
+// values for each element, so long rows take more lanes instead.
+template <bool WHOLE, bool BWD, int NT, typename F>
 static hipError_t with_row_shape_of(int D, F f) {
+    if (D <= 8) return f(RowShape<1, 1, NT, WHOLE>{});
+    if (D <= 16) return f(RowShape<2, 1, NT, WHOLE>{});
+    if (D <= 32) return f(RowShape<4, 1, NT, WHOLE>{});
     if (D <= 64) return f(RowShape<8, 1, NT, WHOLE>{});
     if (D <= 128) return f(RowShape<16, 1, NT, WHOLE>{});
     if (D <= 256) return f(RowShape<32, 1, NT, WHOLE>{});
+    if (D <= 384) return f(RowShape<16, 3, NT, WHOLE>{});
     if (D <= 512) return f(RowShape<64, 1, NT, WHOLE>{});
+    if (D <= 768) return f(RowShape<32, 3, NT, WHOLE>{});
     if (D <= 1024) return f(RowShape<64, 2, NT, WHOLE>{});
-    if (D <= 2048) return f(RowShape<128, 2, NT, WHOLE>{});
-    if (D <= 4096) return f(RowShape<256, 2, NT, WHOLE>{});
-    if (D <= 8192) return f(RowShape<512, 2, 512, WHOLE>{});
+    if constexpr (BWD) {
+        if (D <= 2048) return f(RowShape<256, 1, NT, WHOLE>{});
+        if (D <= 4096) return f(RowShape<512, 1, 512, WHOLE>{});
+        if (D <= 8192) return f(RowShape<1024, 1, 1024, WHOLE>{});
+    } else {
+        if (D <= 1536) return f(RowShape<64, 3, NT, WHOLE>{});
+        if (D <= 2048) return f(RowShape<128, 2, NT, WHOLE>{});
+        if (D <= 4096) return f(RowShape<256, 2, NT, WHOLE>{});
+        if (D <= 6144) return f(RowShape<256, 3, NT, WHOLE>{});
+        if (D <= 8192) return f(RowShape<512, 2, 512, WHOLE>{});
+        if (D <= 12288) return f(RowShape<512, 3, 512, WHOLE>{});
+    }
     return f(RowShape<1024, 2, 1024, WHOLE>{});
 }
-template <int NT, typename F>
+template <bool BWD, int NT, typename F>
 static hipError_t with_row_shape(int D, F f) {
-    return D % 8 == 0 ? with_row_shape_of<true, NT>(D, f) : with_row_shape_of<false, NT>(D, f);
+    return D % 8 == 0 ? with_row_shape_of<true, BWD, NT>(D, f) : with_row_shape_of<false, BWD, NT>(D, f);
 }
 
 // Threads of a block.  Measured at 262144 x 128 and 4093 x 1001 (backward):
@@ -356,16 +380,18 @@ static hipError_t with_row_shape(int D, F f) {
 constexpr int kFwdThreads = 256, kBwdThreads = 512;
 constexpr int64_t kFwdBlocks = 8192;   // more only load the parameters again
 
-// Blocks of the backward kernel, and so lines of partial sums.
+// Blocks of the backward kernel, and so lines of partial sums: four turns of a
+// block at least, so that the lines stay small beside the rows, unless that
+// leaves less than 128 blocks (511 x 4100: 32 -> 19 us).
 static int64_t bwd_blocks(int64_t rows, int rows_per_block, int threads) {
     const int64_t most = 256 * (1024 / threads);   // 1024 threads on each of 256 CUs
-    const int64_t need = (rows + rows_per_block - 1) / rows_per_block;
-    return need < most ? need : most;
+    const int64_t turns = (rows + rows_per_block - 1) / rows_per_block;
+    return std::min({most, turns, std::max<int64_t>((turns + 3) / 4, 128)});
 }
 
 size_t layernorm_bwd_workspace(int64_t rows, int32_t dim) {
     int64_t lines = 0;
-    with_row_shape<kBwdThreads>(dim, [&](auto s) {
+    with_row_shape<true, kBwdThreads>(dim, [&](auto s) {
         using S = decltype(s);
         lines = bwd_blocks(rows, S::ROWS, S::NT);
         return hipSuccess;
@@ -378,7 +404,7 @@ hipError_t launch_layernorm_fwd(const NormArgs &a, hipStream_t st) {
     return with_types(a.in_dtype, a.out_dtype, a.in_dtype, [&](auto x, auto y, auto) {
         using x_t = decltype(x);
         using y_t = decltype(y);
-        return with_row_shape<kFwdThreads>(a.dim, [&](auto s) {
+        return with_row_shape<false, kFwdThreads>(a.dim, [&](auto s) {
             using S = decltype(s);
             const int64_t need = (a.rows + S::ROWS - 1) / S::ROWS;
             const unsigned blocks = (unsigned)(need < kFwdBlocks ? need : kFwdBlocks);
@@ -400,24 +426,29 @@ hipError_t launch_layernorm_bwd(const NormArgs &a, hipStream_t st) {
         e = with_types(a.in_dtype, a.out_dtype, a.in_dtype, [&](auto x, auto y, auto) {
             using x_t = decltype(x);
             using y_t = decltype(y);
-            return with_row_shape<kBwdThreads>(a.dim, [&](auto s) {
+            return with_row_shape<true, kBwdThreads>(a.dim, [&](auto s) {
                 using S = decltype(s);
                 blocks = bwd_blocks(a.rows, S::ROWS, S::NT);
                 auto go = [&](auto *kernel) {
                     kernel<<<(unsigned)blocks, S::NT, 0, st>>>(
                         a.rows, a.dim, static_cast<const y_t *>(a.dy), static_cast<const x_t *>(a.x), a.mean, a.rstd,
-                        a.weight, static_cast<x_t *>(a.dx), part);
+                        a.weight, static_cast<x_t *>(a.dx), sums ? part : nullptr);
                     return hipGetLastError();
                 };
-                return sums ? go(layernorm_bwd_kernel<S, x_t, y_t, true>)
-                            : go(layernorm_bwd_kernel<S, x_t, y_t, false>);
+                return go(layernorm_bwd_kernel<S, x_t, y_t>);
             });
         });
     }
     if (e != hipSuccess || !sums) return e;
     ProfScope prof("gdn_layernorm_sums", st);
-    layernorm_sums_kernel<<<(unsigned)((2 * a.dim + 15) / 16), 1024, 0, st>>>((int)blocks, a.dim, part, a.dweight,
-                                                                            a.dbias);
+    auto add = [&](auto cols) {
+        constexpr int C = decltype(cols)::value;
+        layernorm_sums_kernel<C><<<(unsigned)((2 * a.dim + C - 1) / C), 1024, 0, st>>>((int)blocks, a.dim, part,
+                                                                                  a.dweight, a.dbias);
+    };
+    // whole cache lines where that leaves enough blocks
+    if (a.dim >= 4096) add(std::integral_constant<int, 64>{});
+    else add(std::integral_constant<int, 16>{});
     return hipGetLastError();
 }
 
