@@ -70,6 +70,7 @@ constexpr int kNt = 512;        // threads of a block
 constexpr int kElems = 32;      // elements per thread
 constexpr int kTc = kNt * kElems / kCw;   // tokens of a tile: 128
 constexpr int kGroup = 8;       // tiles per group of a chain, and groups per section
+constexpr int kShortRow = 32;   // tokens of a row that a thread takes alone
 constexpr uint64_t kEmpty = ~0ull;
 constexpr int64_t kMaxGridX = 1 << 20;
 constexpr int kPatience = 4096; // looks at a word before a block helps itself
@@ -740,6 +741,112 @@ __global__ __launch_bounds__(kNt, (min_waves<V, l_t, h_t, h_t>())) void scan_bwd
     if constexpr (PACKED) hand_on(p, dfin, dinit);
 }
 
+// ---- short rows --------------------------------------------------------------------
+//
+// Batches of many short rows: one thread takes V channels of a row from its
+// first token to its last, kBatch tokens in flight at a time.  No joins and no
+// hand-overs, and no lane waits for a tile that the row does not fill.
+constexpr int kBatch = 8;
+
+template <typename x_t, typename l_t, typename h_t, int V>
+__global__ __launch_bounds__(256) void scan_fwd_rows_kernel(int64_t rows, int T, int D, int32_t *__restrict__ meta,
+                                                            const x_t *__restrict__ x, const l_t *__restrict__ la,
+                                                            const float *init, float *fin, h_t *__restrict__ h) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) meta[0] = meta[1] = 0;
+    const int per = (D + V - 1) / V;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = quotient(i, per);
+        const int ch = min((int)(i - row * per) * V, D - V);   // the last thread ends with the row, as in a tile
+        const int64_t base = row * T * D + ch, at = row * D + ch;
+        float s[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] = init ? init[at + j] : 0.f;
+        for (int t0 = 0; t0 < T; t0 += kBatch) {
+            Held<x_t, V> xr[kBatch];
+            Held<l_t, V> lr[kBatch];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const uint32_t off = (uint32_t)min(t0 + q, T - 1) * (uint32_t)D;
+                lr[q].load(la + base, off);
+                xr[q].load(x + base, off);
+            }
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                if (t0 + q >= T) break;
+                h_t o[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    s[j] = fmaf(exp_gate(lr[q].get(j)), s[j], xr[q].get(j));
+                    o[j] = round_to<h_t>(s[j]);
+                }
+                store_vec<h_t, V>(h + base, (uint32_t)(t0 + q) * (uint32_t)D, o);
+            }
+        }
+        if (fin)
+#pragma unroll
+            for (int j = 0; j < V; ++j) fin[at + j] = s[j];
+    }
+}
+
+template <typename x_t, typename l_t, typename h_t, int V>
+__global__ __launch_bounds__(256) void scan_bwd_rows_kernel(int64_t rows, int T, int D, int32_t *__restrict__ meta,
+                                                            const l_t *__restrict__ la, const h_t *__restrict__ h,
+                                                            const float *__restrict__ init,
+                                                            const h_t *__restrict__ dh,
+                                                            const float *__restrict__ dfin, x_t *__restrict__ dx,
+                                                            l_t *__restrict__ dla, float *__restrict__ dinit) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) meta[0] = meta[1] = 0;
+    const int per = (D + V - 1) / V;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = quotient(i, per);
+        const int ch = min((int)(i - row * per) * V, D - V);
+        const int64_t base = row * T * D + ch, at = row * D + ch;
+        float e[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) e[j] = dfin ? dfin[at + j] : 0.f;
+        for (int t0 = T - 1; t0 >= 0; t0 -= kBatch) {
+            Held<l_t, V> lr[kBatch];
+            Held<h_t, V> gr[kBatch], hr[kBatch];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int t = max(t0 - q, 0);
+                lr[q].load(la + base, (uint32_t)t * (uint32_t)D);
+                gr[q].load(dh + base, (uint32_t)t * (uint32_t)D);
+                hr[q].load(h + base, (uint32_t)max(t - 1, 0) * (uint32_t)D);
+            }
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int t = t0 - q;
+                if (t < 0) break;
+                x_t ox[V];
+                l_t ol[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float g = gr[q].get(j) + e[j];
+                    e[j] = exp_gate(lr[q].get(j)) * g;
+                    const float past = t > 0 ? hr[q].get(j) : init ? init[at + j] : 0.f;
+                    ox[j] = round_to<x_t>(g);
+                    ol[j] = round_to<l_t>(e[j] * past);
+                }
+                store_vec<x_t, V>(dx + base, (uint32_t)t * (uint32_t)D, ox);
+                store_vec<l_t, V>(dla + base, (uint32_t)t * (uint32_t)D, ol);
+            }
+        }
+        if (dinit)
+#pragma unroll
+            for (int j = 0; j < V; ++j) dinit[at + j] = e[j];
+    }
+}
+
+// Rows of at most 32 tokens with a thread for every lane of the GPU, or of one
+// batch.  Measured in bf16 at D = 1024, rows and tiles: 4096 x 8 tokens 38 and
+// 184 us, 1024 x 16 20 and 51, 1024 x 32 39 and 58, 512 x 64 51 and 40
+// (forward); 256 x 32 21 and 18, its gradient 18 and 28.
+static bool short_rows(const ScanArgs &a) {
+    return !a.cu_seqlens && a.T > 0 &&
+           (a.T <= kBatch || (a.T <= kShortRow && (int64_t)a.B * a.D >= 256 * 1024));
+}
+
 static int scan_patience() {
     const char *s = getenv("GDN_SCAN_PATIENCE");
     return s && *s ? std::max(atoi(s), 0) : kPatience;
@@ -803,7 +910,17 @@ hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st) {
             using x_t = decltype(x);
             using l_t = decltype(l);
             using h_t = decltype(h);
-            scan_fwd_kernel<x_t, l_t, h_t, decltype(v)::value, decltype(packed)::value>
+            constexpr int V = decltype(v)::value;
+            if constexpr (!decltype(packed)::value) {
+                if (short_rows(a)) {
+                    const int64_t threads = a.B * scan_tiles(a.D, V);
+                    scan_fwd_rows_kernel<x_t, l_t, h_t, V>
+                        <<<(unsigned)std::min<int64_t>(scan_tiles(threads, 256), 1 << 20), 256, 0, st>>>(
+                    a.B, a.T, a.D, c.meta, static_cast<const x_t *>(a.x), static_cast<const l_t *>(a.log_alpha), init, a.final_state, static_cast<h_t *>(a.h));
+                    return hipGetLastError();
+                }
+            }
+            scan_fwd_kernel<x_t, l_t, h_t, V, decltype(packed)::value>
                 <<<blocks, kNt, 0, st>>>(c, static_cast<const x_t *>(a.x),
                                                    static_cast<const l_t *>(a.log_alpha), init, a.final_state,
                                                    static_cast<h_t *>(a.h));
@@ -824,7 +941,18 @@ hipError_t launch_scan_bwd(const ScanArgs &a, hipStream_t st) {
             using x_t = decltype(x);
             using l_t = decltype(l);
             using h_t = decltype(h);
-            scan_bwd_kernel<x_t, l_t, h_t, decltype(v)::value, decltype(packed)::value>
+            constexpr int V = decltype(v)::value;
+            if constexpr (!decltype(packed)::value) {
+                if (short_rows(a)) {
+                    const int64_t threads = a.B * scan_tiles(a.D, V);
+                    scan_bwd_rows_kernel<x_t, l_t, h_t, V>
+                        <<<(unsigned)std::min<int64_t>(scan_tiles(threads, 256), 1 << 20), 256, 0, st>>>(
+                    a.B, a.T, a.D, c.meta, static_cast<const l_t *>(a.log_alpha), static_cast<const h_t *>(a.h), init, static_cast<const h_t *>(a.d_h),
+                    a.d_final, static_cast<x_t *>(a.dx), static_cast<l_t *>(a.dlog_alpha), a.d_init);
+                    return hipGetLastError();
+                }
+            }
+            scan_bwd_kernel<x_t, l_t, h_t, V, decltype(packed)::value>
                 <<<blocks, kNt, 0, st>>>(c, static_cast<const l_t *>(a.log_alpha),
                                                    static_cast<const h_t *>(a.h), init,
                                                    static_cast<const h_t *>(a.d_h), a.d_final,

@@ -23,6 +23,7 @@ TYPES = [("fp32", "fp32", "fp32"), ("bf16", "fp32", "bf16"), ("bf16", "bf16", "b
          ("fp32", "bf16", "fp32"), ("bf16", "fp32", "fp32"), ("fp16", "fp32", "fp32"), ("fp32", "fp16", "fp16")]
 SHAPES = [  # B, T, D, cu
     (1, 1, 1, None), (2, 3, 5, None), (2, 300, 3, None), (1, 260, 4, None), (2, 140, 129, None), (1, 400, 131, None),
+    (700, 21, 381, None), (530, 9, 512, None), (4, 32, 40, None), (3, 8, 131, None),   # short rows
     (1, 270, 2, [0, 100, 270]), (1, 300, 259, [0, 7, 7, 300]), (3, 127, 33, None), (2, 128, 64, None), (1, 129, 65, None),
     (2, 300, 130, None), (1, 1000, 24, None), (1, 2500, 8, None), (4, 515, 72, None), (130, 2, 16, None),
     (1, 9, 20, [0, 3, 3, 4, 9]), (1, 700, 40, [0, 0, 1, 128, 256, 257, 640, 640, 700, 700]),
@@ -160,7 +161,7 @@ def test_zero_tokens_and_no_final():
 
 
 @pytest.mark.parametrize("D", [1, 3, 37, 64, 129, 131, 257, 322])
-@pytest.mark.parametrize("T", [1, 60, 700])
+@pytest.mark.parametrize("T", [1, 12, 60, 700])
 def test_batched_in_place(D, T):
     """The final states over the initial ones: the bits of separate buffers, also where blocks share channels."""
     t, _ = inputs(9, T, D, None, ("bf16", "bf16", "fp32"), seed=D)
