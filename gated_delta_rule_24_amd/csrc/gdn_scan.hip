@@ -106,9 +106,9 @@ ScanWorkspace scan_workspace_layout(int32_t B, int32_t T, int32_t D, int32_t N, 
     return w;
 }
 
-// Empties the words; packed: checks cu_seqlens (codes as
-// in chunk_table_kernel) and writes down each token's sequence; copies the
-// initial states where need be (keeps_init).
+// Empties the words; packed: checks cu_seqlens (codes as in
+// chunk_table_kernel) and writes down each token's sequence; copies the initial
+// states where need be (keeps_init).
 __global__ __launch_bounds__(256) void scan_setup_kernel(int N, int T, const int32_t *__restrict__ cu,
                                                          int32_t *__restrict__ meta, int32_t *__restrict__ seq,
                                                          u32x4_t *__restrict__ words, int64_t nwords16,
@@ -372,7 +372,6 @@ __device__ __forceinline__ float chain_state(const Chain &p, int64_t chain, int 
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
-__device__ __forceinline__ int64_t modulo(int64_t a, int64_t b) { return a - quotient(a, b) * b; }
 
 // This block's chain and its place there; false past the last tile.
 __device__ __forceinline__ bool take_tile(const Chain &p, int64_t &chain, int &k) {

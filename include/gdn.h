@@ -400,8 +400,10 @@ gdn_status gdn_scan_workspace_size(const gdn_scan_desc *desc, size_t *bytes);
  * Forward pass.
  *
  *   x            [B, T, D]  in_dtype
- *   log_alpha    [B, T, D]  gate_dtype, <= 0 (not checked; a positive value
- *                           is computed as given, -inf forgets everything)
+ *   log_alpha    [B, T, D]  gate_dtype, <= 0 (not checked; -inf forgets
+ *                           everything.  Products of alpha over up to 8192
+ *                           tokens are formed: with positive values they may
+ *                           overflow where the recurrence would not)
  *   init_state   [N, D]     fp32 or NULL (zeros)
  *   cu_seqlens   int32 [N+1] or NULL, as for gdn_chunk_fwd: empty sequences
  *                are allowed, a malformed array makes the kernels write
@@ -484,8 +486,9 @@ gdn_status gdn_scan_step(int32_t N, int32_t D, int32_t in_dtype, int32_t gate_dt
  *   y          [R, D]  out_dtype (written)
  *   mean, rstd [R]     fp32 (written) or both NULL (not returned)
  * in_dtype and out_dtype: each FP32 or one 16-bit type, not BF16 with FP16.
- * Statistics are fp32 sums of (x - mean) taken after the mean; y is rounded
- * once.  A row's results depend on that row alone.
+ * Statistics are fp32 sums, the squares taken about the mean; y is rounded
+ * once.  A row's results depend on that row alone.  With eps = 0 a constant
+ * row has no finite rstd.
  * x, y, weight and bias must be 16-byte aligned, mean and rstd 4-byte.  The
  * outputs must not overlap each other or an input.
  * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_ALIGN,
