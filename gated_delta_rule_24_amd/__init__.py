@@ -500,8 +500,10 @@ def _rows(x, name):
     dev = _cuda(x, name)
     if x.dim() < 1:
         raise ValueError(f"{name} must have at least one dim")
-    _need(x, name, _FLOATS, dev, x.dim())
-    return dev, x.shape[:-1].numel(), x.shape[-1]
+    if x.dtype not in _FLOATS or not x.is_contiguous():
+        _need(x, name, _FLOATS, dev, x.dim())
+    D = x.shape[-1]
+    return dev, x.numel() // D if D else 0, D
 
 
 def layernorm_fwd(x, weight=None, bias=None, *, eps=1e-5, out_dtype=torch.float32, y=None, stats=True):
