@@ -179,18 +179,40 @@ __device__ __forceinline__ float exp_gate(float x) { return __builtin_amdgcn_exp
 
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 // the same on any element's address (rows of D elements start anywhere)
-typedef uint32_t loose1_t __attribute__((aligned(2)));
 typedef u32x2_t loose2_t __attribute__((aligned(2)));
 typedef u32x4_t loose4_t __attribute__((aligned(2)));
-// Every element is used once: loads and stores that leave no trace in the caches.
-template <typename R>
-__device__ __forceinline__ R stream_load(const char *p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const R *>(p));
+// Every element is used once: loads and stores that leave no trace in the
+// caches.  The loose types are named at each access: a template argument would
+// lose their alignment, and the compiler would take addresses for aligned that
+// are not.
+__device__ __forceinline__ void stream_load(const char *p, uint16_t &r) {
+    r = __builtin_nontemporal_load(reinterpret_cast<const uint16_t *>(p));
 }
-template <typename R>
-__device__ __forceinline__ void stream_store(char *p, R r) {
-    __builtin_nontemporal_store(r, reinterpret_cast<R *>(p));
+__device__ __forceinline__ void stream_load(const char *p, uint32_t &r) {   // an fp32 element
+    r = __builtin_nontemporal_load(reinterpret_cast<const uint32_t *>(p));
 }
+__device__ __forceinline__ void stream_load(const char *p, u32x2_t &r) {
+    r = __builtin_nontemporal_load(reinterpret_cast<const loose2_t *>(p));
+}
+__device__ __forceinline__ void stream_load(const char *p, u32x4_t &r) {
+    r = __builtin_nontemporal_load(reinterpret_cast<const loose4_t *>(p));
+}
+__device__ __forceinline__ void stream_store(char *p, uint16_t r) {
+    __builtin_nontemporal_store(r, reinterpret_cast<uint16_t *>(p));
+}
+__device__ __forceinline__ void stream_store(char *p, uint32_t r) {
+    __builtin_nontemporal_store(r, reinterpret_cast<uint32_t *>(p));
+}
+__device__ __forceinline__ void stream_store(char *p, u32x2_t r) {
+    __builtin_nontemporal_store(r, reinterpret_cast<loose2_t *>(p));
+}
+__device__ __forceinline__ void stream_store(char *p, u32x4_t r) {
+    __builtin_nontemporal_store(r, reinterpret_cast<loose4_t *>(p));
+}
+// The registers that hold B bytes of consecutive elements.
+template <int B>
+using words_t = std::conditional_t<
+    B == 2, uint16_t, std::conditional_t<B == 4, uint32_t, std::conditional_t<B == 8, u32x2_t, u32x4_t>>>;
 
 // V consecutive elements as loaded (16-bit types two to a register).  Values
 // are converted each time they are used: the registers that this saves let
@@ -202,20 +224,13 @@ struct Held {
     // element `off` of a uniform base (32-bit byte offsets: one scalar base for all of a thread's loads)
     __device__ __forceinline__ void load(const T *base, uint32_t off) {
         const char *p = reinterpret_cast<const char *>(base) + (uint32_t)(off * (uint32_t)sizeof(T));
-        constexpr int B = V * (int)sizeof(T);
-        if constexpr (B == 2)
-            w[0] = stream_load<uint16_t>(p);
-        else if constexpr (B == 4)
-            w[0] = stream_load<loose1_t>(p);
-        else if constexpr (B == 8)
-            take(stream_load<loose2_t>(p));
+        words_t<V * (int)sizeof(T)> r;
+        stream_load(p, r);
+        if constexpr (W == 1)
+            w[0] = r;
         else
-            take(stream_load<loose4_t>(p));
-    }
-    template <typename R>
-    __device__ __forceinline__ void take(R r) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = r[i];
+            for (int i = 0; i < W; ++i) w[i] = r[i];
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -254,20 +269,12 @@ struct Gate : Held<T, V> {
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T *base, uint32_t off, const T (&v)[V]) {
     char *p = reinterpret_cast<char *>(base) + (uint32_t)(off * (uint32_t)sizeof(T));
-    constexpr int B = V * (int)sizeof(T);
     struct A {
         T e[V];
     } a;
 #pragma unroll
     for (int j = 0; j < V; ++j) a.e[j] = v[j];
-    if constexpr (B == 2)
-        stream_store(p, __builtin_bit_cast(uint16_t, a));
-    else if constexpr (B == 4)
-        stream_store<loose1_t>(p, __builtin_bit_cast(uint32_t, a));
-    else if constexpr (B == 8)
-        stream_store<loose2_t>(p, __builtin_bit_cast(u32x2_t, a));
-    else
-        stream_store<loose4_t>(p, __builtin_bit_cast(u32x4_t, a));
+    stream_store(p, __builtin_bit_cast(words_t<(int)sizeof(A)>, a));
 }
 
 // ---- the chain --------------------------------------------------------------------
