@@ -21,7 +21,7 @@
 // one hand-over per 64 tiles is serial.
 // Every published value is one 8-byte word, written and read by relaxed
 // device-scope atomics, so a word is whole or not there: scan_setup_kernel
-// fills the words with kEmpty, which no published word equals (not-a-number
+// fills the words with kEmpty, which no published word equals (a not-a-number H
 // is published in one form).  No fence is needed, as nothing but the word
 // itself is handed over.
 // Every wait ends, in whatever order the blocks run: tiles are given to blocks
@@ -47,10 +47,11 @@
 // with dx_t = g_t, dlog_alpha_t = e_t h_{t-1}.
 //
 // Packed batches are one chain over all tokens, cut at sequence starts: a map
-// that crosses a start forgets what enters it.  Such a map has A = -0 (no
-// product of exponentials is negative), and forgetting is a selection, not a
-// product with zero, so not-a-number and infinite states stay in their own
-// sequence.
+// that crosses a start forgets what enters it.  Such a map has kForgets for A
+// (no product of exponentials is negative), and forgetting is a selection, not
+// a product with zero, so not-a-number and infinite states stay in their own
+// sequence.  Inside a sequence an infinite state stays infinite: products of
+// decays do not fall to 0 by underflow (times).
 #include "gdn_device.h"
 #include "gdn_ops.h"
 #include "gdn_types.h"
@@ -149,18 +150,35 @@ __global__ __launch_bounds__(256) void scan_setup_kernel(int N, int T, const int
 
 // ---- maps ---------------------------------------------------------------------
 
-__device__ __forceinline__ bool forgets(float A) { return __float_as_uint(A) == 0x80000000u; }
+// A of a map that forgets: all bits set.  A not-a-number with its sign set counts
+// as that too, which changes nothing: the map's H is not-a-number as well.
+#define kForgets __uint_as_float(~0u)
+__device__ __forceinline__ bool forgets(float A) { return (int32_t)__float_as_uint(A) < 0; }
 // What map (A, H) makes of state s.
 template <bool PACKED>
 __device__ __forceinline__ float apply(float A, float H, float s) {
     const float v = fmaf(A, s, H);
     return PACKED && forgets(A) ? H : v;
 }
+// A product of decays is 0 only if a decay is: underflow stops at the smallest
+// number, 2^-149, so that an infinite state that decays stays infinite, as it
+// does token by token.  A finite state is off by at most 2^-149 of itself, a step
+// of the product's type there.  Decays are not negative, so their bits are
+// ordered as they are, not-a-number on top and what forgets above all.
+__device__ __forceinline__ float above_zero(float product, bool none_is_zero) {
+    return __uint_as_float(max(__float_as_uint(product), none_is_zero ? 1u : 0u));
+}
+template <bool PACKED>
+__device__ __forceinline__ float times(float A, float nA) {
+    const uint32_t a = __float_as_uint(A), n = __float_as_uint(nA);
+    const uint32_t least = min(min(a, n), 1u), forget = PACKED ? (uint32_t)((int32_t)(a | n) >> 31) : 0u;
+    return __uint_as_float(max(max(__float_as_uint(A * nA), least), forget));
+}
 // (A, H) followed by (nA, nH).
 template <bool PACKED>
 __device__ __forceinline__ void join(float &A, float &H, float nA, float nH) {
     H = apply<PACKED>(nA, nH, H);
-    A = PACKED && (forgets(nA) || forgets(A)) ? -0.f : A * nA;
+    A = times<PACKED>(A, nA);
 }
 // The word of a published pair.  H is not-a-number in one form only, so no
 // word equals kEmpty.
@@ -266,6 +284,38 @@ struct Gate : Held<T, V> {
         return exp_gate(this->get(j));
     }
 };
+// The products A of a thread's decays where some came out as 0 (above_zero).
+// Whether a decay is 0 is seen from the gates as they are held, which takes no
+// registers beside theirs: fp32 decays, or the bits of 16-bit log alpha, whose
+// decay is 0 from kZeroDecay on.  Taking `times` for every token instead costs
+// 1-2% in packed calls and with fp32 gates.
+template <typename T>
+constexpr uint32_t kZeroDecay = std::is_same_v<T, bf16_t> ? 0xC2AFu : 0xD576u;   // -87.5, -87.375
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+template <typename T, int V, int TT>
+__device__ __forceinline__ void mend_products(float (&A)[V], const Gate<T, V> (&gate)[TT]) {
+    bool zero = false;
+#pragma unroll
+    for (int j = 0; j < V; ++j) zero |= A[j] == 0.f;
+    if (!zero) return;
+    constexpr int W = Gate<T, V>::W;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        if constexpr (std::is_same_v<T, float>) {
+            uint32_t least = 1;
+#pragma unroll
+            for (int i = 0; i < TT; ++i) least = min(least, gate[i].w[k]);
+            A[k] = above_zero(A[k], least != 0);
+        } else {
+            u16x2_t most = 0;
+#pragma unroll
+            for (int i = 0; i < TT; ++i)
+                most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2_t, gate[i].w[k]));
+            A[2 * k] = above_zero(A[2 * k], most[0] < kZeroDecay<T>);
+            if constexpr (V > 1) A[2 * k + 1] = above_zero(A[2 * k + 1], most[1] < kZeroDecay<T>);
+        }
+    }
+}
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T *base, uint32_t off, const T (&v)[V]) {
     char *p = reinterpret_cast<char *>(base) + (uint32_t)(off * (uint32_t)sizeof(T));
@@ -495,9 +545,10 @@ __device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, int
             A[j] *= a;
         }
     }
+    mend_products(A, lr);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        sA[g][lp * V + j] = PACKED && starts ? -0.f : A[j];
+        sA[g][lp * V + j] = PACKED && starts ? kForgets : A[j];
         sH[g][lp * V + j] = H[j];
     }
     // The final state may go where the initial one is: it is here before
@@ -516,7 +567,7 @@ __device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, int
 #pragma nounroll
             for (int q = 0; q < G; ++q) {
                 float mA = 1.f, mH = 0.f;
-                bool forget = false;
+                bool forget = false, nonzero = true;
 #pragma nounroll
                 for (int64_t t = at + q * TT; t < at + (q + 1) * TT; ++t) {
                     if (PACKED && (t == 0 || p.seq[t - 1] != p.seq[t])) {
@@ -526,8 +577,9 @@ __device__ __forceinline__ void scan_fwd_tile(const Chain &p, int64_t chain, int
                     const float a = exp_gate(to_f32(la[t * p.D + c]));
                     mH = fmaf(a, mH, to_f32(x[t * p.D + c]));
                     mA *= a;
+                    nonzero &= a != 0.f;
                 }
-                join<PACKED>(tA, tH, PACKED && forget ? -0.f : mA, mH);
+                join<PACKED>(tA, tH, PACKED && forget ? kForgets : above_zero(mA, nonzero), mH);
             }
         };
         float s = chain_state<PACKED>(p, chain, k, tid, bA, bH, edge, map);
@@ -654,9 +706,10 @@ __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, int
             A[j] *= a;
         }
     }
+    mend_products(A, lr);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        sA[g][lp * V + j] = PACKED && ends ? -0.f : A[j];
+        sA[g][lp * V + j] = PACKED && ends ? kForgets : A[j];
         sH[g][lp * V + j] = H[j];
     }
     asm volatile("" : "+v"(edge));
@@ -673,7 +726,7 @@ __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, int
 #pragma nounroll
             for (int q = G - 1; q >= 0; --q) {
                 float mA = 1.f, mH = 0.f;
-                bool forget = false;
+                bool forget = false, nonzero = true;
 #pragma nounroll
                 for (int i = min(from + (q + 1) * TT, to) - 1; i >= from + q * TT; --i) {
                     const int64_t t = (int64_t)row * p.T + i;
@@ -684,8 +737,9 @@ __device__ __forceinline__ void scan_bwd_tile(const Chain &p, int64_t chain, int
                     const float a = exp_gate(to_f32(la[t * p.D + c]));
                     mH = a * (to_f32(dh[t * p.D + c]) + mH);
                     mA *= a;
+                    nonzero &= a != 0.f;
                 }
-                join<PACKED>(tA, tH, PACKED && forget ? -0.f : mA, mH);
+                join<PACKED>(tA, tH, PACKED && forget ? kForgets : above_zero(mA, nonzero), mH);
             }
         };
         float s = chain_state<PACKED>(p, chain, k, tid, bA, bH, edge, map);

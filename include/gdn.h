@@ -402,8 +402,10 @@ gdn_status gdn_scan_workspace_size(const gdn_scan_desc *desc, size_t *bytes);
  *   x            [B, T, D]  in_dtype
  *   log_alpha    [B, T, D]  gate_dtype, <= 0 (not checked; -inf forgets
  *                           everything.  Products of alpha over up to 8192
- *                           tokens are formed: with positive values they may
- *                           overflow where the recurrence would not)
+ *                           tokens are formed, and sums of what a tile adds
+ *                           to a state of 0: with positive log_alpha, or x
+ *                           next to the largest fp32 values, they may overflow
+ *                           where the recurrence would not)
  *   init_state   [N, D]     fp32 or NULL (zeros)
  *   cu_seqlens   int32 [N+1] or NULL, as for gdn_chunk_fwd: empty sequences
  *                are allowed, a malformed array makes the kernels write
@@ -412,6 +414,10 @@ gdn_status gdn_scan_workspace_size(const gdn_scan_desc *desc, size_t *bytes);
  *   final_state  [N, D]     fp32 or NULL (not returned).  May be the same
  *                           pointer as init_state (in-place continuation),
  *                           not a partial overlap.
+ * Values that are not finite are carried as the recurrence carries them: an
+ * infinite state stays infinite however long it decays, and becomes
+ * not-a-number where alpha is 0 (log_alpha below -87.3 counts as that: alpha
+ * has no values between 0 and 2^-126).
  * Nothing of one sequence reaches another, not-a-number and infinite values
  * included.  Equal calls give equal bits.  Long sequences are cut into tiles
  * whose blocks hand states on through the workspace; the environment variable

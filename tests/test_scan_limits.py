@@ -1,0 +1,94 @@
+"""The gated linear recurrence at the limits of its values and sizes."""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_24_amd as gdn
+from oracle import operators as R
+
+from .op_util import DT, cu_tensor, dev, host
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def same(got, want, clean, label):
+    """Not-a-number and infinities where the fp64 recurrence has them, elsewhere the bits of `clean`."""
+    g = host(got)
+    assert np.array_equal(np.isnan(g), np.isnan(want)), label
+    assert np.array_equal(np.where(np.isinf(g), g, 0), np.where(np.isinf(want), want, 0)), label
+    finite = torch.from_numpy(np.isfinite(want)).cuda()
+    assert torch.equal(got[finite], clean[finite]), label
+
+
+@pytest.mark.parametrize("patience", ["4096", "0"])
+@pytest.mark.parametrize("gate", [-0.05, -1.0, -20.0])
+@pytest.mark.parametrize("gate_type", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("T,D,cu", [(20, 8, None), (100, 3, None), (9000, 3, None), (9000, 24, None),
+                                    (9000, 3, [0, 40, 40, 8800, 9000]), (9000, 24, [0, 40, 40, 8800, 9000])])
+def test_infinite_states_decay_as_the_recurrence_says(monkeypatch, T, D, cu, gate_type, gate, patience):
+    """An infinite state times decays that are not 0 is infinite, whatever the product of the decays is in fp32
+    (-0.05 underflows over a few tiles of 128 tokens, -1 within a tile, -20 within a thread's 8 tokens); times a
+    decay of 0 it is not-a-number.  One channel each: an infinite initial state, an infinite x in the middle, both
+    with a decay of 0 later on, where there are channels for it."""
+    monkeypatch.setenv("GDN_SCAN_PATIENCE", patience)
+    g = np.random.default_rng(T + D)
+    N = 1 if cu is None else len(cu) - 1
+    at, end = (T // 3, T - 2) if cu is None else (3000, 8000)     # both in the long sequence
+    n = 0 if cu is None else 2
+    x, dh = g.standard_normal((1, T, D)), g.standard_normal((1, T, D))
+    la = np.full((1, T, D), gate)
+    init, dfin = g.standard_normal((N, D)), g.standard_normal((N, D))
+    put = lambda *v: [dev(u, gate_type if i == 1 else "fp32") for i, u in enumerate(v)]    # noqa: E731
+    clean = put(x, la, init, dh, dfin)
+    init[n, 0], x[0, at, 1] = INF, -INF
+    dfin[n, 0], dh[0, end, 1] = -INF, INF
+    if D > 4:
+        init[n, 4], dfin[n, 4] = -INF, INF
+        la[0, (at + end) // 2, 4] = -INF
+        x[0, at, 5], x[0, at + 5, 5] = INF, -INF                  # infinities of both signs meet
+        dh[0, end, 5], dh[0, end - 3, 5] = INF, -INF
+    t = put(x, la, init, dh, dfin)
+    cuts = cu_tensor(cu)
+    h, fin = gdn.scan_fwd(t[0], t[1], t[2], cuts)
+    ch, cfin = gdn.scan_fwd(clean[0], t[1], clean[2], cuts)
+    with np.errstate(invalid="ignore"):
+        want, wfin = R.scan(*(host(v) for v in t[:3]), cu)
+        wx, wl, wi = R.scan_bwd(host(t[1]), host(ch), host(t[3]), host(clean[2]), host(t[4]), cu)
+    assert np.isinf(want).any() and np.isinf(wx).any()
+    same(h, want, ch, "h")
+    same(fin, wfin, cfin, "final state")
+    dx, dl, di = gdn.scan_bwd(t[1], ch, t[3], clean[2], t[4], cuts)
+    cx, cl, ci = gdn.scan_bwd(t[1], ch, clean[3], clean[2], clean[4], cuts)
+    same(dx, wx, cx, "dx")
+    same(dl, wl, cl, "dlog_alpha")
+    same(di, wi, ci, "d_init")
+
+
+def test_decays_below_the_smallest_normal_number_are_zero():
+    """alpha has no values between 0 and 2^-126: at log_alpha = -90 a finite state is forgotten, in every form."""
+    x = torch.randn(2, 300, 20, device="cuda")
+    la = torch.full_like(x, -90.0)
+    init = 1e30 * torch.randn(2, 20, device="cuda")
+    h, fin = gdn.scan_fwd(x, la, init)
+    assert torch.equal(h, x) and torch.equal(fin, x[:, -1])
+    assert torch.equal(gdn.scan_fwd(x[:, :5].contiguous(), la[:, :5].contiguous(), init)[0], x[:, :5])
+    assert torch.equal(gdn.scan_step(init.clone(), x[:, 0].contiguous(), la[:, 0].contiguous()), x[:, 0])
+
+
+@pytest.mark.parametrize("gate_type,some,zero", [("fp32", -87.3, -87.4), ("bf16", -87.0, -87.5),
+                                                 ("fp16", -87.3125, -87.375)])
+@pytest.mark.parametrize("T", [1, 5, 300, 9000])
+def test_the_border_of_zero_decays(T, gate_type, some, zero):
+    """The last log_alpha whose decay is not 0 and the first whose decay is, by what they make of an infinite state
+    in each kernel: infinite and not-a-number."""
+    x = torch.randn(1, T, 8, device="cuda")
+    init = torch.full((1, 8), INF, device="cuda")
+    for gate, test in ((some, torch.isinf), (zero, torch.isnan)):
+        la = torch.full((1, T, 8), gate, device="cuda").to(DT[gate_type])
+        h, fin = gdn.scan_fwd(x, la, init)
+        assert test(h).all() and test(fin).all()
+        assert test(gdn.scan_step(init.clone(), x[:, 0].contiguous(), la[:, 0].contiguous())).all()
+        dx, _, di = gdn.scan_bwd(la, torch.zeros_like(x), x, None, init)
+        assert torch.isinf(dx[:, -1]).all() and test(dx[:, :-1]).all() and test(di).all()
