@@ -92,3 +92,23 @@ def test_the_border_of_zero_decays(T, gate_type, some, zero):
         assert test(gdn.scan_step(init.clone(), x[:, 0].contiguous(), la[:, 0].contiguous())).all()
         dx, _, di = gdn.scan_bwd(la, torch.zeros_like(x), x, None, init)
         assert torch.isinf(dx[:, -1]).all() and test(dx[:, :-1]).all() and test(di).all()
+
+
+def test_more_tiles_than_one_grid_dimension():
+    """Over 2^20 tiles: the last rows are those of a small call, and of the oracle's."""
+    B, T = 1_100_000, 33
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(B, T, 1, generator=g, device="cuda")
+    la = -torch.rand(B, T, 1, generator=g, device="cuda")
+    d = torch.randn(B, T, 1, generator=g, device="cuda")
+    h, fin = gdn.scan_fwd(x, la)
+    grads = gdn.scan_bwd(la, h, d)
+    for part in (slice(0, 40), slice((1 << 20) - 20, (1 << 20) + 20), slice(B - 40, B)):
+        sx, sl, sd = (v[part].contiguous() for v in (x, la, d))
+        sh, sf = gdn.scan_fwd(sx, sl)
+        assert torch.equal(h[part], sh) and torch.equal(fin[part], sf)
+        # 33 terms, each off by at most 8 + 4 |l| steps of fp32 a decay: 33 (12 * 33 + 40) 2^-24 of 33 values
+        assert np.abs(host(sh) - R.scan(host(sx), host(sl))[0]).max() <= 33 * 440 * 2.0 ** -24 * float(sx.abs().max())
+        small = gdn.scan_bwd(sl, sh, sd)
+        assert torch.equal(grads[0][part], small[0]) and torch.equal(grads[1][part], small[1])
+        assert torch.equal(grads[2][part], small[2])
