@@ -31,6 +31,20 @@ def test_layernorm_gradient_in_turns(D, types):
     check_bwd(1030 if D < 8000 else 530, D, types, seed=D)
 
 
+def test_layernorm_sums_over_many_rows_are_exact():
+    """Over 2^31 values: sums of small whole numbers below 2^24 have no rounding, so a row that is lost or counted
+    twice shows in dweight and in dbias."""
+    rows, D = 2_200_000, 1000
+    r = torch.arange(rows, device="cuda")
+    dy = ((r * 7 + r // 512) % 3).to(torch.bfloat16)[:, None].expand(rows, D).contiguous()
+    x = (1 + (r * 5 + r // 2048) % 2).to(torch.bfloat16)[:, None].expand(rows, D).contiguous()
+    mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    _, dw, db = gdn.layernorm_bwd(dy, x, mean, rstd)
+    want_w, want_b = int((dy[:, 0].long() * x[:, 0].long()).sum()), int(dy[:, 0].long().sum())
+    assert 2 ** 20 < want_b < want_w < 2 ** 24
+    assert (dw == want_w).all() and (db == want_b).all()
+
+
 def test_more_layers_than_one_launch():
     """Over 65535 layers: two launches, one after the other, over chains (pages that are read and written) and forks."""
     L = 70_000
