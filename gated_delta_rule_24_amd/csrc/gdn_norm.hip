@@ -10,12 +10,25 @@
 // that it ends with the row: the elements that it shares with the group before
 // count once and are written twice, with the same bits.  Rows of less than 8
 // elements go one by one.  A block walks over rows a grid apart and has the
-// loads of its next rows in flight while it works on a row.
+// loads of its next rows in flight while it works on a row.  The gradient of
+// rows wider than 8192 does not fit: 1024 threads have 128 registers each, and up
+// to 36 of what a thread holds go to scratch where D is a multiple of 8, 89 to 145
+// where it is not.
 //
 // Measured (MI355X, a large copy reaches 5.4 TB/s): 262144 x 128 from fp32 to
-// bf16 36 us (5.6 TB/s), its gradient in bf16 39 us (5.2), 16384 x 2048 in
-// bf16 24 us (5.6), the gradient of 4093 x 1001 in fp16 17 us, which is
-// latency: a block's two turns, the join of its sums and the second launch.
+// bf16 36 us (5.6 TB/s), its gradient in bf16 40 us (5.1), 16384 x 2048 in
+// bf16 24 us (5.6), its gradient 43 us (4.7).  The gradient of 4093 x 1001 in fp16
+// takes 17 us, 13 of them in the kernel over the rows: 128 blocks on 256 CUs, each
+// with four turns behind one another and a join of its sums, then a second launch.
+// Lanes per row are a power of two with one to three groups each, so widths just
+// above a step leave up to half of the lanes idle; and the partial sums are
+// written and read again (256 lines of 2 D: a sixth of the rows' own bytes at
+// 2048 x 16384).  2^25 elements in bf16, forward and gradient in us, a copy of the
+// bytes 25 and 37:
+//     33  38   50       1032  27   64       4100  44   70       8200  47   67
+//    264  26   52       2048  23   43       5000  26   68      12288  39   66
+//    300  38   48       2050  50   61       8192  28   55      16383  50  111
+//   1001  31   42       4096  24   53                          16384  40   69
 //
 // The gradients of weight and bias are sums over rows.  A block walks over
 // rows a grid apart and keeps its columns' sums in registers, its row groups
@@ -222,7 +235,9 @@ __global__ __launch_bounds__(S::NT) void layernorm_fwd_kernel(int64_t rows, int 
     }
 }
 
-// part: the block's line of partial sums goes to part[block][2][D]; NULL: none.
+// part: the block's line of partial sums goes to part[block][2][D]; NULL: none
+// (the sums are taken all the same: 34 us instead of 38 at 262144 x 128, 41 instead
+// of 69 at 2048 x 16384, where the lines are what is saved).
 template <typename S, typename x_t, typename y_t>
 __global__ __launch_bounds__(S::NT) void layernorm_bwd_kernel(int64_t rows, int D, const y_t *__restrict__ dy,
                                                               const x_t *__restrict__ x,
@@ -379,15 +394,18 @@ static hipError_t with_row_shape(int D, F f) {
     return D % 8 == 0 ? with_row_shape_of<true, BWD, NT>(D, f) : with_row_shape_of<false, BWD, NT>(D, f);
 }
 
-// Threads of a block.  Measured at 262144 x 128 and 4093 x 1001 (backward):
-// 512 threads, two blocks a CU, 40 and 18 us; 256 threads 46 and 25; 1024
-// threads as 512.
+// Threads of a block.  Measured (backward, bf16) with 256, 512 and 1024: 16384 x
+// 2048 53, 43 and 45 us, 262144 x 128 40, 39 and 40, 20000 x 264 17.5, 17.3 and
+// 54, 4093 x 1001 in fp16 15.5, 15.7 and 27.
 constexpr int kFwdThreads = 256, kBwdThreads = 512;
 constexpr int64_t kFwdBlocks = 8192;   // more only load the parameters again
 
 // Blocks of the backward kernel, and so lines of partial sums: four turns of a
 // block at least, so that the lines stay small beside the rows, unless that
-// leaves less than 128 blocks (511 x 4100: 32 -> 19 us).
+// leaves less than 128 blocks.  Measured in bf16 with 64, 128 and 256 for that
+// limit: 255 x 8200 24.6, 21.2 and 25.1 us, 128 x 16384 28.9, 27.0 and 26.9, 511 x
+// 4100 18.1, 18.1 and 18.8, 20000 x 264 17.3, 17.3 and 15.6, 4093 x 1001 and 300 x
+// 1001 alike.
 static int64_t bwd_blocks(int64_t rows, int rows_per_block, int threads) {
     const int64_t most = 256 * (1024 / threads);   // 1024 threads on each of 256 CUs
     const int64_t turns = (rows + rows_per_block - 1) / rows_per_block;

@@ -2,7 +2,8 @@
 // gradient and its single step.  All three are bound by HBM: no value is used
 // twice, and a token costs one exp and two or three multiply-adds a channel.
 //
-// Sequences in one pass.  Tokens compose as affine maps h -> A h + H:
+// Sequences in one pass: a form of the published single-pass scan with
+// look-back.  Tokens compose as affine maps h -> A h + H:
 //   (A1, H1) then (A2, H2)  =  (A1 A2, A2 H1 + H2).
 // A block takes a tile of 128 tokens x 128 channels, reads it once into
 // registers, forms its threads' maps, joins them in LDS, gets the state that
@@ -31,8 +32,12 @@
 // its own itself, in the same order of sums.
 //
 // Measured (MI355X, a large copy reaches 5.4 TB/s): 4 x 4096 x 2048 from bf16
-// with fp32 gates 55 us (4.9 TB/s), its gradient 91 us (5.2), 32768 x 4096 in
-// fp16 backward 247 us (5.4), 50408 packed tokens x 2048 in bf16 135 us (4.6).
+// with fp32 gates 54 us (5.0 TB/s), its gradient 91 us (5.2), 32768 x 4096 in
+// fp16 backward 249 us (5.4), 50408 packed tokens x 2048 in bf16 136 us (4.6),
+// their gradient 204 us (5.1), with fp32 gates and h 337 us (5.5).  The form of
+// the tile is the same whatever the sizes: few tiles or few channels leave most
+// of the GPU idle (3 x 1001 x 333 in fp32 13 us, 65536 x 16 in bf16 17 us, where a
+// copy of their bytes takes 2 and 1).
 // Tiles are 256 bytes a row because a plain copy in tiles of 128 tokens runs at
 // 4.9 TB/s with rows of 128 bytes, 5.5 with 256, 6.0 with 512; 256 channels in
 // blocks of 512 threads leave 64 tokens a tile and twice the words (prefill 59
@@ -164,7 +169,9 @@ __device__ __forceinline__ float apply(float A, float H, float s) {
 // number, 2^-149, so that an infinite state that decays stays infinite, as it
 // does token by token.  A finite state is off by at most 2^-149 of itself, a step
 // of the product's type there.  Decays are not negative, so their bits are
-// ordered as they are, not-a-number on top and what forgets above all.
+// ordered as they are, not-a-number on top and what forgets above all.  A chain
+// of 512 tiles pays 0.3 to 0.8 us for it (65536 x 16, 17 us), other calls less
+// than 1%.
 __device__ __forceinline__ float above_zero(float product, bool none_is_zero) {
     return __uint_as_float(max(__float_as_uint(product), none_is_zero ? 1u : 0u));
 }
@@ -192,7 +199,8 @@ __device__ __forceinline__ void put(uint64_t *p, uint64_t v) {
 __device__ __forceinline__ uint64_t get(const uint64_t *p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// exp(x): exp2's instruction on x log2(e).
+// exp(x): exp2's instruction on x log2(e).  It gives 0 below 2^-126, which is off
+// by at most 2^-126 of a finite state.
 __device__ __forceinline__ float exp_gate(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
@@ -899,9 +907,18 @@ __global__ __launch_bounds__(256) void scan_bwd_rows_kernel(int64_t rows, int T,
 }
 
 // Rows of at most 32 tokens with a thread for every lane of the GPU, or of one
-// batch.  Measured in bf16 at D = 1024, rows and tiles: 4096 x 8 tokens 38 and
-// 184 us, 1024 x 16 20 and 51, 1024 x 32 39 and 58, 512 x 64 51 and 40
-// (forward); 256 x 32 21 and 18, its gradient 18 and 28.
+// batch.  Measured in bf16 at D = 1024, rows and tiles, in us:
+//                 forward      gradient
+//   4096 x  8     39   199     57   322
+//   1024 x 16     19    54     30    90
+//    512 x 32     26    31     32    52
+//    256 x 32     23    18     21    27
+//    256 x 16     12    16     13    24
+//    128 x 32     19    11     15    15
+//    512 x 64     51    40     65    71
+// and 11 and 11, 13 and 13 at 4 x 8, which is the call's own time.  At the border of
+// the rule, 256 x 32, the forward pass loses 5 us and the gradient gains 7: one
+// rule stands for both.
 static bool short_rows(const ScanArgs &a) {
     return !a.cu_seqlens && a.T > 0 &&
            (a.T <= kBatch || (a.T <= kShortRow && (int64_t)a.B * a.D >= 256 * 1024));
@@ -947,7 +964,10 @@ static hipError_t scan_setup(const ScanArgs &a, Chain &c, const float *&init, hi
 }
 
 // Loads of 4 channels, of one where there are fewer.  Rows start on any
-// element: the vectors need no alignment beyond the element's.
+// element: the vectors need no alignment beyond the element's.  One channel at
+// a time takes the gradient past its registers (3 to 38 of a thread's are in
+// scratch; 64 x 4096 x 3 in fp32 39 us); at four, fp32 h leaves 2 to 16 there,
+// which costs nothing that shows (337 us above).
 template <typename F>
 static hipError_t with_shape(const ScanArgs &a, F f) {
     using std::integral_constant;

@@ -416,7 +416,7 @@ gdn_status gdn_scan_workspace_size(const gdn_scan_desc *desc, size_t *bytes);
  *                           not a partial overlap.
  * Values that are not finite are carried as the recurrence carries them: an
  * infinite state stays infinite however long it decays, and becomes
- * not-a-number where alpha is 0 (log_alpha below -87.3 counts as that: alpha
+ * not-a-number where alpha is 0 (log_alpha below -87.33 counts as that: alpha
  * has no values between 0 and 2^-126).
  * Nothing of one sequence reaches another, not-a-number and infinite values
  * included.  Equal calls give equal bits.  Long sequences are cut into tiles
