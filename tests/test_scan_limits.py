@@ -66,6 +66,34 @@ def test_infinite_states_decay_as_the_recurrence_says(monkeypatch, T, D, cu, gat
     same(di, wi, ci, "d_init")
 
 
+@pytest.mark.parametrize("bits", [0x7FC00000, 0xFFC00000, 0xFFFFFFFF], ids=hex)
+@pytest.mark.parametrize("gate_type", ["fp32", "bf16"])
+@pytest.mark.parametrize("cu", [[0, 5, 60, 2000, 2000, 2300], None], ids=str)
+def test_gates_that_are_not_a_number(cu, gate_type, bits):
+    """Not-a-number of either sign as a gate: everything behind it in its channel and sequence is not-a-number
+    (before it, for the gradient), over several tiles, and nothing else changes."""
+    T, D, t0 = 2300, 40, 300
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, d = (torch.randn(1, T, D, generator=g, device="cuda") for _ in range(2))
+    la = (-torch.rand(1, T, D, generator=g, device="cuda")).to(DT[gate_type])
+    cuts, (first, end), n = cu_tensor(cu), ((60, 2000) if cu else (0, T)), 2 if cu else 0
+    clean = gdn.scan_fwd(x, la, None, cuts)
+    cgrad = gdn.scan_bwd(la, clean[0], d, None, None, cuts)
+    bad = la.clone()
+    raw = bad.view(torch.int32 if gate_type == "fp32" else torch.int16)
+    raw[0, t0, 7] = np.array([bits >> (0 if gate_type == "fp32" else 16)], dtype=np.uint32).astype(
+        np.uint32 if gate_type == "fp32" else np.uint16).view(np.int32 if gate_type == "fp32" else np.int16)[0].item()
+    h, fin = gdn.scan_fwd(x, bad, None, cuts)
+    dx, dl, di = gdn.scan_bwd(bad, clean[0], d, None, None, cuts)
+    assert h[0, t0:end, 7].isnan().all() and fin[n, 7].isnan()
+    assert dx[0, first:t0, 7].isnan().all() and dl[0, first + 1:t0 + 1, 7].isnan().all() and di[n, 7].isnan()
+    h[0, t0:end, 7], fin[n, 7] = clean[0][0, t0:end, 7], clean[1][n, 7]
+    dx[0, first:t0, 7], dl[0, first:t0 + 1, 7], di[n, 7] = cgrad[0][0, first:t0, 7], cgrad[1][0, first:t0 + 1, 7], \
+        cgrad[2][n, 7]
+    for got, want in ((h, clean[0]), (fin, clean[1]), (dx, cgrad[0]), (dl, cgrad[1]), (di, cgrad[2])):
+        assert torch.equal(got, want)
+
+
 def test_decays_below_the_smallest_normal_number_are_zero():
     """alpha has no values between 0 and 2^-126: at log_alpha = -90 a finite state is forgotten, in every form."""
     x = torch.randn(2, 300, 20, device="cuda")
