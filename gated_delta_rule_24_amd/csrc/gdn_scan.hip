@@ -978,12 +978,20 @@ static hipError_t with_shape(const ScanArgs &a, F f) {
     return a.D >= 4 ? vec(integral_constant<int, 4>{}) : vec(integral_constant<int, 1>{});
 }
 
+// A block for each tile, and packed for each sequence up to 2048: empty sequences
+// are shared out over the blocks (hand_on).  4096 sequences, 16 of them with a
+// token, x 128 channels, one tile: 1015 us with its one block, 19 us so.
+static dim3 scan_grid(const ScanArgs &a, const Chain &c) {
+    const int64_t n = a.cu_seqlens ? std::max<int64_t>(c.blocks, std::min(a.N, 2048)) : c.blocks;
+    return dim3((unsigned)std::min(n, kMaxGridX), (unsigned)scan_tiles(n, kMaxGridX));
+}
+
 hipError_t launch_scan_fwd(const ScanArgs &a, hipStream_t st) {
     Chain c;
     const float *init;
     hipError_t e = scan_setup(a, c, init, st);
     if (e != hipSuccess) return e;
-    const dim3 blocks((unsigned)std::min(c.blocks, kMaxGridX), (unsigned)scan_tiles(c.blocks, kMaxGridX));
+    const dim3 blocks = scan_grid(a, c);
     ProfScope prof("gdn_scan_fwd", st);
     return with_types(a.in_dtype, a.gate_dtype, a.out_dtype, [&](auto x, auto l, auto h) {
         return with_shape(a, [&](auto v, auto packed) {
@@ -1014,7 +1022,7 @@ hipError_t launch_scan_bwd(const ScanArgs &a, hipStream_t st) {
     const float *init;
     hipError_t e = scan_setup(a, c, init, st);
     if (e != hipSuccess) return e;
-    const dim3 blocks((unsigned)std::min(c.blocks, kMaxGridX), (unsigned)scan_tiles(c.blocks, kMaxGridX));
+    const dim3 blocks = scan_grid(a, c);
     ProfScope prof("gdn_scan_bwd", st);
     return with_types(a.in_dtype, a.gate_dtype, a.out_dtype, [&](auto x, auto l, auto h) {
         return with_shape(a, [&](auto v, auto packed) {

@@ -122,6 +122,29 @@ def test_the_border_of_zero_decays(T, gate_type, some, zero):
         assert torch.isinf(dx[:, -1]).all() and test(dx[:, :-1]).all() and test(di).all()
 
 
+@pytest.mark.parametrize("N,T,D", [(5000, 16, 40), (3000, 1, 3), (70_000, 300, 5), (2500, 0, 16)])
+def test_many_empty_sequences(N, T, D):
+    """More sequences than blocks and tokens: empty ones hand on what they were given, in place and elsewhere."""
+    g = np.random.default_rng(N)
+    cu = np.concatenate([[0], np.sort(g.integers(0, T + 1, N - 1)), [T]]).tolist()
+    x, d, init, dfin = (dev(g.standard_normal(s)) for s in ((1, T, D), (1, T, D), (N, D), (N, D)))
+    la, cuts = -x.abs(), cu_tensor(cu)
+    empty = torch.tensor(np.diff(cu) == 0).cuda()
+    h, fin = gdn.scan_fwd(x, la, init, cuts)
+    assert torch.equal(fin[empty], init[empty])
+    assert not gdn.scan_fwd(x, la, None, cuts)[1][empty].any()
+    state = init.clone()
+    h2, _ = gdn.scan_fwd(x, la, state, cuts, final_state=state)
+    assert torch.equal(h, h2) and torch.equal(state, fin)
+    for n in np.flatnonzero(np.diff(cu))[:5]:          # the others are as they are alone
+        t = slice(cu[n], cu[n + 1])
+        alone = gdn.scan_fwd(x[:, t].clone(), la[:, t].clone(), init[n:n + 1].clone())
+        assert torch.allclose(fin[n], alone[1][0], rtol=1e-5, atol=1e-6)
+    di = gdn.scan_bwd(la, h, d, init, dfin, cuts)[2]
+    assert torch.equal(di[empty], dfin[empty])
+    assert not gdn.scan_bwd(la, h, d, init, None, cuts)[2][empty].any()
+
+
 def test_more_tiles_than_one_grid_dimension():
     """Over 2^20 tiles: the last rows are those of a small call, and of the oracle's."""
     B, T = 1_100_000, 33
