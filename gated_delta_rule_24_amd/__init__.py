@@ -60,6 +60,12 @@ class ChunkDesc(ctypes.Structure):
                 ("flags", ctypes.c_int32)]
 
 
+class SwaDesc(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("batch", "seqlen", "keylen", "heads", "kv_heads", "dim", "num_seqs",
+                                                    "window", "sinks", "dtype")] \
+        + [("scale", ctypes.c_float), ("flags", ctypes.c_int32)]
+
+
 class ScanDesc(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32), ("channels", ctypes.c_int32),
                 ("num_seqs", ctypes.c_int32), ("in_dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32),
@@ -102,7 +108,7 @@ def load():
     lib.gdn_chunk_fwd_check.argtypes = [vp, vp, ctypes.POINTER(i32)]
     lib.gdn_decode_step.restype = ctypes.c_int
     lib.gdn_decode_step.argtypes = [i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
-    i64, scan_desc = ctypes.c_int64, ctypes.POINTER(ScanDesc)
+    i64, scan_desc, swa_desc = ctypes.c_int64, ctypes.POINTER(ScanDesc), ctypes.POINTER(SwaDesc)
     for name, args in {
             "gdn_scan_workspace_size": [scan_desc, ctypes.POINTER(sz)],
             "gdn_scan_fwd": [scan_desc] + [vp] * 7 + [sz, vp],
@@ -111,7 +117,9 @@ def load():
             "gdn_layernorm_fwd": [i64, i32, i32, i32, ctypes.c_float] + [vp] * 7,
             "gdn_layernorm_bwd_workspace_size": [i64, i32, ctypes.POINTER(sz)],
             "gdn_layernorm_bwd": [i64, i32, i32, i32] + [vp] * 9 + [sz, vp],
-            "gdn_state_move": [i32, i32, i64, i32] + [vp] * 5}.items():
+            "gdn_state_move": [i32, i32, i64, i32] + [vp] * 5,
+            "gdn_swa_fwd_workspace_size": [swa_desc, ctypes.POINTER(sz)],
+            "gdn_swa_fwd": [swa_desc] + [vp] * 8 + [sz, vp]}.items():
         getattr(lib, name).restype, getattr(lib, name).argtypes = ctypes.c_int, args
     lib.gdn_profile_enable.restype = ctypes.c_int
     lib.gdn_profile_enable.argtypes = [i32]
@@ -582,6 +590,72 @@ def state_move_check(status: torch.Tensor) -> int:
     1 for a source out of range, 2 for a destination out of range, 3 for a
     destination given twice."""
     return chunk_fwd_check(status)
+
+
+# ---- windowed attention and its resident cache --------------------------------------
+
+@functools.lru_cache(maxsize=256)
+def _swa_desc(which, *fields):
+    """Descriptor of these sizes and types, and the workspace size of gdn_swa_<which>."""
+    d = SwaDesc(*fields, 0)
+    n = ctypes.c_size_t(0)
+    _check(getattr(load(), f"gdn_swa_{which}_workspace_size")(ctypes.byref(d), ctypes.byref(n)))
+    return d, int(n.value)
+
+
+def _swa_call(which, q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, scale, workspace):
+    """Device, shapes, descriptor and workspace of a swa_fwd or swa_bwd call."""
+    dev = _cuda(q, "q")
+    _need(q, "q", _FLOATS, dev, 4)
+    B, T, H, d = shape = tuple(q.shape)
+    _need(k, "k", (q.dtype,), dev, 4)
+    Tk, KV = k.shape[1], k.shape[2]
+    kshape = (B, Tk, KV, d)
+    _shaped(k, "k", kshape, (q.dtype,), dev)
+    _shaped(v, "v", kshape, (q.dtype,), dev)
+    N = B
+    if cu_seqlens is None:
+        if cu_seqlens_k is not None:
+            raise ValueError("cu_seqlens_k needs cu_seqlens")
+    else:
+        _need(cu_seqlens, "cu_seqlens", (torch.int32,), dev, 1)
+        N = cu_seqlens.shape[0] - 1
+        if cu_seqlens_k is None:
+            if Tk != T:
+                raise ValueError(f"k has {Tk} tokens and q {T}: cu_seqlens_k is needed")
+            cu_seqlens_k = cu_seqlens
+        else:
+            _shaped(cu_seqlens_k, "cu_seqlens_k", (N + 1,), (torch.int32,), dev)
+    desc, need = _swa_desc(which, B, T, Tk, H, KV, d, N, window, sinks, _DT[q.dtype],
+                           d ** -0.5 if scale is None else scale)
+    return dev, shape, kshape, cu_seqlens_k, desc, *_workspace(workspace, need, dev)
+
+
+def swa_fwd_workspace_size(B, T, Tk, H, KV, d, num_seqs, window, sinks=0, dtype=torch.bfloat16) -> int:
+    return _swa_desc("fwd", B, T, Tk, H, KV, d, num_seqs, window, sinks, _code(dtype), 1.0)[1]
+
+
+def swa_fwd(q, k, v, window, sinks=0, cu_seqlens=None, cu_seqlens_k=None, *, scale=None, o=None, lse=True,
+            workspace=None):
+    """Attention with a sliding window and sinks: a query sees the keys at most
+    window - 1 positions back, and its sequence's first `sinks` keys.
+
+    q [B,T,H,d], k, v [B,Tk,KV,d] (fp32/bf16/fp16, one dtype; H a multiple of
+    KV); a row's queries are its last T positions.  cu_seqlens int32 [N+1]
+    (packed batch, B == 1) or None, cu_seqlens_k the keys' (None: the same).
+    scale: None for 1 / sqrt(d).  Returns (o [B,T,H,d], lse [B,T,H] fp32 or
+    None without `lse`).
+    """
+    dev, shape, _, cu_k, desc, workspace, size = _swa_call("fwd", q, k, v, window, sinks, cu_seqlens, cu_seqlens_k,
+                                                           scale, workspace)
+    if o is None:
+        o = torch.empty(shape, dtype=q.dtype, device=dev)
+    else:
+        _shaped(o, "o", shape, (q.dtype,), dev)
+    lse = torch.empty(shape[:3], dtype=torch.float32, device=dev) if lse else None
+    _call("gdn_swa_fwd", dev, desc, _addr(q), _addr(k), _addr(v), _addr(cu_seqlens), _addr(cu_k), _addr(o),
+          _addr(lse), _addr(workspace), size)
+    return o, lse
 
 
 class profile:

@@ -30,4 +30,50 @@ inline bool overlap(const Range &a, const Range &b) {
     return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
 }
 
+// A pointer argument with what is checked of it.
+struct Arg {
+    const char *name;
+    const void *p;
+    size_t bytes;
+    bool required, written;
+    int align;
+};
+
+inline gdn_status check_args(const Arg *a, int n) {
+    for (int i = 0; i < n; ++i)
+        if (a[i].required && !a[i].p) return fail(GDN_ERR_NULL, "%s is required", a[i].name);
+    for (int i = 0; i < n; ++i)
+        if (a[i].p && (reinterpret_cast<uintptr_t>(a[i].p) & (a[i].align - 1)))
+            return fail(GDN_ERR_ALIGN, "%s is not %d-byte aligned", a[i].name, a[i].align);
+    return GDN_OK;
+}
+
+// No written range may overlap another one; `same`: the one pair that may be
+// the same buffer.
+inline gdn_status check_overlap(const Arg *a, int n, int same0 = -1, int same1 = -1) {
+    for (int i = 0; i < n; ++i) {
+        if (!a[i].written) continue;
+        for (int j = 0; j < n; ++j) {
+            if (i == j || (a[j].written && j < i)) continue;
+            if (((i == same0 && j == same1) || (i == same1 && j == same0)) && a[i].p == a[j].p) continue;
+            if (overlap(rng(a[i].name, a[i].p, a[i].bytes), rng(a[j].name, a[j].p, a[j].bytes)))
+                return fail(GDN_ERR_ALIAS, "%s overlaps %s", a[i].name, a[j].name);
+        }
+    }
+    return GDN_OK;
+}
+
+// Each type fp32 or one 16-bit type.
+inline gdn_status check_types(const int32_t *dt, int n) {
+    int32_t half = GDN_FP32;
+    for (int i = 0; i < n; ++i) {
+        if (!valid_dtype(dt[i])) return fail(GDN_ERR_DTYPE, "unknown dtype code %d", dt[i]);
+        if (dt[i] == GDN_FP32) continue;
+        if (half != GDN_FP32 && half != dt[i])
+            return fail(GDN_ERR_UNSUPPORTED, "bf16 and fp16 do not mix in one call");
+        half = dt[i];
+    }
+    return GDN_OK;
+}
+
 }  // namespace gdn

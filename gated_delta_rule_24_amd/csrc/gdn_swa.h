@@ -1,0 +1,429 @@
+// Shared parts of windowed attention (gdn_swa.hip forward, gdn_swa_bwd.hip
+// gradient): the call's shape, which unit of work a block has, and products
+// of 32 x 32 tiles whose operands lie in LDS as rows.
+//
+// The query heads that share a key head are rows of one matrix: row r of a tile
+// is query token r / G, head r mod G of the group (G = heads / kv_heads), so
+// keys and values are staged once for the group, and a few tokens of many
+// heads fill a tile.  A tile takes whole tokens (rows / G of them); what is
+// left over of its rows is computed and dropped.
+#pragma once
+
+#include "gdn_device.h"
+#include "gdn_launch.h"
+#include "gdn_types.h"
+
+namespace gdn {
+
+constexpr int kSwaMaxGroup = 16;
+constexpr int kSwaMaxSinks = 128;
+constexpr int kSwaKeyTile = 128;     // keys of a block of the key gradient
+
+struct SwaArgs {
+    int32_t B, T, Tk, N, H, KV, D, window, sinks, dtype;
+    float scale;
+    const void *q, *k, *v;
+    const int32_t *cu, *cuk;         // packed, or both NULL
+    void *o;                         // forward: written
+    float *lse;
+    const void *d_o;                 // backward
+    void *dq, *dk, *dv;
+    void *workspace;
+};
+
+// Workspace (byte offsets): status words and the table of units (packed), then
+// for the backward pass D = rowsum(dO o), the far parts' share of the sinks'
+// gradients, and its own tables.
+struct SwaWorkspace {
+    int64_t row_units, key_units, far_units;   // upper bounds
+    size_t off_rows, off_keys, off_dsum, off_far;
+    size_t total;
+};
+int swa_row_tile(const SwaArgs &a, bool bwd);
+SwaWorkspace swa_workspace_layout(const SwaArgs &a, bool bwd);
+hipError_t launch_swa_fwd(const SwaArgs &a, hipStream_t stream);
+hipError_t launch_swa_bwd(const SwaArgs &a, hipStream_t stream);
+
+// Tokens of far queries in one part of the sinks' key gradient.
+inline int swa_far_chunk(int window) { return window + kSwaKeyTile < 1024 ? 1024 : window + kSwaKeyTile; }
+
+// Builds the table of units of a packed batch: int2 {sequence, unit of the sequence}.
+// key_side: units are key tiles, then the far parts of the sinks; else tiles of
+// `tokens` query tokens.  meta: {count, code of the offsets' check}.
+hipError_t launch_swa_table(const SwaArgs &a, bool key_side, int tokens, int32_t *meta, int2 *table,
+                            hipStream_t stream);
+
+// What the kernels need to find a block's unit.
+struct SwaShape {
+    int32_t T, Tk, H, KV, G, window, sinks;
+    int32_t tokens;                  // query tokens of a tile
+    int32_t per_seq;                 // units of a sequence (not packed)
+    int32_t units;                   // of all sequences (not packed)
+    const int32_t *cu, *cuk, *meta;  // packed
+    const int2 *table;
+    float c;                         // scale log2(e)
+    float scale;
+};
+
+struct SwaUnit {
+    int unit, hk;                    // unit of the sequence, key head
+    int64_t q0, k0;                  // the sequence's first query and key
+    int Lq, Lk, n;
+};
+
+// The unit of this block; false: none.  Blocks go to the 8 XCDs in turn: each
+// XCD takes a contiguous share of the units, neighbouring tiles of one head, so
+// that the keys that they share are in one L2.
+__device__ __forceinline__ bool swa_find(const SwaShape &s, SwaUnit &u) {
+    int units = s.units;
+    if (s.cu) {
+        if (s.meta[1]) return false;
+        units = s.meta[0];
+    }
+    const int64_t total = (int64_t)units * s.KV;
+    const int64_t per = (total + 7) / 8, i = blockIdx.x >> 3, at = (blockIdx.x & 7) * per + i;
+    if (i >= per || at >= total) return false;
+    u.hk = (int)(at / units);
+    const int x = units - 1 - (int)(at - (int64_t)u.hk * units);   // later queries see more: first
+    if (s.cu) {
+        const int2 e = s.table[x];
+        u.n = e.x;
+        u.unit = e.y;
+        const int q0 = s.cu[e.x], k0 = s.cuk[e.x];
+        u.q0 = q0, u.Lq = s.cu[e.x + 1] - q0;
+        u.k0 = k0, u.Lk = s.cuk[e.x + 1] - k0;
+    } else {
+        u.n = x / s.per_seq;
+        u.unit = x - u.n * s.per_seq;
+        u.q0 = (int64_t)u.n * s.T, u.Lq = s.T;
+        u.k0 = (int64_t)u.n * s.Tk, u.Lk = s.Tk;
+    }
+    return true;
+}
+
+// ---- tiles in LDS --------------------------------------------------------------
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+
+// acc += A B over one 16-byte chunk of both operands' rows.  32 x 32 tiles:
+// lane l, m = l % 32, h = l / 32.  The accumulator holds C[8 (i / 4) + 4 h + i % 4][m]
+// in element i < 16; a lane supplies row m of A and column m of B, the two halves
+// h different chunks.
+template <typename T>
+__device__ __forceinline__ void mma32(f32x16_t &acc, u32x4_t a, u32x4_t b) {
+    if constexpr (std::is_same_v<T, bf16_t>) {
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                     __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+    } else if constexpr (std::is_same_v<T, _Float16>) {
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b),
+                                                    acc, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i]), __uint_as_float(b[i]), acc, 0, 0, 0);
+    }
+}
+
+// Two fp32 values as 16-bit values in one word, rounded to nearest.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (std::is_same_v<T, bf16_t>) {
+        return pack_bf16x2(a, b);
+    } else {
+        typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+        typedef float f2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), h2));
+    }
+}
+
+__device__ __forceinline__ uint32_t lds_addr(const void *p) { return (uint32_t)(uintptr_t)p; }
+
+// Rows of D elements in LDS, each RB bytes, their 32-byte pairs of chunks
+// permuted by the row so that neither eight rows at one chunk nor a transposing
+// read of four rows meets a bank twice.
+template <typename T, int D>
+struct Rows {
+    static constexpr int RB = D * (int)sizeof(T);
+    static constexpr int NS = RB / 32;                    // chunk pairs, steps of a product over D
+    static constexpr int RPL = RB >= 256 ? 1 : 256 / RB;  // rows across the banks
+    static constexpr int SW = (NS < 8 ? NS : 8) - 1;
+    static constexpr int ND = D / 32;                     // tiles along D
+    static constexpr bool F32 = std::is_same_v<T, float>;
+    __device__ __forceinline__ static int swz(int row) { return (row / RPL) & SW; }
+    __device__ __forceinline__ static int chunk_off(int row, int chunk) {
+        return row * RB + (((chunk >> 1) ^ swz(row)) << 5) + ((chunk & 1) << 4);
+    }
+    // What a lane's reads start from.  fresh(): the same values, which the compiler
+    // takes for new ones, so that it forms addresses where they are used instead of
+    // keeping all of them in registers.
+    struct Lane {
+        int l, row, col;
+        __device__ __forceinline__ Lane() {
+            l = threadIdx.x & 63;
+            row = (l & 31) * RB + (swz(l & 31) << 5) + ((l >> 5) << 4);
+            const int sub = (l >> 4) & 1, s = l & 15, r = 4 * (l >> 5) + (s >> 2);
+            col = r * RB + ((sub ^ swz(r)) << 5) + ((s & 3) << 3);
+        }
+        __device__ __forceinline__ Lane fresh() const {
+            Lane x = *this;
+            asm volatile("" : "+v"(x.l), "+v"(x.row), "+v"(x.col));
+            return x;
+        }
+    };
+    // Operand rows r0 .. r0 + 31 (r0 a multiple of 32), step s of the product over D.
+    __device__ __forceinline__ static u32x4_t frag(const char *t, const Lane &ln, int r0, int s) {
+        return *reinterpret_cast<const u32x4_t *>(t + (ln.row ^ (s << 5)) + r0 * RB);
+    }
+    // Columns 32 dt .. +31 of rows r0 .. r0 + 31 as the A operand of a product
+    // over the rows, in the order in which an accumulator holds its rows.
+    // 16 bits: rows 16 ks .. +15 of them.
+    __device__ __forceinline__ static u32x4_t col16(const char *t, const Lane &ln, int r0, int ks, int dt) {
+        const char *p = t + (ln.col ^ (dt << 6)) + (r0 + 16 * ks) * RB;
+        const uint2 lo = lds_read_tr16(p), hi = lds_read_tr16(p + 8 * RB);
+        return u32x4_t{lo.x, lo.y, hi.x, hi.y};
+    }
+    // fp32: the lane's value of the row that accumulator element i stands for.
+    __device__ __forceinline__ static float col32(const char *t, const Lane &ln, int r0, int i, int dt) {
+        const int m = ln.l & 31, row = 4 * (ln.l >> 5) + (i & 3);
+        const int pair = (4 * dt + (m >> 3)) ^ swz(row + 8 * (i >> 2));
+        return *reinterpret_cast<const float *>(t + row * RB + (pair << 5) + 4 * (m & 7) + (r0 + 8 * (i >> 2)) * RB);
+    }
+
+    // acc[dt] += X^T W: rows r0 .. r0 + 31 of X, W in the accumulator layout of a
+    // 32 x 32 tile (rounded to T, to nearest, as an operand).
+    __device__ __forceinline__ static void add(f32x16_t (&acc)[ND], const char *t, const Lane &ln, int r0,
+                                               const f32x16_t &w) {
+        if constexpr (F32) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt)
+                    acc[dt] = __builtin_amdgcn_mfma_f32_32x32x2f32(col32(t, ln, r0, i, dt), w[i], acc[dt], 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                u32x4_t b;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) b[e] = pack2<T>(w[8 * ks + 2 * e], w[8 * ks + 2 * e + 1]);
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) mma32<T>(acc[dt], col16(t, ln, r0, ks, dt), b);
+            }
+        }
+    }
+
+    // Whether rows r0 .. r0 + 31 hold an infinity or a NaN (the same answer in all lanes).
+    __device__ __forceinline__ static bool not_finite(const char *t, const Lane &ln, int r0) {
+        uint32_t bad = 0;
+#pragma unroll 4
+        for (int b = 0; b < 32 * RB; b += 1024) {
+            const u32x4_t x = *reinterpret_cast<const u32x4_t *>(t + r0 * RB + b + ln.l * 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (F32) {
+                    bad |= (x[e] & 0x7F800000u) == 0x7F800000u;
+                } else {
+                    constexpr uint32_t M = std::is_same_v<T, bf16_t> ? 0x7F80u : 0x7C00u;
+                    bad |= (x[e] & M) == M;
+                    bad |= ((x[e] >> 16) & M) == M;
+                }
+            }
+        }
+        return __any(bad != 0);
+    }
+
+    // add() for a tile that hides some of its (row, column) pairs and whose rows
+    // are not all finite: a hidden pair has weight 0, and 0 times infinity must
+    // not count.  The rows' finite values go through add()'s product.  What is seen
+    // of +inf and NaN then adds a product that overflows to +inf, what is seen of
+    // -inf and NaN one to -inf: both make a NaN, and a hidden one adds 0.  seen: bit
+    // i for accumulator element i.
+    // A real call on copies in memory: rare, and inlined it costs the paths beside
+    // it their registers.
+    __device__ __forceinline__ static void add_seen(f32x16_t (&acc)[ND], const char *t, int r0, const f32x16_t &w,
+                                                    uint32_t seen) {
+        f32x16_t x[ND + 1];
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) x[dt] = acc[dt];
+        x[ND] = w;
+        add_seen_call(x, lds_addr(t), r0, seen);
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) acc[dt] = x[dt];
+    }
+    __device__ __attribute__((noinline)) static void add_seen_call(f32x16_t *x, uint32_t lds, int r0, uint32_t seen) {
+        const char *t = (const char *)(const __attribute__((address_space(3))) char *)(uintptr_t)lds;
+        f32x16_t acc[ND];
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) acc[dt] = x[dt];
+        const f32x16_t w = x[ND];
+        const Lane ln;
+        constexpr float BIG = 0x1p127f;
+        auto finite = [](float x) { return fabsf(x) < __builtin_inff() ? x : 0.f; };
+        auto large = [](float x, float sign) {        // sign BIG where x is NaN or the infinity of that sign
+            return !(fabsf(x) < __builtin_inff()) && !(x * sign < 0.f) ? sign * BIG : 0.f;
+        };
+        const f32x16_t zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if constexpr (F32) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt)
+                    acc[dt] = __builtin_amdgcn_mfma_f32_32x32x2f32(finite(col32(t, ln, r0, i, dt)), w[i], acc[dt], 0, 0, 0);
+#pragma unroll 1
+            for (float sign = 1.f; sign >= -1.f; sign -= 2.f)
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) {
+                    f32x16_t z = zero;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        z = __builtin_amdgcn_mfma_f32_32x32x2f32(large(col32(t, ln, r0, i, dt), sign),
+                                                                 seen >> i & 1u ? BIG : 0.f, z, 0, 0, 0);
+                    acc[dt] += z;
+                }
+        } else {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                u32x4_t b;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) b[e] = pack2<T>(w[8 * ks + 2 * e], w[8 * ks + 2 * e + 1]);
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) {
+                    u32x4_t a = col16(t, ln, r0, ks, dt);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a[e] = pack2<T>(finite(half_of(a[e])), finite(half_of(a[e] >> 16)));
+                    mma32<T>(acc[dt], a, b);
+                }
+            }
+#pragma unroll 1
+            for (float sign = 1.f; sign >= -1.f; sign -= 2.f)
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) {
+                    f32x16_t z = zero;
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks) {
+                        u32x4_t a = col16(t, ln, r0, ks, dt), b;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            a[e] = pack_bf16x2(large(half_of(a[e]), sign), large(half_of(a[e] >> 16), sign));
+                            b[e] = pack_bf16x2(seen >> (8 * ks + 2 * e) & 1u ? BIG : 0.f,
+                                               seen >> (8 * ks + 2 * e + 1) & 1u ? BIG : 0.f);
+                        }
+                        mma32<bf16_t>(z, a, b);
+                    }
+                    acc[dt] += z;
+                }
+        }
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) x[dt] = acc[dt];
+    }
+    __device__ __forceinline__ static float half_of(uint32_t x) {
+        if constexpr (std::is_same_v<T, bf16_t>) return __uint_as_float(x << 16);
+        else return (float)__builtin_bit_cast(_Float16, (uint16_t)x);
+    }
+};
+
+// ---- staging ---------------------------------------------------------------------
+
+// Copies of PIECES KiB per wave, global -> LDS: lane l's 16 bytes at base + off[i]
+// land at lds + i * step + 16 l.  Offsets at or past `bytes` touch no memory.
+// Inline assembly, so that the compiler does not make later LDS reads wait for it:
+// completion is awaited by the caller (vmcnt, then a barrier).  M0 holds the LDS
+// address and is put back.
+template <int PIECES, int STEP>
+__device__ __forceinline__ void stage(const char *base, uint32_t bytes, const uint32_t (&off)[PIECES], uint32_t lds) {
+    u32x4_t rsrc;
+    const uint64_t b = (uint64_t)(uintptr_t)base;
+    rsrc[0] = __builtin_amdgcn_readfirstlane((uint32_t)b);
+    rsrc[1] = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32) & 0xFFFFu);
+    rsrc[2] = __builtin_amdgcn_readfirstlane(bytes);
+    rsrc[3] = 0x00020000u;
+    lds = __builtin_amdgcn_readfirstlane(lds);
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        uint32_t saved;
+        asm volatile(
+            "s_mov_b32 %0, m0\n\t"
+            "s_mov_b32 m0, %3\n\t"
+            "s_nop 0\n\t"
+            "buffer_load_dwordx4 %1, %2, 0 offen lds\n\t"
+            "s_nop 0\n\t"
+            "s_mov_b32 m0, %0"
+            : "=&s"(saved)
+            : "v"(off[i]), "s"(rsrc), "s"(lds + i * STEP)
+            : "memory");
+    }
+}
+__device__ __forceinline__ void staged_barrier() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// The two halves' values of a lane's column joined.
+__device__ __forceinline__ float half_max(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// A lane's column of a transposed D x 32 result, times f, to a row of D elements.
+// Elements 4 a .. 4 a + 3 of tile dt are columns 32 dt + 8 a + 4 h .. +3: the halves
+// exchange, so that each stores 16 bytes.
+template <typename T, int D>
+__device__ __forceinline__ void store_column(T *row, const f32x16_t (&acc)[D / 32], float f, bool on) {
+    const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt) {
+        if constexpr (std::is_same_v<T, float>) {
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                float4_t x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = acc[dt][4 * a + e] * f;
+                if (on) *reinterpret_cast<float4_t *>(row + 32 * dt + 8 * a + 4 * h) = x;
+            }
+        } else {
+#pragma unroll
+            for (int a = 0; a < 4; a += 2) {
+                uint32_t x[2][2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        x[b][e] = pack2<T>(acc[dt][4 * (a + b) + 2 * e] * f, acc[dt][4 * (a + b) + 2 * e + 1] * f);
+                const auto p = __builtin_amdgcn_permlane32_swap(x[0][0], x[1][0], false, false);
+                const auto q = __builtin_amdgcn_permlane32_swap(x[0][1], x[1][1], false, false);
+                if (on) *reinterpret_cast<u32x4_t *>(row + 32 * dt + 8 * a + 8 * h) = u32x4_t{p[0], q[0], p[1], q[1]};
+            }
+        }
+    }
+}
+
+// Lets a kernel have `bytes` of dynamic LDS.
+template <typename K>
+hipError_t swa_lds(K *kernel, int bytes) {
+    if (bytes <= 65536) return hipSuccess;
+    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// f(T{}, integral_constant<D>{}) for the call's element type and head dim.
+template <bool D256, typename F>
+hipError_t swa_with(int32_t dtype, int32_t dim, F f) {
+    auto with_dim = [&](auto t) {
+        using T = decltype(t);
+        switch (dim) {
+            case 32: return f(t, std::integral_constant<int, 32>{});
+            case 64: return f(t, std::integral_constant<int, 64>{});
+            case 128: return f(t, std::integral_constant<int, 128>{});
+        }
+        if constexpr (D256 && !std::is_same_v<T, float>)
+            if (dim == 256) return f(t, std::integral_constant<int, 256>{});
+        return hipErrorInvalidValue;
+    };
+    if (dtype == DT_BF16) return with_dim(bf16_t{});
+    if (dtype == DT_FP16) return with_dim(_Float16{});
+    return with_dim(float{});
+}
+
+}  // namespace gdn

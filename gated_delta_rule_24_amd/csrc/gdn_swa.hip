@@ -1,0 +1,325 @@
+// Windowed attention with sinks, forward:
+//   query at position p sees key j iff j <= p and (p - j < window or j < sinks)
+//   o = sum_j exp(s_j - lse) v_j,  s_j = scale q k_j,  lse = log sum_j exp(s_j)
+// over the visible keys, in one pass with the running maximum and sum of the
+// softmax in fp32.
+//
+// A wave owns 32 rows (query token, head of the group).  It forms S^T = K Q^T in
+// 32 x 32 matrix-core tiles, so that a lane holds one row's scores: the maximum
+// and sum over keys stay in the lane but for one exchange of the wave's halves,
+// and the probabilities are, as they lie, the operand of O^T += V^T P^T (K rows by
+// 16-byte LDS reads, V by transposing ones).  Q and O^T stay in registers.  The
+// waves of a block share tiles of 64 keys, copied straight to LDS one tile ahead.
+// Only tiles that the mask cuts are masked; tiles that it hides are not visited.
+#include "gdn_ops.h"
+#include "gdn_swa.h"
+
+#include <algorithm>
+
+namespace gdn {
+
+constexpr int kKeys = 64;            // keys of a staged tile
+constexpr float kSlack = 8.f;        // log2: how far scores may pass the maximum that is subtracted
+
+template <typename T, int D, int NW>
+__global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_fwd_kernel(SwaShape sh, const T *__restrict__ q,
+                                                                          const T *__restrict__ k,
+                                                                          const T *__restrict__ v, T *__restrict__ o,
+                                                                          float *__restrict__ lse) {
+    using R = Rows<T, D>;
+    constexpr int RB = R::RB, TILE = kKeys * RB, PIECES = TILE / 1024 / NW;
+    extern __shared__ __align__(16) char smem[];   // two stages of K and V tiles
+    SwaUnit u;
+    if (!swa_find(sh, u)) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, h = l >> 5;
+    const int shift = u.Lk - u.Lq;                 // position of a token less its index
+    const int t0 = u.unit * sh.tokens, t1 = min(t0 + sh.tokens, u.Lq);   // the block's tokens
+    const int pfirst = t0 + shift, plast = t1 - 1 + shift;
+    const int W = sh.window;
+
+    // the wave's and the lane's rows
+    const int row = wave * 32 + (l & 31), tt = row / sh.G, token = t0 + tt;
+    const bool on = tt < sh.tokens && token < t1;
+    const int pos = min(token, t1 - 1) + shift;
+    const int w0 = t0 + wave * 32 / sh.G;
+    const bool busy = w0 < t1 && wave * 32 / sh.G < sh.tokens;
+    const int p0 = w0 + shift, p1 = min(t0 + (wave * 32 + 31) / sh.G, t1 - 1) + shift;
+    const int64_t at = (u.q0 + min(token, t1 - 1)) * sh.H + u.hk * sh.G + row % sh.G;
+    u32x4_t qf[R::NS];
+#pragma unroll
+    for (int s = 0; s < R::NS; ++s)
+        qf[s] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const char *>(q + at * D) + 32 * s + 16 * h);
+
+    // key tiles: the sinks, then the band from `low`; one range where they meet
+    int low = max(pfirst - W + 1, 0);
+    const int high = plast + 1;
+    if (low <= sh.sinks) low = 0;
+    const int ns = low > 0 ? (sh.sinks + kKeys - 1) / kKeys : 0;
+    const int tiles = high > low ? ns + (high - low + kKeys - 1) / kKeys : 0;
+    auto first_key = [&](int it) { return it < ns ? it * kKeys : low + (it - ns) * kKeys; };
+
+    const uint32_t stride = (uint32_t)sh.KV * RB;
+    const int64_t head = (u.k0 * sh.KV + u.hk) * (int64_t)RB;
+    uint32_t off[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int b = (i * NW + wave) * 1024 + l * 16, r = b / RB, c = (b % RB) / 16;
+        off[i] = r * stride + ((((c >> 1) ^ R::swz(r)) << 5) | (c & 1) << 4);
+    }
+    const uint32_t lds = lds_addr(smem) + wave * 1024;
+    auto load = [&](int it) {
+        const int j0 = first_key(it), n = min(u.Lk - j0, kKeys);
+        const int64_t b = head + (int64_t)j0 * stride;
+        const uint32_t bytes = (n - 1) * stride + RB;
+        const uint32_t to = lds + (it & 1) * 2 * TILE;
+        stage<PIECES, NW * 1024>(reinterpret_cast<const char *>(k) + b, bytes, off, to);
+        stage<PIECES, NW * 1024>(reinterpret_cast<const char *>(v) + b, bytes, off, to + TILE);
+    };
+
+    f32x16_t acc[R::ND];
+#pragma unroll
+    for (int dt = 0; dt < R::ND; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[dt][i] = 0.f;
+    float m = -__builtin_inff(), sum = 0.f;        // log2 units; this lane's part of the sum
+
+    const typename R::Lane lane;
+    if (tiles) load(0);
+    for (int it = 0; it < tiles; ++it) {
+        staged_barrier();
+        if (it + 1 < tiles) load(it + 1);
+        if (!busy) continue;
+        const int j0 = first_key(it), jend = it < ns ? sh.sinks : high;
+        const char *kt = smem + (it & 1) * 2 * TILE, *vt = kt + TILE;
+        // 0: no row of the wave sees any of 32 keys, 2: all rows see all, 1: else
+        auto sees = [&](int j) {
+            if (j > p1 || j >= jend || (j + 31 <= p0 - W && j >= sh.sinks)) return 0;
+            return j + 31 <= p0 && j + 31 < jend && (j > p1 - W || j + 31 < sh.sinks) ? 2 : 1;
+        };
+        auto process = [&](auto subs, auto masked, int r0) {
+            constexpr int NSUB = decltype(subs)::value;
+            constexpr bool MASK = decltype(masked)::value;
+            const typename R::Lane ln = lane.fresh();
+            f32x16_t S[NSUB];
+#pragma unroll
+            for (int n = 0; n < NSUB; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[n][i] = 0.f;
+#pragma unroll
+            for (int s = 0; s < R::NS; ++s)
+#pragma unroll
+                for (int n = 0; n < NSUB; ++n) mma32<T>(S[n], R::frag(kt, ln, r0 + 32 * n, s), qf[s]);
+            uint32_t seen = 0;
+            if constexpr (MASK) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int j = j0 + r0 + 4 * (ln.l >> 5) + 8 * (i >> 2) + (i & 3);
+                    const bool see = j <= pos && j < jend && (j > pos - W || j < sh.sinks);
+                    S[0][i] = see ? S[0][i] : -__builtin_inff();
+                    seen |= (uint32_t)see << i;
+                }
+            }
+            float top = S[0][0];
+#pragma unroll
+            for (int n = 0; n < NSUB; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, S[n][i]);
+            top = half_max(top) * sh.c;
+            if (__any(top > m + kSlack)) {
+                const float up = fmaxf(m, top);
+                const float f = m == up ? 1.f : __builtin_amdgcn_exp2f(m - up);
+                m = up;
+                sum *= f;
+#pragma unroll
+                for (int dt = 0; dt < R::ND; ++dt)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[dt][i] *= f;
+            }
+            const float base = m == -__builtin_inff() ? 0.f : m;
+#pragma unroll
+            for (int n = 0; n < NSUB; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    S[n][i] = __builtin_amdgcn_exp2f(fmaf(S[n][i], sh.c, -base));
+                    sum += S[n][i];
+                }
+            if constexpr (MASK) {
+                if (__builtin_expect(R::not_finite(vt, ln, r0), 0)) {
+                    R::add_seen(acc, vt, r0, S[0], seen);
+                    return;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NSUB; ++n) R::add(acc, vt, ln, r0 + 32 * n, S[n]);
+        };
+        using std::integral_constant;
+        const int s0 = sees(j0), s1 = sees(j0 + 32);
+        if (s0 == 2 && s1 == 2) {
+            process(integral_constant<int, 2>{}, std::false_type{}, 0);
+        } else {
+#pragma unroll 1
+            for (int r0 = 0; r0 < kKeys; r0 += 32)
+                if (sees(j0 + r0)) process(integral_constant<int, 1>{}, std::true_type{}, r0);
+        }
+    }
+
+    if (!busy) return;
+    sum = half_sum(sum);
+    store_column<T, D>(o + at * D, acc, sum == 0.f ? 0.f : 1.f / sum, on);
+    if (lse && on && h == 0)
+        lse[at] = sum == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+}
+
+// ---- packed batches: the table of units ---------------------------------------------
+
+__global__ __launch_bounds__(1024) void swa_table_kernel(int N, int T, int Tk, const int32_t *__restrict__ cu,
+                                                         const int32_t *__restrict__ cuk, int key_side, int tokens,
+                                                         int window, int sinks, int far, int most,
+                                                         int32_t *__restrict__ meta, int2 *__restrict__ table) {
+    __shared__ int first[1025], part[16], code;
+    const int tid = threadIdx.x;
+    if (tid == 0) code = 0;
+    __syncthreads();
+    int bad = 0;
+    for (int n = tid; n < N; n += 1024) {
+        if (cu[n + 1] < cu[n]) bad |= 2;
+        if (cuk[n + 1] < cuk[n]) bad |= 16;
+    }
+    if (tid == 0) {
+        if (cu[0] != 0) bad |= 1;
+        if (cu[N] != T) bad |= 4;
+        if (cuk[0] != 0) bad |= 8;
+        if (cuk[N] != Tk) bad |= 32;
+    }
+    if (bad) atomicOr(&code, bad);
+    __syncthreads();
+    bad = code;
+    int total = 0;
+    for (int n0 = 0; n0 < N && !bad; n0 += 1024) {
+        const int n = n0 + tid;
+        int x = 0;
+        if (n < N) {
+            const int Lq = cu[n + 1] - cu[n], Lk = cuk[n + 1] - cuk[n];
+            if (key_side) {
+                x = (Lk + kSwaKeyTile - 1) / kSwaKeyTile;
+                // tokens past those that the first key tile's window reaches
+                const int64_t reach = (int64_t)kSwaKeyTile + window - 1 - (Lk - Lq);
+                const int rest = (int)min((int64_t)Lq, max((int64_t)Lq - reach, (int64_t)0));
+                if (x && sinks) x += (rest + far - 1) / far;
+            } else {
+                x = (Lq + tokens - 1) / tokens;
+            }
+        }
+        int sum = x;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int y = __shfl_up(sum, d, 64);
+            if ((tid & 63) >= d) sum += y;
+        }
+        if ((tid & 63) == 63) part[tid >> 6] = sum;
+        __syncthreads();
+        for (int w = 0; w < (tid >> 6); ++w) sum += part[w];
+        first[tid + 1] = sum;
+        if (tid == 0) first[0] = 0;
+        __syncthreads();
+        const int here = first[1024];
+        for (int i = tid; i < here && total + i < most; i += 1024) {
+            int a = 0, b = 1024;                   // the last sequence whose first unit is at most i
+            while (b - a > 1) {
+                const int c = (a + b) / 2;
+                if (first[c] <= i) a = c;
+                else b = c;
+            }
+            table[total + i] = int2{n0 + a, i - first[a]};
+        }
+        total += here;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        meta[0] = min(total, most);
+        meta[1] = bad ? __builtin_ctz(bad) + 1 : 0;
+    }
+}
+
+static int64_t far_tokens(const SwaArgs &a) { return swa_far_chunk(a.window); }
+
+hipError_t launch_swa_table(const SwaArgs &a, bool key_side, int tokens, int32_t *meta, int2 *table,
+                            hipStream_t st) {
+    ProfScope prof("gdn_swa_table", st);
+    const SwaWorkspace w = swa_workspace_layout(a, key_side);
+    swa_table_kernel<<<1, 1024, 0, st>>>(a.N, a.T, a.Tk, a.cu, a.cuk, key_side, tokens, a.window, a.sinks,
+                                         (int)far_tokens(a), (int)(key_side ? w.key_units : w.row_units), meta, table);
+    return hipGetLastError();
+}
+
+// Rows of a block's tile: two waves where the sequences' rows fill no more than
+// that on average.
+int swa_row_tile(const SwaArgs &a, bool) {
+    const int64_t rows = (int64_t)a.B * a.T * (a.H / a.KV);
+    return rows <= 64 * (int64_t)a.N ? 64 : 128;
+}
+
+SwaWorkspace swa_workspace_layout(const SwaArgs &a, bool bwd) {
+    SwaWorkspace w{};
+    const int tokens = swa_row_tile(a, bwd) / (a.H / a.KV);
+    const int64_t T = (int64_t)a.B * a.T, Tk = (int64_t)a.B * a.Tk, far = far_tokens(a);
+    const bool table = a.B == 1;                  // a packed batch, or one sequence
+    w.row_units = T / tokens + a.N;
+    w.far_units = a.sinks ? T / far + a.N : 0;
+    w.key_units = Tk / kSwaKeyTile + a.N + w.far_units;
+    size_t at = 256;
+    auto take = [&](size_t bytes) {
+        const size_t x = at;
+        at += (bytes + 255) / 256 * 256;
+        return x;
+    };
+    w.off_rows = take(table ? (size_t)w.row_units * 8 : 0);
+    if (bwd) {
+        w.off_keys = take(table ? (size_t)w.key_units * 8 : 0);
+        w.off_dsum = take((size_t)T * a.H * 4);
+        // every part of the sinks' tile, the near one included: dK and dV of the sinks in fp32
+        w.off_far = take(a.sinks ? (size_t)(w.far_units + a.N) * a.KV * 2 * a.sinks * a.D * 4 : 0);
+    }
+    w.total = at;
+    return w;
+}
+
+hipError_t launch_swa_fwd(const SwaArgs &a, hipStream_t st) {
+    const SwaWorkspace w = swa_workspace_layout(a, false);
+    const int rows = swa_row_tile(a, false), G = a.H / a.KV;
+    SwaShape s{};
+    s.T = a.T, s.Tk = a.Tk, s.H = a.H, s.KV = a.KV, s.G = G, s.window = a.window, s.sinks = a.sinks;
+    s.tokens = rows / G;
+    s.scale = a.scale, s.c = a.scale * 1.4426950408889634f;
+    int64_t units = w.row_units;
+    if (a.cu) {
+        int32_t *meta = static_cast<int32_t *>(a.workspace);
+        int2 *table = reinterpret_cast<int2 *>(static_cast<char *>(a.workspace) + w.off_rows);
+        hipError_t e = launch_swa_table(a, false, s.tokens, meta, table, st);
+        if (e != hipSuccess) return e;
+        s.cu = a.cu, s.cuk = a.cuk, s.meta = meta, s.table = table;
+    } else {
+        s.per_seq = (a.T + s.tokens - 1) / s.tokens;
+        units = (int64_t)s.per_seq * a.N;
+        s.units = (int)units;
+    }
+    if (units == 0) return hipSuccess;
+    ProfScope prof("gdn_swa_fwd", st);
+    return swa_with<true>(a.dtype, a.D, [&](auto t, auto dim) {
+        using T = decltype(t);
+        constexpr int D = decltype(dim)::value;
+        auto go = [&](auto waves) {
+            constexpr int NW = decltype(waves)::value;
+            const unsigned blocks = (unsigned)((units * a.KV + 7) / 8 * 8);
+            constexpr int lds = 4 * kKeys * Rows<T, D>::RB;
+            hipError_t e = swa_lds(swa_fwd_kernel<T, D, NW>, lds);
+            if (e != hipSuccess) return e;
+            swa_fwd_kernel<T, D, NW><<<blocks, 64 * NW, lds, st>>>(
+                s, static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.v),
+                static_cast<T *>(a.o), a.lse);
+            return hipGetLastError();
+        };
+        return rows == 64 ? go(std::integral_constant<int, 2>{}) : go(std::integral_constant<int, 4>{});
+    });
+}
+
+}  // namespace gdn

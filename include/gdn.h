@@ -25,8 +25,11 @@
  *
  * Next to it, in the same conventions: the elementwise gated linear
  * recurrence (gdn_scan_fwd, gdn_scan_bwd, gdn_scan_step), layer norm
- * (gdn_layernorm_fwd, gdn_layernorm_bwd) and moves of resident states
- * (gdn_state_move), described at their declarations.
+ * (gdn_layernorm_fwd, gdn_layernorm_bwd), moves of resident states
+ * (gdn_state_move), and the other token mixer of hybrid stacks, attention
+ * with a sliding window and sinks (gdn_swa_fwd, gdn_swa_bwd, gdn_swa_step),
+ * with its resident cache (gdn_cache_write, gdn_cache_read), described at
+ * their declarations.
  *
  * Both evaluations return the same numbers as the recurrence up to floating-point
  * rounding.  Chunked, single-step and save-then-resume evaluations agree
@@ -94,7 +97,8 @@ typedef enum {
 typedef enum {
     GDN_FP32 = 0,
     GDN_BF16 = 1,
-    GDN_FP16 = 2
+    GDN_FP16 = 2,
+    GDN_E4M3 = 3   /* only as the type of a cache (gdn_cache_desc) */
 } gdn_dtype;
 
 /*
@@ -570,6 +574,95 @@ gdn_status gdn_layernorm_bwd(int64_t rows, int32_t dim, int32_t in_dtype, int32_
 gdn_status gdn_state_move(int32_t layers, int32_t slots, int64_t page_bytes, int32_t moves,
                           void *state, const int32_t *src, const int32_t *dst, int32_t *status,
                           hipStream_t stream);
+
+/*
+ * Attention with a sliding window and sinks, the softmax token mixer that the
+ * hybrid stacks put between gated delta rule layers.  The query at position p
+ * of a sequence sees the key at position j iff
+ *
+ *     j <= p  and  (p - j < window  or  j < sinks)
+ *
+ * and with s_j = scale q k_j over the keys that it sees
+ *
+ *     lse = log sum_j exp(s_j)        o = sum_j exp(s_j - lse) v_j
+ *
+ * A window of at least the sequence's length is causal attention.
+ *   gdn_swa_fwd   -- whole sequences (prefill, training), optionally packed
+ *   gdn_swa_bwd   -- its gradients
+ *   gdn_swa_step  -- one token for resident sequences, on their cache
+ *
+ * Shape of a gdn_swa_fwd / gdn_swa_bwd call:
+ *   batch      B >= 1: batch rows.  Must be 1 when cu_seqlens is given.
+ *   seqlen     T >= 0: query tokens per row (packed: in all); B * T < 2^30
+ *   keylen     Tk >= 0: key tokens per row (packed: in all); B * Tk < 2^30
+ *   heads      H, 1..1024: query heads
+ *   kv_heads   KV: key heads; H is a multiple of KV, at most 16 KV.  Query head h
+ *              reads key head h / (H / KV).
+ *   dim        d: 32, 64, 128 or 256 (FP32 and gdn_swa_bwd: at most 128)
+ *   num_seqs   N: B without cu_seqlens; with it, both arrays hold N + 1 offsets
+ *   window     W >= 1
+ *   sinks      S: 0..128
+ *   dtype      of q, k, v, o and their gradients.  Products of 16-bit types run
+ *              on the 16-bit matrix cores and add in fp32; the probabilities
+ *              (and, backward, the scores' gradients) are rounded to dtype as
+ *              operands.  Scores, maxima, sums and lse are fp32.
+ *   scale      finite and > 0
+ *   flags      0
+ * A sequence's queries are its last: the query i stands at position
+ * i + (its keys) - (its queries), so that a prompt can go on behind keys that
+ * it has already (keylen > seqlen; what was read back of a full cache, sinks
+ * and then the window, serves as it is).  A query that sees no key has o = 0,
+ * lse = -inf and no gradient.  What a query does not see does not reach it,
+ * not-a-number and infinite values included.  Visible scores that are all
+ * -inf count as none.
+ */
+typedef struct {
+    int32_t batch;
+    int32_t seqlen;
+    int32_t keylen;
+    int32_t heads;
+    int32_t kv_heads;
+    int32_t dim;
+    int32_t num_seqs;
+    int32_t window;
+    int32_t sinks;
+    int32_t dtype;   /* gdn_dtype */
+    float scale;
+    int32_t flags;
+} gdn_swa_desc;
+
+/*
+ * Workspaces in bytes, written to *bytes (host pointer).  They depend only on
+ * the descriptor, need not be initialised, and may be reused by later calls
+ * ordered after this one on the stream.
+ * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_UNSUPPORTED.
+ */
+gdn_status gdn_swa_fwd_workspace_size(const gdn_swa_desc *desc, size_t *bytes);
+gdn_status gdn_swa_bwd_workspace_size(const gdn_swa_desc *desc, size_t *bytes);
+
+/*
+ * Forward pass.
+ *
+ *   q             [B, T, H, d]    dtype
+ *   k, v          [B, Tk, KV, d]  dtype
+ *   cu_seqlens,   int32 [N+1] each, or both NULL.  Packed batch (B == 1): the
+ *   cu_seqlens_k  queries of sequence n are tokens cu[n] .. cu[n+1]-1 of T, its
+ *                 keys cuk[n] .. cuk[n+1]-1 of Tk; each starts at 0, does not
+ *                 decrease and ends at T (Tk).  Empty sequences are allowed.
+ *                 The arrays are checked on the device; malformed ones make
+ *                 the kernels write nothing and gdn_chunk_fwd_check(workspace,
+ *                 ...) reports them (1 to 3 as there, 4 to 6 for the keys').
+ *   o             [B, T, H, d]    dtype (written)
+ *   lse           [B, T, H]       fp32 or NULL (not returned), natural log
+ *   workspace     at least gdn_swa_fwd_workspace_size bytes
+ * Equal calls give equal bits.  q, k, v, o and the workspace must be 16-byte
+ * aligned, the offsets and lse 4-byte.  o, lse and the workspace must not overlap
+ * anything else.
+ * Errors: as gdn_chunk_fwd.
+ */
+gdn_status gdn_swa_fwd(const gdn_swa_desc *desc, const void *q, const void *k, const void *v,
+                       const int32_t *cu_seqlens, const int32_t *cu_seqlens_k, void *o, float *lse,
+                       void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
  * Per-kernel timing for measurement harnesses (host-side bookkeeping only;
