@@ -119,7 +119,9 @@ def load():
             "gdn_layernorm_bwd": [i64, i32, i32, i32] + [vp] * 9 + [sz, vp],
             "gdn_state_move": [i32, i32, i64, i32] + [vp] * 5,
             "gdn_swa_fwd_workspace_size": [swa_desc, ctypes.POINTER(sz)],
-            "gdn_swa_fwd": [swa_desc] + [vp] * 8 + [sz, vp]}.items():
+            "gdn_swa_bwd_workspace_size": [swa_desc, ctypes.POINTER(sz)],
+            "gdn_swa_fwd": [swa_desc] + [vp] * 8 + [sz, vp],
+            "gdn_swa_bwd": [swa_desc] + [vp] * 12 + [sz, vp]}.items():
         getattr(lib, name).restype, getattr(lib, name).argtypes = ctypes.c_int, args
     lib.gdn_profile_enable.restype = ctypes.c_int
     lib.gdn_profile_enable.argtypes = [i32]
@@ -656,6 +658,29 @@ def swa_fwd(q, k, v, window, sinks=0, cu_seqlens=None, cu_seqlens_k=None, *, sca
     _call("gdn_swa_fwd", dev, desc, _addr(q), _addr(k), _addr(v), _addr(cu_seqlens), _addr(cu_k), _addr(o),
           _addr(lse), _addr(workspace), size)
     return o, lse
+
+
+def swa_bwd_workspace_size(B, T, Tk, H, KV, d, num_seqs, window, sinks=0, dtype=torch.bfloat16) -> int:
+    return _swa_desc("bwd", B, T, Tk, H, KV, d, num_seqs, window, sinks, _code(dtype), 1.0)[1]
+
+
+def swa_bwd(d_o, q, k, v, o, lse, window, sinks=0, cu_seqlens=None, cu_seqlens_k=None, *, scale=None, workspace=None):
+    """Gradients of swa_fwd's o with respect to q, k and v.
+
+    q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, scale as for swa_fwd; o
+    and lse as it returned them; d_o [B,T,H,d] in their dtype.  Returns (dq, dk,
+    dv) in that dtype.
+    """
+    dev, shape, kshape, cu_k, desc, workspace, size = _swa_call("bwd", q, k, v, window, sinks, cu_seqlens, cu_seqlens_k,
+                                                                scale, workspace)
+    _shaped(d_o, "d_o", shape, (q.dtype,), dev)
+    _shaped(o, "o", shape, (q.dtype,), dev)
+    _shaped(lse, "lse", shape[:3], (torch.float32,), dev)
+    dq = torch.empty(shape, dtype=q.dtype, device=dev)
+    dk, dv = (torch.empty(kshape, dtype=q.dtype, device=dev) for _ in range(2))
+    _call("gdn_swa_bwd", dev, desc, _addr(d_o), _addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), _addr(cu_seqlens),
+          _addr(cu_k), _addr(dq), _addr(dk), _addr(dv), _addr(workspace), size)
+    return dq, dk, dv
 
 
 class profile:

@@ -47,10 +47,11 @@ hipError_t launch_swa_bwd(const SwaArgs &a, hipStream_t stream);
 // Tokens of far queries in one part of the sinks' key gradient.
 inline int swa_far_chunk(int window) { return window + kSwaKeyTile < 1024 ? 1024 : window + kSwaKeyTile; }
 
-// Builds the table of units of a packed batch: int2 {sequence, unit of the sequence}.
-// key_side: units are key tiles, then the far parts of the sinks; else tiles of
-// `tokens` query tokens.  meta: {count, code of the offsets' check}.
-hipError_t launch_swa_table(const SwaArgs &a, bool key_side, int tokens, int32_t *meta, int2 *table,
+// Builds the tables of units of a packed batch, int2 {sequence, unit of the
+// sequence}: tiles of `tokens` query tokens, and for the backward pass the key
+// tiles, each sequence's followed by the far parts of its sinks.  meta: {units of
+// the first table, code of the offsets' check, units of the second, the code}.
+hipError_t launch_swa_table(const SwaArgs &a, bool bwd, int tokens, int32_t *meta, int2 *rows, int2 *keys,
                             hipStream_t stream);
 
 // What the kernels need to find a block's unit.

@@ -172,10 +172,16 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
 
 // ---- packed batches: the table of units ---------------------------------------------
 
+// Block 0: the query tiles' table, block 1: the key tiles'.
 __global__ __launch_bounds__(1024) void swa_table_kernel(int N, int T, int Tk, const int32_t *__restrict__ cu,
-                                                         const int32_t *__restrict__ cuk, int key_side, int tokens,
-                                                         int window, int sinks, int far, int most,
-                                                         int32_t *__restrict__ meta, int2 *__restrict__ table) {
+                                                         const int32_t *__restrict__ cuk, int tokens, int window,
+                                                         int sinks, int far, int most_rows, int most_keys,
+                                                         int32_t *__restrict__ meta, int2 *__restrict__ rows,
+                                                         int2 *__restrict__ keys) {
+    const bool key_side = blockIdx.x == 1;
+    const int most = key_side ? most_keys : most_rows;
+    int2 *table = key_side ? keys : rows;
+    meta += 2 * blockIdx.x;
     __shared__ int first[1025], part[16], code;
     const int tid = threadIdx.x;
     if (tid == 0) code = 0;
@@ -242,12 +248,13 @@ __global__ __launch_bounds__(1024) void swa_table_kernel(int N, int T, int Tk, c
 
 static int64_t far_tokens(const SwaArgs &a) { return swa_far_chunk(a.window); }
 
-hipError_t launch_swa_table(const SwaArgs &a, bool key_side, int tokens, int32_t *meta, int2 *table,
+hipError_t launch_swa_table(const SwaArgs &a, bool bwd, int tokens, int32_t *meta, int2 *rows, int2 *keys,
                             hipStream_t st) {
     ProfScope prof("gdn_swa_table", st);
-    const SwaWorkspace w = swa_workspace_layout(a, key_side);
-    swa_table_kernel<<<1, 1024, 0, st>>>(a.N, a.T, a.Tk, a.cu, a.cuk, key_side, tokens, a.window, a.sinks,
-                                         (int)far_tokens(a), (int)(key_side ? w.key_units : w.row_units), meta, table);
+    const SwaWorkspace w = swa_workspace_layout(a, bwd);
+    swa_table_kernel<<<bwd ? 2 : 1, 1024, 0, st>>>(a.N, a.T, a.Tk, a.cu, a.cuk, tokens, a.window, a.sinks,
+                                                   (int)far_tokens(a), (int)w.row_units, (int)w.key_units, meta, rows,
+                                                   keys);
     return hipGetLastError();
 }
 
@@ -294,7 +301,7 @@ hipError_t launch_swa_fwd(const SwaArgs &a, hipStream_t st) {
     if (a.cu) {
         int32_t *meta = static_cast<int32_t *>(a.workspace);
         int2 *table = reinterpret_cast<int2 *>(static_cast<char *>(a.workspace) + w.off_rows);
-        hipError_t e = launch_swa_table(a, false, s.tokens, meta, table, st);
+        hipError_t e = launch_swa_table(a, false, s.tokens, meta, table, nullptr, st);
         if (e != hipSuccess) return e;
         s.cu = a.cu, s.cuk = a.cuk, s.meta = meta, s.table = table;
     } else {

@@ -107,4 +107,39 @@ gdn_status gdn_swa_fwd(const gdn_swa_desc *desc, const void *q, const void *k, c
     return ok();
 }
 
+gdn_status gdn_swa_bwd(const gdn_swa_desc *desc, const void *d_o, const void *q, const void *k, const void *v,
+                       const void *o, const float *lse, const int32_t *cu_seqlens, const int32_t *cu_seqlens_k,
+                       void *dq, void *dk, void *dv, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    gdn_status s = check_swa_desc(desc, true);
+    if (s != GDN_OK) return s;
+    const gdn_swa_desc &d = *desc;
+    SwaArgs a = swa_args(d);
+    const size_t need = swa_workspace_layout(a, true).total;
+    s = check_swa_layout(d, cu_seqlens, cu_seqlens_k, workspace, workspace_bytes, need);
+    if (s != GDN_OK) return s;
+    const size_t rows = (size_t)d.batch * d.seqlen * d.heads, keys = (size_t)d.batch * d.keylen * d.kv_heads;
+    const size_t row = (size_t)d.dim * dtype_size(d.dtype), offs = 4 * ((size_t)d.num_seqs + 1);
+    const Arg args[] = {{"d_o", d_o, rows * row, rows > 0, false, 16},
+                        {"q", q, rows * row, rows > 0, false, 16},
+                        {"k", k, keys * row, keys > 0, false, 16},
+                        {"v", v, keys * row, keys > 0, false, 16},
+                        {"o", o, rows * row, rows > 0, false, 16},
+                        {"lse", lse, rows * 4, rows > 0, false, 4},
+                        {"cu_seqlens", cu_seqlens, offs, false, false, 4},
+                        {"cu_seqlens_k", cu_seqlens_k, offs, false, false, 4},
+                        {"dq", dq, rows * row, rows > 0, true, 16},
+                        {"dk", dk, keys * row, keys > 0, true, 16},
+                        {"dv", dv, keys * row, keys > 0, true, 16},
+                        {"workspace", workspace, need, true, true, 16}};
+    s = check_args(args, 12);
+    if (s == GDN_OK) s = check_overlap(args, 12);
+    if (s != GDN_OK) return s;
+    a.q = q, a.k = k, a.v = v, a.cu = cu_seqlens, a.cuk = cu_seqlens_k;
+    a.o = const_cast<void *>(o), a.lse = const_cast<float *>(lse), a.d_o = d_o;
+    a.dq = dq, a.dk = dk, a.dv = dv, a.workspace = workspace;
+    hipError_t err = launch_swa_bwd(a, stream);
+    if (err != hipSuccess) return hip_fail(err, "gdn_swa_bwd launch");
+    return ok();
+}
+
 }  // extern "C"

@@ -1,0 +1,450 @@
+// Windowed attention with sinks, backward.  With P = exp(s - lse) over the visible
+// pairs and D_i = d_o_i o_i,
+//   dV = P^T dO      dP = dO V^T      dS = P (dP - D)
+//   dQ = scale dS K  dK = scale dS^T Q
+// Two kernels, so that every sum has one owner and a fixed order, without atomics;
+// S and dP are formed in both (7 products of the visible pairs' size instead of 5).
+//
+// Query side: a wave owns 32 rows (query token, head of the group) and walks over
+// the keys that they see, as forward: S^T and dP^T as 32 x 32 tiles with a row in
+// each lane, dS^T as it lies the operand of dQ^T += K^T dS^T.
+//
+// Key side: a wave owns 32 keys and walks over the rows that see them: S and dP
+// with a key in each lane, P and dS the operands of dV^T += dO^T P and
+// dK^T += Q^T dS.  All later tokens see the sinks: what lies past the window of the
+// first key tile is cut into parts, each a block of its own whose share of the sinks'
+// gradients goes to the workspace in fp32, and a last kernel adds the parts.
+#include "gdn_ops.h"
+#include "gdn_swa.h"
+
+#include <algorithm>
+
+namespace gdn {
+
+constexpr int kKeys = 64;            // keys of a staged tile, query side
+constexpr int kRows = 64;            // rows of a staged tile, key side
+
+__device__ __forceinline__ float log2_lse(float lse) {
+    // a row that saw nothing: every probability 0
+    return lse == -__builtin_inff() ? __builtin_inff() : lse * 1.4426950408889634f;
+}
+
+template <typename T, int D, int NW>
+__global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dq_kernel(
+    SwaShape sh, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, const T *__restrict__ o,
+    const float *__restrict__ lse, const T *__restrict__ d_o, T *__restrict__ dq, float *__restrict__ dsum) {
+    using R = Rows<T, D>;
+    constexpr int RB = R::RB, TILE = kKeys * RB, PIECES = TILE / 1024 / NW;
+    extern __shared__ __align__(16) char smem[];   // two stages of K and V tiles
+    SwaUnit u;
+    if (!swa_find(sh, u)) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, h = l >> 5;
+    const int shift = u.Lk - u.Lq;
+    const int t0 = u.unit * sh.tokens, t1 = min(t0 + sh.tokens, u.Lq);
+    const int pfirst = t0 + shift, plast = t1 - 1 + shift;
+    const int W = sh.window;
+
+    const int row = wave * 32 + (l & 31), tt = row / sh.G, token = t0 + tt;
+    const bool on = tt < sh.tokens && token < t1;
+    const int pos = min(token, t1 - 1) + shift;
+    const int w0 = t0 + wave * 32 / sh.G;
+    const bool busy = w0 < t1 && wave * 32 / sh.G < sh.tokens;
+    const int p0 = w0 + shift, p1 = min(t0 + (wave * 32 + 31) / sh.G, t1 - 1) + shift;
+    const int64_t at = (u.q0 + min(token, t1 - 1)) * sh.H + u.hk * sh.G + row % sh.G;
+    u32x4_t qf[R::NS], gf[R::NS];
+    float dd = 0.f;
+#pragma unroll
+    for (int s = 0; s < R::NS; ++s) {
+        const int64_t b = at * RB + 32 * s + 16 * h;
+        qf[s] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const char *>(q) + b);
+        gf[s] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const char *>(d_o) + b);
+        const u32x4_t of = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const char *>(o) + b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (R::F32) {
+                dd = fmaf(__uint_as_float(of[e]), __uint_as_float(gf[s][e]), dd);
+            } else {
+                dd = fmaf(R::half_of(of[e]), R::half_of(gf[s][e]), dd);
+                dd = fmaf(R::half_of(of[e] >> 16), R::half_of(gf[s][e] >> 16), dd);
+            }
+        }
+    }
+    dd = half_sum(dd);
+    if (on && h == 0) dsum[at] = dd;
+    const float lse2 = log2_lse(lse[at]);
+
+    int low = max(pfirst - W + 1, 0);
+    const int high = plast + 1;
+    if (low <= sh.sinks) low = 0;
+    const int ns = low > 0 ? (sh.sinks + kKeys - 1) / kKeys : 0;
+    const int tiles = high > low ? ns + (high - low + kKeys - 1) / kKeys : 0;
+    auto first_key = [&](int it) { return it < ns ? it * kKeys : low + (it - ns) * kKeys; };
+
+    const uint32_t stride = (uint32_t)sh.KV * RB;
+    const int64_t head = (u.k0 * sh.KV + u.hk) * (int64_t)RB;
+    uint32_t off[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int b = (i * NW + wave) * 1024 + l * 16, r = b / RB, c = (b % RB) / 16;
+        off[i] = r * stride + ((((c >> 1) ^ R::swz(r)) << 5) | (c & 1) << 4);
+    }
+    const uint32_t lds = lds_addr(smem) + wave * 1024;
+    auto load = [&](int it) {
+        const int j0 = first_key(it), n = min(u.Lk - j0, kKeys);
+        const int64_t b = head + (int64_t)j0 * stride;
+        const uint32_t bytes = (n - 1) * stride + RB;
+        const uint32_t to = lds + (it & 1) * 2 * TILE;
+        stage<PIECES, NW * 1024>(reinterpret_cast<const char *>(k) + b, bytes, off, to);
+        stage<PIECES, NW * 1024>(reinterpret_cast<const char *>(v) + b, bytes, off, to + TILE);
+    };
+
+    f32x16_t acc[R::ND];
+#pragma unroll
+    for (int dt = 0; dt < R::ND; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[dt][i] = 0.f;
+
+    const typename R::Lane lane;
+    if (tiles) load(0);
+    for (int it = 0; it < tiles; ++it) {
+        staged_barrier();
+        if (it + 1 < tiles) load(it + 1);
+        if (!busy) continue;
+        const int j0 = first_key(it), jend = it < ns ? sh.sinks : high;
+        const char *kt = smem + (it & 1) * 2 * TILE, *vt = kt + TILE;
+        // 0: no row of the wave sees any of 32 keys, 2: all rows see all, 1: else
+        auto sees = [&](int j) {
+            if (j > p1 || j >= jend || (j + 31 <= p0 - W && j >= sh.sinks)) return 0;
+            return j + 31 <= p0 && j + 31 < jend && (j > p1 - W || j + 31 < sh.sinks) ? 2 : 1;
+        };
+        auto process = [&](auto masked, int r0) {
+            constexpr bool MASK = decltype(masked)::value;
+            const typename R::Lane ln = lane.fresh();
+            f32x16_t S, P;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[i] = P[i] = 0.f;
+#pragma unroll
+            for (int s = 0; s < R::NS; ++s) {
+                mma32<T>(S, R::frag(kt, ln, r0, s), qf[s]);
+                mma32<T>(P, R::frag(vt, ln, r0, s), gf[s]);
+            }
+            uint32_t seen = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float x = __builtin_amdgcn_exp2f(fmaf(S[i], sh.c, -lse2)) * (P[i] - dd);
+                if constexpr (MASK) {
+                    const int j = j0 + r0 + 4 * (ln.l >> 5) + 8 * (i >> 2) + (i & 3);
+                    const bool see = j <= pos && j < jend && (j > pos - W || j < sh.sinks);
+                    S[i] = see ? x : 0.f;
+                    seen |= (uint32_t)see << i;
+                } else {
+                    S[i] = x;
+                }
+            }
+            if constexpr (MASK) {
+                if (__builtin_expect(R::not_finite(kt, ln, r0), 0)) {
+                    R::add_seen(acc, kt, r0, S, seen);
+                    return;
+                }
+            }
+            R::add(acc, kt, ln, r0, S);
+        };
+        if (sees(j0) == 2 && sees(j0 + 32) == 2) {
+#pragma unroll
+            for (int r0 = 0; r0 < kKeys; r0 += 32) process(std::false_type{}, r0);
+        } else {
+#pragma unroll 1
+            for (int r0 = 0; r0 < kKeys; r0 += 32)
+                if (sees(j0 + r0)) process(std::true_type{}, r0);
+        }
+    }
+    if (busy) store_column<T, D>(dq + at * D, acc, sh.scale, on);
+}
+
+// Where the far parts of a sequence begin: tokens from `reach` on are past the
+// window of the first key tile.
+struct FarParts {
+    int reach, parts;
+};
+__host__ __device__ __forceinline__ FarParts far_parts(int Lq, int Lk, int window, int sinks, int far) {
+    const int64_t reach = (int64_t)kSwaKeyTile + window - 1 - (Lk - (int64_t)Lq);
+    FarParts f;
+    f.reach = (int)(reach < 0 ? 0 : reach > Lq ? Lq : reach);
+    f.parts = sinks && Lk > 0 ? (Lq - f.reach + far - 1) / far : 0;
+    return f;
+}
+// First part of sequence n in the workspace: part 0 is the near one's.
+__device__ __forceinline__ int64_t far_first(int64_t q0, int n, int far) { return q0 / far + 2 * (int64_t)n; }
+
+template <typename T, int D>
+__global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_kernel(
+    SwaShape sh, int far, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+    const float *__restrict__ lse, const T *__restrict__ d_o, const float *__restrict__ dsum, T *__restrict__ dk,
+    T *__restrict__ dv, float *__restrict__ share) {
+    using R = Rows<T, D>;
+    constexpr int NW = 4, RB = R::RB, TILE = kRows * RB, PIECES = TILE / 1024 / NW;
+    extern __shared__ __align__(16) char smem[];   // two stages of Q and dO tiles, of lse and D
+    float *stats = reinterpret_cast<float *>(smem + 4 * TILE);
+    SwaUnit u;
+    if (!swa_find(sh, u)) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, h = l >> 5;
+    const int shift = u.Lk - u.Lq, W = sh.window;
+    const int key_tiles = (u.Lk + kSwaKeyTile - 1) / kSwaKeyTile;
+    const FarParts fp = far_parts(u.Lq, u.Lk, W, sh.sinks, far);
+    const int part = u.unit - key_tiles;           // >= 0: a far part
+    const int jt = part >= 0 ? 0 : u.unit * kSwaKeyTile;
+
+    // the tokens that this block takes
+    int ta, tb;
+    if (part >= 0) {
+        ta = fp.reach + part * far;
+        tb = min(ta + far, u.Lq);
+    } else {
+        ta = max(jt - shift, 0);
+        tb = (int)min((int64_t)jt + kSwaKeyTile - 1 + W - shift, (int64_t)u.Lq);
+    }
+    const int tiles = tb > ta ? (tb - ta + sh.tokens - 1) / sh.tokens : 0;
+
+    const int k0 = jt + wave * 32, key = k0 + (l & 31);
+    const bool busy = k0 < u.Lk && (part < 0 || k0 < sh.sinks);
+    const int64_t at = (u.k0 + min(key, u.Lk - 1)) * sh.KV + u.hk;
+    u32x4_t kf[R::NS], vf[R::NS];
+#pragma unroll
+    for (int s = 0; s < R::NS; ++s) {
+        const int64_t b = at * RB + 32 * s + 16 * h;
+        kf[s] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const char *>(k) + b);
+        vf[s] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const char *>(v) + b);
+    }
+
+    // rows left over of a tile (the group's size does not divide it) are never
+    // copied: they stay zeros, and their probabilities 0
+    const int rows = sh.tokens * sh.G;
+    if (rows < kRows) {
+        for (int b = threadIdx.x * 16; b < (kRows - rows) * RB; b += 256 * 16)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) *reinterpret_cast<u32x4_t *>(smem + x * TILE + rows * RB + b) = u32x4_t{0u, 0u, 0u, 0u};
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    const uint32_t stride = (uint32_t)sh.H * RB;
+    uint32_t off[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int b = (i * NW + wave) * 1024 + l * 16, r = b / RB, c = (b % RB) / 16;
+        off[i] = r < rows ? (r / sh.G) * stride + (r % sh.G) * RB + ((((c >> 1) ^ R::swz(r)) << 5) | (c & 1) << 4)
+                          : 0xFFFFFFFFu;
+    }
+    const uint32_t lds = lds_addr(smem) + wave * 1024;
+    const int srow = l, stoken = srow / sh.G;      // waves 0 and 1 bring lse and D of the tile's rows
+    float stat = 0.f;
+    auto load = [&](int it) {
+        const int t0 = ta + it * sh.tokens, n = min(tb - t0, sh.tokens);
+        const int64_t first = (u.q0 + t0) * sh.H + u.hk * sh.G, b = first * RB;
+        const uint32_t bytes = (n - 1) * stride + sh.G * RB;
+        const uint32_t to = lds + (it & 1) * 2 * TILE;
+        stage<PIECES, NW * 1024>(reinterpret_cast<const char *>(q) + b, bytes, off, to);
+        stage<PIECES, NW * 1024>(reinterpret_cast<const char *>(d_o) + b, bytes, off, to + TILE);
+        if (wave < 2) {
+            const bool there = srow < rows && stoken < n;
+            const int64_t a = first + (there ? (int64_t)stoken * sh.H + srow % sh.G : 0);
+            stat = wave == 0 ? log2_lse(lse[a]) : dsum[a];
+            if (!there) stat = wave == 0 ? __builtin_inff() : 0.f;
+        }
+    };
+    auto put = [&](int it) {
+        if (wave < 2) stats[((it & 1) * 2 + wave) * kRows + l] = stat;
+    };
+
+    f32x16_t ak[R::ND], av[R::ND];
+#pragma unroll
+    for (int dt = 0; dt < R::ND; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ak[dt][i] = av[dt][i] = 0.f;
+
+    const typename R::Lane lane;
+    if (tiles) {
+        load(0);
+        put(0);
+    }
+    for (int it = 0; it < tiles; ++it) {
+        staged_barrier();
+        if (it + 1 < tiles) load(it + 1);
+        const int t0 = ta + it * sh.tokens;
+        const char *qt = smem + (it & 1) * 2 * TILE, *gt = qt + TILE;
+        const float *st = stats + (it & 1) * 2 * kRows;
+        // 0: none of 32 rows sees any of the wave's keys, 2: all see all, 1: else
+        auto sees = [&](int r0) {
+            const int a = t0 + r0 / sh.G, b = min(t0 + (r0 + 31) / sh.G, t0 + sh.tokens - 1);
+            if (!busy || r0 >= rows || a >= tb) return 0;
+            const int p0 = a + shift, p1 = min(b, tb - 1) + shift;
+            if (k0 > p1 || (k0 + 31 <= p0 - W && k0 >= sh.sinks)) return 0;
+            return k0 + 31 <= p0 && (k0 > p1 - W || k0 + 31 < sh.sinks) && b < tb ? 2 : 1;
+        };
+        auto process = [&](auto masked, int r0) {
+            constexpr bool MASK = decltype(masked)::value;
+            const typename R::Lane ln = lane.fresh();
+            f32x16_t S, P;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[i] = P[i] = 0.f;
+#pragma unroll
+            for (int s = 0; s < R::NS; ++s) {
+                mma32<T>(S, R::frag(qt, ln, r0, s), kf[s]);
+                mma32<T>(P, R::frag(gt, ln, r0, s), vf[s]);
+            }
+            uint32_t seen = 0;
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const int r = r0 + 8 * a + 4 * (ln.l >> 5);
+                const float4_t L = *reinterpret_cast<const float4_t *>(st + r);
+                const float4_t dd = *reinterpret_cast<const float4_t *>(st + kRows + r);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 4 * a + e;
+                    const float p = __builtin_amdgcn_exp2f(fmaf(S[i], sh.c, -L[e]));
+                    const float x = p * (P[i] - dd[e]);
+                    if constexpr (MASK) {
+                        const int token = t0 + (r + e) / sh.G, pos = token + shift;
+                        const bool see = r + e < rows && token < tb && key <= pos && (key > pos - W || key < sh.sinks);
+                        S[i] = see ? p : 0.f;
+                        P[i] = see ? x : 0.f;
+                        seen |= (uint32_t)see << i;
+                    } else {
+                        S[i] = p;
+                        P[i] = x;
+                    }
+                }
+            }
+            if constexpr (MASK) {
+                if (__builtin_expect(R::not_finite(qt, ln, r0) || R::not_finite(gt, ln, r0), 0)) {
+                    R::add_seen(av, gt, r0, S, seen);
+                    R::add_seen(ak, qt, r0, P, seen);
+                    return;
+                }
+            }
+            R::add(av, gt, ln, r0, S);
+            R::add(ak, qt, ln, r0, P);
+        };
+        if (sees(0) == 2 && sees(32) == 2) {
+#pragma unroll
+            for (int r0 = 0; r0 < kRows; r0 += 32) process(std::false_type{}, r0);
+        } else {
+#pragma unroll 1
+            for (int r0 = 0; r0 < kRows; r0 += 32)
+                if (sees(r0)) process(std::true_type{}, r0);
+        }
+        if (it + 1 < tiles) put(it + 1);
+    }
+
+    if (!busy) return;
+    const bool shared = fp.parts > 0 && jt == 0 && key < sh.sinks;   // the parts are added later
+    if (part < 0) {
+        const bool on = key < u.Lk && !shared;
+        store_column<T, D>(dk + at * D, ak, sh.scale, on);
+        store_column<T, D>(dv + at * D, av, 1.f, on);
+    }
+    if (fp.parts > 0 && k0 < sh.sinks && jt == 0) {
+        const int64_t slot = far_first(u.q0, u.n, far) + (part >= 0 ? part + 1 : 0);
+        float *to = share + ((slot * sh.KV + u.hk) * 2 * sh.sinks + key) * (int64_t)D;
+        store_column<float, D>(to, ak, sh.scale, shared && key < u.Lk);
+        store_column<float, D>(to + (int64_t)sh.sinks * D, av, 1.f, shared && key < u.Lk);
+    }
+}
+
+// Adds the parts' shares of the sinks' gradients, in their order.
+template <typename T>
+__global__ __launch_bounds__(256) void swa_sinks_kernel(SwaShape sh, int far, int D, const float *__restrict__ share,
+                                                        T *__restrict__ dk, T *__restrict__ dv) {
+    if (sh.cu && sh.meta[1]) return;
+    const int n = blockIdx.x / sh.KV, hk = blockIdx.x - n * sh.KV;
+    int64_t q0 = (int64_t)n * sh.T, k0 = (int64_t)n * sh.Tk;
+    int Lq = sh.T, Lk = sh.Tk;
+    if (sh.cu) {
+        q0 = sh.cu[n], Lq = sh.cu[n + 1] - sh.cu[n];
+        k0 = sh.cuk[n], Lk = sh.cuk[n + 1] - sh.cuk[n];
+    }
+    const FarParts fp = far_parts(Lq, Lk, sh.window, sh.sinks, far);
+    if (fp.parts == 0) return;
+    const int i = blockIdx.y * 256 + threadIdx.x, size = min(sh.sinks, Lk) * D;
+    if (i >= size) return;
+    const int64_t step = (int64_t)sh.KV * 2 * sh.sinks * D;
+    const float *from = share + far_first(q0, n, far) * step + (int64_t)hk * 2 * sh.sinks * D + i;
+    float a = 0.f, b = 0.f;
+#pragma unroll 8
+    for (int p = 0; p <= fp.parts; ++p) {
+        a += from[p * step];
+        b += from[p * step + (int64_t)sh.sinks * D];
+    }
+    const int64_t to = ((k0 + i / D) * sh.KV + hk) * D + i % D;
+    dk[to] = round_to<T>(a);
+    dv[to] = round_to<T>(b);
+}
+
+hipError_t launch_swa_bwd(const SwaArgs &a, hipStream_t st) {
+    const SwaWorkspace w = swa_workspace_layout(a, true);
+    const int rows = swa_row_tile(a, true), G = a.H / a.KV, far = swa_far_chunk(a.window);
+    char *ws = static_cast<char *>(a.workspace);
+    float *dsum = reinterpret_cast<float *>(ws + w.off_dsum), *share = reinterpret_cast<float *>(ws + w.off_far);
+    SwaShape s{};
+    s.T = a.T, s.Tk = a.Tk, s.H = a.H, s.KV = a.KV, s.G = G, s.window = a.window, s.sinks = a.sinks;
+    s.tokens = rows / G;
+    s.scale = a.scale, s.c = a.scale * 1.4426950408889634f;
+    SwaShape sk = s;
+    sk.tokens = kRows / G;
+    int64_t units = w.row_units, key_units = w.key_units;
+    bool join = a.sinks && (int64_t)a.Tk >= (int64_t)kSwaKeyTile + a.window;
+    if (a.cu) {
+        int32_t *meta = static_cast<int32_t *>(a.workspace);
+        int2 *table = reinterpret_cast<int2 *>(ws + w.off_rows), *keys = reinterpret_cast<int2 *>(ws + w.off_keys);
+        hipError_t e = launch_swa_table(a, true, s.tokens, meta, table, keys, st);
+        if (e != hipSuccess) return e;
+        s.cu = sk.cu = a.cu, s.cuk = sk.cuk = a.cuk;
+        s.meta = meta, s.table = table;
+        sk.meta = meta + 2, sk.table = keys;
+    } else {
+        const FarParts fp = far_parts(a.T, a.Tk, a.window, a.sinks, far);
+        s.per_seq = (a.T + s.tokens - 1) / s.tokens;
+        sk.per_seq = (a.Tk + kSwaKeyTile - 1) / kSwaKeyTile + fp.parts;
+        units = (int64_t)s.per_seq * a.N;
+        key_units = (int64_t)sk.per_seq * a.N;
+        s.units = (int)units, sk.units = (int)key_units;
+        join = fp.parts > 0;
+    }
+    return swa_with<false>(a.dtype, a.D, [&](auto t, auto dim) {
+        using T = decltype(t);
+        constexpr int D = decltype(dim)::value, RB = Rows<T, D>::RB;
+        auto in = [](const void *p) { return static_cast<const T *>(p); };
+        auto out = [](void *p) { return static_cast<T *>(p); };
+        hipError_t e = hipSuccess;
+        if (units) {
+            ProfScope prof("gdn_swa_dq", st);
+            auto go = [&](auto waves) {
+                constexpr int NW = decltype(waves)::value, lds = 4 * kKeys * RB;
+                hipError_t x = swa_lds(swa_dq_kernel<T, D, NW>, lds);
+                if (x != hipSuccess) return x;
+                swa_dq_kernel<T, D, NW><<<(unsigned)((units * a.KV + 7) / 8 * 8), 64 * NW, lds, st>>>(
+                    s, in(a.q), in(a.k), in(a.v), in(a.o), a.lse, in(a.d_o), out(a.dq), dsum);
+                return hipGetLastError();
+            };
+            e = rows == 64 ? go(std::integral_constant<int, 2>{}) : go(std::integral_constant<int, 4>{});
+            if (e != hipSuccess) return e;
+        }
+        if (key_units) {
+            ProfScope prof("gdn_swa_dkv", st);
+            constexpr int lds = 4 * kRows * RB + 4 * kRows * 4;
+            e = swa_lds(swa_dkv_kernel<T, D>, lds);
+            if (e != hipSuccess) return e;
+            swa_dkv_kernel<T, D><<<(unsigned)((key_units * a.KV + 7) / 8 * 8), 256, lds, st>>>(
+                sk, far, in(a.q), in(a.k), in(a.v), a.lse, in(a.d_o), dsum, out(a.dk), out(a.dv), share);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        if (join) {
+            ProfScope prof("gdn_swa_sinks", st);
+            const dim3 grid((unsigned)(a.N * a.KV), (unsigned)((a.sinks * D + 255) / 256));
+            swa_sinks_kernel<T><<<grid, 256, 0, st>>>(s, far, D, share, out(a.dk), out(a.dv));
+            e = hipGetLastError();
+        }
+        return e;
+    });
+}
+
+}  // namespace gdn

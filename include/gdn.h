@@ -665,6 +665,27 @@ gdn_status gdn_swa_fwd(const gdn_swa_desc *desc, const void *q, const void *k, c
                        void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Backward pass.  With P = exp(s - lse) over the visible pairs and
+ * D = sum over d of d_o o,
+ *     dv_j = sum_i P_ij d_o_i      dS = P (d_o v - D)
+ *     dq_i = scale sum_j dS_ij k_j      dk_j = scale sum_i dS_ij q_i
+ * summed over the query heads that share a key head.
+ *
+ *   q, k, v, cu_seqlens, cu_seqlens_k   as for gdn_swa_fwd
+ *   o, lse        as gdn_swa_fwd gave them
+ *   d_o           [B, T, H, d]    dtype
+ *   dq            [B, T, H, d]    dtype (written)
+ *   dk, dv        [B, Tk, KV, d]  dtype (written)
+ *   workspace     at least gdn_swa_bwd_workspace_size bytes
+ * Every sum is taken in fp32 and in a fixed order: equal calls give equal bits.
+ * The outputs must not overlap each other, any input or the workspace.
+ * Errors: as gdn_chunk_bwd.
+ */
+gdn_status gdn_swa_bwd(const gdn_swa_desc *desc, const void *d_o, const void *q, const void *k, const void *v,
+                       const void *o, const float *lse, const int32_t *cu_seqlens, const int32_t *cu_seqlens_k,
+                       void *dq, void *dk, void *dv, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * Per-kernel timing for measurement harnesses (host-side bookkeeping only;
  * kernels are unchanged).  While enabled, every launch made by this library
  * is bracketed by a pair of HIP events recorded on the launch stream.
