@@ -19,6 +19,15 @@ linear recurrence, layer norm, and moves of resident states.
     y, mean, rstd = layernorm_fwd(x, weight=None, bias=None)
     dx, dweight, dbias = layernorm_bwd(dy, x, mean, rstd, weight=None)
     state_move(state, src, dst)                              # state updated in place
+
+And the other token mixer of hybrid stacks, attention with a sliding window and
+sinks, with its resident ring cache in the inputs' type or in 8 bits.
+
+    o, lse = swa_fwd(q, k, v, window, sinks=0, cu_seqlens=None, cu_seqlens_k=None)
+    dq, dk, dv = swa_bwd(d_o, q, k, v, o, lse, window, sinks=0, cu_seqlens=None, cu_seqlens_k=None)
+    o    = swa_step(cache, q, k, v, lengths, sinks=0, scales=None, slots=None)   # cache updated in place
+    cache_write(cache, k, v, lengths=None, sinks=0, scales=None, slots=None, cu_seqlens=None)
+    k, v = cache_read(cache, lengths, sinks=0, scales=None, slots=None, cu_seqlens=None)
 """
 from __future__ import annotations
 
@@ -31,13 +40,14 @@ import torch
 
 __all__ = ["GdnError", "chunk_fwd", "chunk_fwd_noalloc", "decode_step", "chunk_bwd", "chunk_fwd_workspace_size",
            "chunk_bwd_workspace_size", "chunk_fwd_check", "scan_fwd", "scan_bwd", "scan_step", "scan_workspace_size",
-           "layernorm_fwd", "layernorm_bwd", "layernorm_bwd_workspace_size", "state_move", "state_move_check", "load",
-           "lib_path", "profile", "CHUNK"]
+           "layernorm_fwd", "layernorm_bwd", "layernorm_bwd_workspace_size", "state_move", "state_move_check",
+           "swa_fwd", "swa_bwd", "swa_step", "swa_fwd_workspace_size", "swa_bwd_workspace_size", "cache_write",
+           "cache_read", "cache_check", "load", "lib_path", "profile", "CHUNK"]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CHUNK = 64
 
-GDN_FP32, GDN_BF16, GDN_FP16 = 0, 1, 2
+GDN_FP32, GDN_BF16, GDN_FP16, GDN_E4M3 = 0, 1, 2, 3
 GDN_QK_L2NORM = 1
 NOALLOC_SCRATCH_BYTES = 64 << 20   # GDN_NOALLOC_SCRATCH_BYTES in gdn.h
 _DT = {torch.float32: GDN_FP32, torch.bfloat16: GDN_BF16, torch.float16: GDN_FP16}
@@ -64,6 +74,10 @@ class SwaDesc(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int32) for name in ("batch", "seqlen", "keylen", "heads", "kv_heads", "dim", "num_seqs",
                                                     "window", "sinks", "dtype")] \
         + [("scale", ctypes.c_float), ("flags", ctypes.c_int32)]
+
+
+class CacheDesc(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("slots", "kv_heads", "window", "sinks", "dim", "dtype")]
 
 
 class ScanDesc(ctypes.Structure):
@@ -109,6 +123,7 @@ def load():
     lib.gdn_decode_step.restype = ctypes.c_int
     lib.gdn_decode_step.argtypes = [i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
     i64, scan_desc, swa_desc = ctypes.c_int64, ctypes.POINTER(ScanDesc), ctypes.POINTER(SwaDesc)
+    cache_desc = ctypes.POINTER(CacheDesc)
     for name, args in {
             "gdn_scan_workspace_size": [scan_desc, ctypes.POINTER(sz)],
             "gdn_scan_fwd": [scan_desc] + [vp] * 7 + [sz, vp],
@@ -121,7 +136,11 @@ def load():
             "gdn_swa_fwd_workspace_size": [swa_desc, ctypes.POINTER(sz)],
             "gdn_swa_bwd_workspace_size": [swa_desc, ctypes.POINTER(sz)],
             "gdn_swa_fwd": [swa_desc] + [vp] * 8 + [sz, vp],
-            "gdn_swa_bwd": [swa_desc] + [vp] * 12 + [sz, vp]}.items():
+            "gdn_swa_bwd": [swa_desc] + [vp] * 12 + [sz, vp],
+            "gdn_swa_step_workspace_size": [cache_desc, i32, i32, ctypes.POINTER(sz)],
+            "gdn_swa_step": [cache_desc, i32, i32, i32, ctypes.c_float] + [vp] * 9 + [sz, vp, vp],
+            "gdn_cache_write": [cache_desc, i32, i32, i32] + [vp] * 9,
+            "gdn_cache_read": [cache_desc, i32, i32, i32] + [vp] * 9}.items():
         getattr(lib, name).restype, getattr(lib, name).argtypes = ctypes.c_int, args
     lib.gdn_profile_enable.restype = ctypes.c_int
     lib.gdn_profile_enable.argtypes = [i32]
@@ -681,6 +700,151 @@ def swa_bwd(d_o, q, k, v, o, lse, window, sinks=0, cu_seqlens=None, cu_seqlens_k
     _call("gdn_swa_bwd", dev, desc, _addr(d_o), _addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), _addr(cu_seqlens),
           _addr(cu_k), _addr(dq), _addr(dk), _addr(dv), _addr(workspace), size)
     return dq, dk, dv
+
+
+_CACHE_DT = {**_DT, torch.float8_e4m3fn: GDN_E4M3}
+
+
+@functools.lru_cache(maxsize=256)
+def _cache_desc(shape, dtype, sinks):
+    window = shape[3] - sinks
+    if shape[0] != 2 or sinks < 0 or window < 1:
+        raise ValueError(f"cache must be [2, slots, kv heads, {sinks} sinks + window, d], got {shape}")
+    return CacheDesc(*shape[1:3], window, sinks, shape[4], _CACHE_DT[dtype])
+
+
+def _cache_call(cache, scales, slots, lengths, sinks):
+    """Device and descriptor of a call on `cache`."""
+    dev = _cuda(cache, "cache")
+    if cache.dtype not in _CACHE_DT or cache.dim() != 5 or not cache.is_contiguous():
+        _need(cache, "cache", tuple(_CACHE_DT), dev, 5)
+    if scales is not None:
+        _shaped(scales, "scales", tuple(cache.shape[:4]), (torch.float32,), dev)
+    if lengths is not None:
+        _need(lengths, "lengths", (torch.int32,), dev, 1)
+        if slots is not None:
+            _shaped(slots, "slots", tuple(lengths.shape), (torch.int32,), dev)
+    elif slots is not None:
+        _need(slots, "slots", (torch.int32,), dev, 1)
+    return dev, _cache_desc(tuple(cache.shape), cache.dtype, sinks)
+
+
+def _cache_tokens(desc, k, v, lengths, slots, cu_seqlens, status, dev):
+    """Number of sequences and tokens of a cache_write or cache_read call."""
+    _need(k, "k", _FLOATS, dev, 4)
+    B, T, KV, d = shape = tuple(k.shape)
+    if (KV, d) != (desc.kv_heads, desc.dim):
+        raise ValueError(f"k must be [.., {desc.kv_heads}, {desc.dim}], got {shape}")
+    _shaped(v, "v", shape, (k.dtype,), dev)
+    if cu_seqlens is None:
+        N = B
+    else:
+        _need(cu_seqlens, "cu_seqlens", (torch.int32,), dev, 1)
+        if B != 1:
+            raise ValueError(f"cu_seqlens needs one row of tokens, got {B}")
+        N = cu_seqlens.shape[0] - 1
+    for name, t in (("lengths", lengths), ("slots", slots)):
+        if t is not None and t.shape[0] != N:
+            raise ValueError(f"{name} must have {N} entries, got {t.shape[0]}")
+    if status is not None:
+        _shaped(status, "status", (2,), (torch.int32,), dev)
+    return N, B * T
+
+
+def cache_write(cache, k, v, lengths=None, sinks=0, scales=None, slots=None, cu_seqlens=None, *, status=None):
+    """Tokens into the resident cache of windowed attention, in place.
+
+    cache [2, slots, KV, sinks + window, d] (fp32/bf16/fp16, k and v's dtype; or
+    float8_e4m3fn with scales [2, slots, KV, sinks + window] fp32): the sinks'
+    rows, then a ring.  k, v [B,T,KV,d]: T tokens for each of B sequences, or a
+    packed batch with cu_seqlens int32 [N+1].  lengths int32 [N]: tokens that
+    each sequence has already (None: 0); not changed.  slots int32 [N]: where
+    each sequence is (None: in order), -1 to leave it out.  Bad indices leave
+    the cache as it was, and cache_check tells of them if `status` (int32 [2] on
+    the device) was given.  Returns cache.
+    """
+    dev, desc = _cache_call(cache, scales, slots, lengths, sinks)
+    N, T = _cache_tokens(desc, k, v, lengths, slots, cu_seqlens, status, dev)
+    _call("gdn_cache_write", dev, desc, N, T, _DT[k.dtype], _addr(k), _addr(v), _addr(cu_seqlens), _addr(lengths),
+          _addr(slots), _addr(cache), _addr(scales), _addr(status))
+    return cache
+
+
+def cache_read(cache, lengths, sinks=0, scales=None, slots=None, cu_seqlens=None, *, out_dtype=None, k=None, v=None,
+               status=None):
+    """What the cache holds of each sequence, in the order of positions: its
+    first `sinks` tokens and its last `window`, as many as it has.
+
+    cache, lengths, sinks, scales, slots as for cache_write.  k, v: where the
+    rows go, [N,R,KV,d] or with cu_seqlens [1,T,KV,d], each sequence's from its
+    part's beginning on; rows behind them are left as they are.  Without them
+    they are allocated with sinks + window rows a sequence (out_dtype: None for
+    the cache's own, bf16 for an 8-bit one).  Returns (k, v).
+    """
+    dev, desc = _cache_call(cache, scales, slots, lengths, sinks)
+    if lengths is None:
+        raise ValueError("lengths is needed")
+    if k is None or v is None:
+        if k is not None or v is not None or cu_seqlens is not None:
+            raise ValueError("k and v go together, and with cu_seqlens both are needed")
+        if out_dtype is None:
+            out_dtype = torch.bfloat16 if desc.dtype == GDN_E4M3 else cache.dtype
+        k, v = (torch.empty((lengths.shape[0], cache.shape[3], *(cache.shape[i] for i in (2, 4))), dtype=out_dtype,
+                            device=dev) for _ in range(2))
+    N, T = _cache_tokens(desc, k, v, lengths, slots, cu_seqlens, status, dev)
+    _call("gdn_cache_read", dev, desc, N, T, _DT[k.dtype], _addr(cache), _addr(scales), _addr(lengths), _addr(slots),
+          _addr(cu_seqlens), _addr(k), _addr(v), _addr(status))
+    return k, v
+
+
+@functools.lru_cache(maxsize=256)
+def _step_workspace(shape, dtype, sinks, N, H) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().gdn_swa_step_workspace_size(ctypes.byref(_cache_desc(shape, dtype, sinks)), N, H, ctypes.byref(n)))
+    return int(n.value)
+
+
+def swa_step(cache, q, k, v, lengths, sinks=0, scales=None, slots=None, *, scale=None, o=None, workspace=None,
+             status=None):
+    """One token of windowed attention for N resident sequences: k, v [N,KV,d]
+    go into the cache (in place) at position lengths[n], and q [N,H,d] attends
+    to what it then holds.  cache, lengths, sinks, scales, slots as for
+    cache_write; scale: None for 1 / sqrt(d).  lengths is not changed: add one
+    when all layers have run.  A sequence with slot -1 is left out, its o is
+    zeros.  Returns o [N,H,d]."""
+    dev, desc = _cache_call(cache, scales, slots, lengths, sinks)
+    _need(q, "q", _FLOATS, dev, 3)
+    N, H, d = shape = tuple(q.shape)
+    _shaped(k, "k", (N, desc.kv_heads, d), (q.dtype,), dev)
+    _shaped(v, "v", (N, desc.kv_heads, d), (q.dtype,), dev)
+    if d != desc.dim:
+        raise ValueError(f"q must be [N, H, {desc.dim}], got {shape}")
+    if lengths is None or lengths.shape[0] != N:
+        raise ValueError(f"lengths must have {N} entries")
+    if o is None:
+        o = torch.empty(shape, dtype=q.dtype, device=dev)
+    else:
+        _shaped(o, "o", shape, (q.dtype,), dev)
+    if status is not None:
+        _shaped(status, "status", (2,), (torch.int32,), dev)
+    need = _step_workspace(tuple(cache.shape), cache.dtype, sinks, N, H)
+    size = 0
+    if need:
+        workspace, size = _workspace(workspace, need, dev)
+    else:
+        workspace = None
+    _call("gdn_swa_step", dev, desc, N, H, _DT[q.dtype], d ** -0.5 if scale is None else scale, _addr(q), _addr(k),
+          _addr(v), _addr(lengths), _addr(slots), _addr(cache), _addr(scales), _addr(o), _addr(workspace), size,
+          _addr(status))
+    return o
+
+
+def cache_check(status: torch.Tensor) -> int:
+    """Synchronise and return the code that cache_write, cache_read or swa_step
+    left in `status`: 0, 1 to 3 for malformed cu_seqlens, 4 for a slot out of
+    range, 5 for a slot given twice, 6 for a length out of range, 7 for a
+    sequence with more rows to read than room for them."""
+    return chunk_fwd_check(status)
 
 
 class profile:

@@ -16,7 +16,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgdn.so")
 SOURCES = ["gdn_api.cpp", "gdn_ops_api.cpp", "gdn_chunk.hip", "gdn_decode.hip", "gdn_bwd.hip", "gdn_scan.hip",
            "gdn_norm.hip", "gdn_pages.hip", "gdn_swa_api.cpp", "gdn_swa.hip",
-           "gdn_swa_bwd.hip"]
+           "gdn_swa_bwd.hip", "gdn_swa_step.hip", "gdn_cache.hip"]
 ARCH = os.environ.get("GDN_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

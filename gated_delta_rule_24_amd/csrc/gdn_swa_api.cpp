@@ -2,6 +2,7 @@
 // workspace sizing.  Declarations and the full contract are in include/gdn.h.
 // Every check runs before anything is enqueued.
 #include "gdn.h"
+#include "gdn_cache.h"
 #include "gdn_check.h"
 #include "gdn_swa.h"
 
@@ -69,6 +70,92 @@ gdn_status swa_size(const gdn_swa_desc *desc, size_t *bytes, bool bwd) {
     if (s != GDN_OK) return s;
     *bytes = swa_workspace_layout(swa_args(*desc), bwd).total;
     return ok();
+}
+
+size_t cache_dtype_size(int32_t d) { return d == GDN_E4M3 ? 1 : dtype_size(d); }
+
+gdn_status check_cache_desc(const gdn_cache_desc *d, int32_t num_seqs) {
+    if (!d) return fail(GDN_ERR_NULL, "desc is NULL");
+    if (!valid_dtype(d->dtype) && d->dtype != GDN_E4M3) return fail(GDN_ERR_DTYPE, "unknown dtype code %d", d->dtype);
+    if (d->slots < 1 || d->kv_heads < 1 || d->window < 1 || d->sinks < 0 || num_seqs < 0)
+        return fail(GDN_ERR_SHAPE, "need slots >= 1, kv_heads >= 1, window >= 1, sinks >= 0, num_seqs >= 0 (got %d, %d, "
+                    "%d, %d, %d)", d->slots, d->kv_heads, d->window, d->sinks, num_seqs);
+    if (d->slots > kCacheMaxSlots || d->kv_heads > 1024 || num_seqs > kCacheMaxSeqs)
+        return fail(GDN_ERR_UNSUPPORTED, "slots %d, kv_heads %d, num_seqs %d not built (at most %d, 1024, %d)", d->slots,
+                    d->kv_heads, num_seqs, kCacheMaxSlots, kCacheMaxSeqs);
+    if (!(d->dim == 32 || d->dim == 64 || d->dim == 128 || d->dim == 256))
+        return fail(GDN_ERR_UNSUPPORTED, "dim %d not built (32, 64, 128, 256)", d->dim);
+    if (d->sinks > kSwaMaxSinks)
+        return fail(GDN_ERR_UNSUPPORTED, "sinks %d not built (at most %d)", d->sinks, kSwaMaxSinks);
+    if ((int64_t)d->window + d->sinks >= (1 << 28)) return fail(GDN_ERR_UNSUPPORTED, "sinks + window too large");
+    return GDN_OK;
+}
+
+// Type of a call's tensors: the cache's own, or any beside 8 bits.
+gdn_status check_cache_type(const gdn_cache_desc &d, int32_t dtype) {
+    if (!valid_dtype(dtype)) return fail(GDN_ERR_DTYPE, "unknown dtype code %d", dtype);
+    if (d.dtype != GDN_E4M3 && dtype != d.dtype)
+        return fail(GDN_ERR_UNSUPPORTED, "dtype %d on a cache of dtype %d not built", dtype, d.dtype);
+    return GDN_OK;
+}
+
+gdn_status check_cache_seqs(const gdn_cache_desc &d, int32_t num_seqs, const int32_t *slots, const float *scales) {
+    if (!slots && num_seqs > d.slots)
+        return fail(GDN_ERR_SHAPE, "%d sequences on %d slots need slots", num_seqs, d.slots);
+    if (!scales != (d.dtype != GDN_E4M3))
+        return fail(d.dtype == GDN_E4M3 ? GDN_ERR_NULL : GDN_ERR_UNSUPPORTED, "scales go with an E4M3 cache alone");
+    return GDN_OK;
+}
+
+CacheArgs cache_args(const gdn_cache_desc &d, int32_t num_seqs, int32_t tokens, int32_t dtype) {
+    CacheArgs a{};
+    a.P = d.slots, a.KV = d.kv_heads, a.window = d.window, a.sinks = d.sinks, a.D = d.dim, a.cache_dtype = d.dtype;
+    a.N = num_seqs, a.tokens = tokens, a.dtype = dtype;
+    return a;
+}
+
+size_t cache_rows(const gdn_cache_desc &d) { return 2 * (size_t)d.slots * d.kv_heads * ((size_t)d.window + d.sinks); }
+
+// gdn_cache_write and gdn_cache_read: the same checks, another direction.
+gdn_status cache_call(const gdn_cache_desc *desc, int32_t num_seqs, int32_t tokens, int32_t dtype, const void *k,
+                      const void *v, const int32_t *cu_seqlens, const int32_t *lengths, const int32_t *slots,
+                      const void *cache, const float *scales, int32_t *status, bool read, hipStream_t stream) {
+    gdn_status s = check_cache_desc(desc, num_seqs);
+    if (s != GDN_OK) return s;
+    const gdn_cache_desc &d = *desc;
+    s = check_cache_type(d, dtype);
+    if (s != GDN_OK) return s;
+    if (tokens < 0 || tokens >= (1 << 30)) return fail(GDN_ERR_SHAPE, "tokens %d out of range", tokens);
+    if (!cu_seqlens && (num_seqs ? tokens % num_seqs : tokens))
+        return fail(GDN_ERR_SHAPE, "without cu_seqlens tokens %d must be a multiple of num_seqs %d", tokens, num_seqs);
+    s = check_cache_seqs(d, num_seqs, slots, scales);
+    if (s != GDN_OK) return s;
+    const size_t moved = (size_t)tokens * d.kv_heads * d.dim * dtype_size(dtype), idx = 4 * (size_t)num_seqs;
+    const size_t rows = cache_rows(d);
+    const bool some = num_seqs > 0;
+    const Arg args[] = {{"k", k, moved, some && tokens > 0, read, 16},
+                        {"v", v, moved, some && tokens > 0, read, 16},
+                        {"cu_seqlens", cu_seqlens, idx + 4, false, false, 4},
+                        {"lengths", lengths, idx, some && read, false, 4},
+                        {"slots", slots, idx, false, false, 4},
+                        {"cache", cache, rows * d.dim * cache_dtype_size(d.dtype), some, !read, 16},
+                        {"scales", scales, rows * 4, false, !read, 4},
+                        {"status", status, 8, false, true, 4}};
+    s = check_args(args, 8);
+    if (s == GDN_OK) s = check_overlap(args, 8);
+    if (s != GDN_OK) return s;
+    if (!some && !status) return ok();
+    CacheArgs a = cache_args(d, num_seqs, tokens, dtype);
+    a.cache = const_cast<void *>(cache), a.scales = const_cast<float *>(scales);
+    a.lengths = lengths, a.slots = slots, a.cu = cu_seqlens, a.k = k, a.v = v, a.status = status;
+    hipError_t err = read ? launch_cache_read(a, stream) : launch_cache_write(a, stream);
+    if (err != hipSuccess) return hip_fail(err, read ? "gdn_cache_read launch" : "gdn_cache_write launch");
+    return ok();
+}
+
+gdn_status check_step(const gdn_cache_desc *desc, int32_t num_seqs, int32_t heads) {
+    gdn_status s = check_cache_desc(desc, num_seqs);
+    return s == GDN_OK ? check_heads(heads, desc->kv_heads) : s;
 }
 
 }  // namespace
@@ -139,6 +226,75 @@ gdn_status gdn_swa_bwd(const gdn_swa_desc *desc, const void *d_o, const void *q,
     a.dq = dq, a.dk = dk, a.dv = dv, a.workspace = workspace;
     hipError_t err = launch_swa_bwd(a, stream);
     if (err != hipSuccess) return hip_fail(err, "gdn_swa_bwd launch");
+    return ok();
+}
+
+gdn_status gdn_cache_write(const gdn_cache_desc *desc, int32_t num_seqs, int32_t tokens, int32_t in_dtype,
+                           const void *k, const void *v, const int32_t *cu_seqlens, const int32_t *lengths,
+                           const int32_t *slots, void *cache, float *scales, int32_t *status, hipStream_t stream) {
+    return cache_call(desc, num_seqs, tokens, in_dtype, k, v, cu_seqlens, lengths, slots, cache, scales, status, false,
+                      stream);
+}
+
+gdn_status gdn_cache_read(const gdn_cache_desc *desc, int32_t num_seqs, int32_t tokens, int32_t out_dtype,
+                          const void *cache, const float *scales, const int32_t *lengths, const int32_t *slots,
+                          const int32_t *cu_seqlens, void *k, void *v, int32_t *status, hipStream_t stream) {
+    return cache_call(desc, num_seqs, tokens, out_dtype, k, v, cu_seqlens, lengths, slots, cache, scales, status, true,
+                      stream);
+}
+
+gdn_status gdn_swa_step_workspace_size(const gdn_cache_desc *desc, int32_t num_seqs, int32_t heads, size_t *bytes) {
+    if (!bytes) return fail(GDN_ERR_NULL, "bytes is NULL");
+    gdn_status s = check_step(desc, num_seqs, heads);
+    if (s != GDN_OK) return s;
+    SwaStepArgs a{};
+    a.c = cache_args(*desc, num_seqs, num_seqs, GDN_FP32);
+    a.H = heads;
+    *bytes = swa_step_workspace(a);
+    return ok();
+}
+
+gdn_status gdn_swa_step(const gdn_cache_desc *desc, int32_t num_seqs, int32_t heads, int32_t dtype, float scale,
+                        const void *q, const void *k, const void *v, const int32_t *lengths, const int32_t *slots,
+                        void *cache, float *scales, void *o, void *workspace, size_t workspace_bytes,
+                        int32_t *status, hipStream_t stream) {
+    gdn_status s = check_step(desc, num_seqs, heads);
+    if (s != GDN_OK) return s;
+    const gdn_cache_desc &d = *desc;
+    s = check_cache_type(d, dtype);
+    if (s != GDN_OK) return s;
+    if (dtype == GDN_FP32 && d.dim > 128) return fail(GDN_ERR_UNSUPPORTED, "dim %d not built with FP32", d.dim);
+    if (!(std::isfinite(scale) && scale > 0.f)) return fail(GDN_ERR_UNSUPPORTED, "scale must be finite and > 0");
+    s = check_cache_seqs(d, num_seqs, slots, scales);
+    if (s != GDN_OK) return s;
+    SwaStepArgs a{};
+    a.c = cache_args(d, num_seqs, num_seqs, dtype);
+    a.H = heads, a.scale = scale;
+    const size_t need = swa_step_workspace(a);
+    if (need && !workspace) return fail(GDN_ERR_WORKSPACE, "workspace is NULL");
+    if (need && workspace_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, this call needs %zu", workspace_bytes, need);
+    const size_t row = (size_t)d.dim * dtype_size(dtype), idx = 4 * (size_t)num_seqs, rows = cache_rows(d);
+    const bool some = num_seqs > 0;
+    const Arg args[] = {{"q", q, (size_t)num_seqs * heads * row, some, false, 16},
+                        {"k", k, (size_t)num_seqs * d.kv_heads * row, some, false, 16},
+                        {"v", v, (size_t)num_seqs * d.kv_heads * row, some, false, 16},
+                        {"lengths", lengths, idx, some, false, 4},
+                        {"slots", slots, idx, false, false, 4},
+                        {"cache", cache, rows * d.dim * cache_dtype_size(d.dtype), some, true, 16},
+                        {"scales", scales, rows * 4, false, true, 4},
+                        {"o", o, (size_t)num_seqs * heads * row, some, true, 16},
+                        {"workspace", workspace, need, false, true, 16},
+                        {"status", status, 8, false, true, 4}};
+    s = check_args(args, 10);
+    if (s == GDN_OK) s = check_overlap(args, 10);
+    if (s != GDN_OK) return s;
+    if (!some && !status) return ok();
+    a.c.cache = cache, a.c.scales = scales, a.c.lengths = lengths, a.c.slots = slots, a.c.k = k, a.c.v = v;
+    a.c.status = status;
+    a.q = q, a.o = o, a.workspace = workspace;
+    hipError_t err = launch_swa_step(a, stream);
+    if (err != hipSuccess) return hip_fail(err, "gdn_swa_step launch");
     return ok();
 }
 

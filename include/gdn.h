@@ -318,8 +318,9 @@ gdn_status gdn_chunk_bwd(const gdn_chunk_desc *desc,
 
 /*
  * Result of the device-side check of the last gdn_chunk_fwd (or packed
- * gdn_chunk_bwd, gdn_scan_fwd, gdn_scan_bwd) that used `workspace`, or of
- * the gdn_state_move that wrote it as its status (codes there).  Synchronises `stream`, then writes 0 (valid) or a
+ * gdn_chunk_bwd, gdn_scan_fwd, gdn_scan_bwd, gdn_swa_fwd, gdn_swa_bwd) that
+ * used `workspace`, or of the gdn_state_move, gdn_cache_write, gdn_cache_read or
+ * gdn_swa_step that wrote it as its status (codes there).  Synchronises `stream`, then writes 0 (valid) or a
  * non-zero code (1: cu[0] != 0, 2: decreasing offsets, 3: cu[N] != T) to
  * *code (host pointer).  Returns GDN_ERR_DEVICE_INPUT when the code is
  * non-zero, GDN_OK otherwise.
@@ -684,6 +685,123 @@ gdn_status gdn_swa_fwd(const gdn_swa_desc *desc, const void *q, const void *k, c
 gdn_status gdn_swa_bwd(const gdn_swa_desc *desc, const void *d_o, const void *q, const void *k, const void *v,
                        const void *o, const float *lse, const int32_t *cu_seqlens, const int32_t *cu_seqlens_k,
                        void *dq, void *dk, void *dv, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The resident cache of windowed attention: for each slot and key head the
+ * rows of the `sinks` first positions, and behind them a ring of the last
+ * `window` ones.  Position p of a sequence sits in row p for p < sinks, else in
+ * row sinks + (p - sinks) mod window: what a sequence still sees, and no more,
+ * whatever its length.
+ *
+ *   cache   [2, P, KV, sinks + window, d]  keys, then values; of type dtype
+ *   scales  [2, P, KV, sinks + window]     fp32, with GDN_E4M3 only (else NULL)
+ *
+ * Unwritten rows are never read: a cache need not be initialised.  A slot is
+ * moved as one page of gdn_state_move with layers = 2 (twice as many for
+ * several layers of a model), the scales likewise.
+ *
+ * GDN_E4M3: a row of d values is held as e4m3 (OCP) numbers with one power of
+ * two, scale = 2^e for the least e >= -126 with max|x| <= 448 * 2^e: value x
+ * is held as x / scale rounded to nearest, ties to even, so that it is off by
+ * at most 2^-4 |x| or 2^-10 scale, whichever is more.  A row with an infinity or a
+ * NaN reads back as NaN throughout.
+ *
+ *   slots     P: 1..65536
+ *   kv_heads  KV: 1..1024
+ *   window    W >= 1      sinks  S: 0..128      S + W < 2^28
+ *   dim       d: 32, 64, 128 or 256
+ *   dtype     FP32, BF16, FP16, or E4M3
+ *
+ * Arguments of the calls on a cache:
+ *   num_seqs  N: 0..4096 sequences of the call
+ *   lengths   int32 [N]: tokens that each sequence has before the call, 0 .. 2^30
+ *             - 1.  Not changed: the layers of a model share it, and their caller
+ *             adds to it when all have run.
+ *   slots     int32 [N] or NULL (sequence n in slot n, N <= P): each a slot, no
+ *             two alike, or -1: the sequence is left out (a padded batch).
+ *   status    int32 [2] or NULL (written): {N, code}.  Offsets, slots and lengths
+ *             are device data and are checked on the device: code 1 to 3 for
+ *             cu_seqlens as for gdn_chunk_fwd, 4 for a slot out of range, 5 for a
+ *             slot given twice, 6 for a length out of range, 7 for a sequence with
+ *             more rows to read than room for them; 0 otherwise.
+ *             gdn_chunk_fwd_check(status, ...) reads it.
+ * Alignment: cache, k, v, q, o 16 bytes; scales, lengths, slots, cu_seqlens and
+ * status 4.
+ */
+typedef struct {
+    int32_t slots;
+    int32_t kv_heads;
+    int32_t window;
+    int32_t sinks;
+    int32_t dim;
+    int32_t dtype;   /* gdn_dtype */
+} gdn_cache_desc;
+
+/*
+ * Writes tokens to the cache, as if one after the other: of more tokens than a
+ * sequence sees, those that no query will see any more are not written.
+ *
+ *   tokens      T >= 0: tokens of the call in all (without cu_seqlens T / N a
+ *               sequence, a multiple of N); T < 2^30
+ *   in_dtype    of k and v: the cache's, or any with E4M3
+ *   k, v        [T, KV, d]  in_dtype
+ *   cu_seqlens  int32 [N+1] or NULL, as for gdn_chunk_fwd
+ *   lengths     may be NULL (all 0)
+ * With a code other than 0 nothing but the status is written.
+ * k, v, the indices, the cache, the scales and the status must not overlap.
+ * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_ALIGN,
+ * GDN_ERR_UNSUPPORTED, GDN_ERR_ALIAS, GDN_ERR_HIP.
+ */
+gdn_status gdn_cache_write(const gdn_cache_desc *desc, int32_t num_seqs, int32_t tokens, int32_t in_dtype,
+                           const void *k, const void *v, const int32_t *cu_seqlens, const int32_t *lengths,
+                           const int32_t *slots, void *cache, float *scales, int32_t *status, hipStream_t stream);
+
+/*
+ * Reads back what the cache holds, in the order of positions: of sequence n its
+ * min(length, sinks + window) rows, the sinks first, to the first rows of its part
+ * of k and v.  The rows behind them keep what they hold: with the next tokens'
+ * keys there they are the keys of a gdn_swa_fwd call that goes on.
+ *
+ *   tokens, cu_seqlens  as for gdn_cache_write: the rows of k and v
+ *   out_dtype           of k and v: the cache's, or any with E4M3 (the value times
+ *                       its scale, rounded once)
+ *   k, v                [T, KV, d]  out_dtype (written)
+ * With a code other than 0 nothing but the status is written.
+ * Errors: as gdn_cache_write.
+ */
+gdn_status gdn_cache_read(const gdn_cache_desc *desc, int32_t num_seqs, int32_t tokens, int32_t out_dtype,
+                          const void *cache, const float *scales, const int32_t *lengths, const int32_t *slots,
+                          const int32_t *cu_seqlens, void *k, void *v, int32_t *status, hipStream_t stream);
+
+/* Workspace of gdn_swa_step in bytes, written to *bytes (host pointer).  Need
+ * not be initialised.  Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE,
+ * GDN_ERR_UNSUPPORTED. */
+gdn_status gdn_swa_step_workspace_size(const gdn_cache_desc *desc, int32_t num_seqs, int32_t heads, size_t *bytes);
+
+/*
+ * One token of each of N resident sequences: its key and value are written to
+ * the cache at position lengths[n], and its queries attend to what the cache
+ * then holds (in 8 bits, the new row as it was rounded).
+ *
+ *   heads      H, as for gdn_swa_fwd
+ *   dtype      of q, k, v and o: the cache's, or any with E4M3 (FP32: d <= 128)
+ *   scale      finite and > 0
+ *   q          [N, H, d]   dtype
+ *   k, v       [N, KV, d]  dtype
+ *   o          [N, H, d]   dtype (written); zeros for a sequence that is left out
+ *   workspace  at least gdn_swa_step_workspace_size bytes, 16-byte aligned; may be
+ *              NULL where that is 0
+ * A sequence whose slot is out of range or another one's as well, or whose length
+ * is out of range, is left out; the status has a code then.
+ * o, the cache, the scales, the workspace and the status must not overlap each
+ * other or an input.
+ * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_ALIGN,
+ * GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE, GDN_ERR_ALIAS, GDN_ERR_HIP.
+ */
+gdn_status gdn_swa_step(const gdn_cache_desc *desc, int32_t num_seqs, int32_t heads, int32_t dtype, float scale,
+                        const void *q, const void *k, const void *v, const int32_t *lengths, const int32_t *slots,
+                        void *cache, float *scales, void *o, void *workspace, size_t workspace_bytes,
+                        int32_t *status, hipStream_t stream);
 
 /*
  * Per-kernel timing for measurement harnesses (host-side bookkeeping only;

@@ -121,7 +121,8 @@ def cache_read(cache, lengths, sinks, scales=None, slots=None):
         if at < 0:
             out.append(None)
             continue
-        rows = [cache_row(p, window, sinks) for p in range(length) if p < sinks or p >= length - window]
+        seen = [*range(min(sinks, length)), *range(max(sinks, length - window), length)]
+        rows = [cache_row(p, window, sinks) for p in seen]
         both = []
         for side in range(2):
             x = cache[side, at].astype(np.float64)[:, rows]
