@@ -48,8 +48,8 @@ hipError_t launch_swa_bwd(const SwaArgs &a, hipStream_t stream);
 inline int swa_far_chunk(int window) { return window + kSwaKeyTile < 1024 ? 1024 : window + kSwaKeyTile; }
 
 // Builds the tables of units of a packed batch, int2 {sequence, unit of the
-// sequence}: tiles of `tokens` query tokens, and for the backward pass the key
-// tiles, each sequence's followed by the far parts of its sinks.  meta: {units of
+// sequence}: tiles of `tokens` query tokens, and for the backward pass the far
+// parts of the sinks and then the key tiles.  meta: {units of
 // the first table, code of the offsets' check, units of the second, the code}.
 hipError_t launch_swa_table(const SwaArgs &a, bool bwd, int tokens, int32_t *meta, int2 *rows, int2 *keys,
                             hipStream_t stream);
@@ -67,25 +67,44 @@ struct SwaShape {
 };
 
 struct SwaUnit {
-    int unit, hk;                    // unit of the sequence, key head
+    int unit, hk, role;              // unit of the sequence, key head, which of `roles`
     int64_t q0, k0;                  // the sequence's first query and key
     int Lq, Lk, n;
 };
 
 // The unit of this block; false: none.  Blocks go to the 8 XCDs in turn: each
 // XCD takes a contiguous share of the units, neighbouring tiles of one head, so
-// that the keys that they share are in one L2.
-__device__ __forceinline__ bool swa_find(const SwaShape &s, SwaUnit &u) {
+// that the keys that they share are in one L2.  last_first: in falling order, as
+// later queries see more keys and the longest units should begin first.  ROLES
+// blocks in a row have the same unit, each another part of its work.
+template <int ROLES = 1>
+__device__ __forceinline__ bool swa_find(const SwaShape &s, bool last_first, SwaUnit &u) {
     int units = s.units;
     if (s.cu) {
         if (s.meta[1]) return false;
         units = s.meta[0];
     }
-    const int64_t total = (int64_t)units * s.KV;
-    const int64_t per = (total + 7) / 8, i = blockIdx.x >> 3, at = (blockIdx.x & 7) * per + i;
+    const int64_t total = (int64_t)units * s.KV * ROLES;
+    const int64_t per = (total + 7) / 8, i = blockIdx.x >> 3;
+    int64_t at = (blockIdx.x & 7) * per + i;
     if (i >= per || at >= total) return false;
+    const int pairs = s.cu ? 0 : units / max(s.per_seq, 1) * s.KV;
+    if (pairs % 8 == 0 && !s.cu) {   // whole (sequence, key head) pairs to an XCD: the longest units of all of them first
+        const int share = pairs / 8 * ROLES;
+        const int x = (int)(i / share), y = (int)(i - (int64_t)x * share);
+        const int pair = (blockIdx.x & 7) * (pairs / 8) + y / ROLES;
+        u.role = y % ROLES;
+        u.hk = pair % s.KV;
+        u.n = pair / s.KV;
+        u.unit = last_first ? s.per_seq - 1 - x : x;
+        u.q0 = (int64_t)u.n * s.T, u.Lq = s.T;
+        u.k0 = (int64_t)u.n * s.Tk, u.Lk = s.Tk;
+        return true;
+    }
+    u.role = (int)(at % ROLES);
+    at /= ROLES;
     u.hk = (int)(at / units);
-    const int x = units - 1 - (int)(at - (int64_t)u.hk * units);   // later queries see more: first
+    const int y = (int)(at - (int64_t)u.hk * units), x = last_first ? units - 1 - y : y;
     if (s.cu) {
         const int2 e = s.table[x];
         u.n = e.x;
@@ -140,21 +159,24 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 __device__ __forceinline__ uint32_t lds_addr(const void *p) { return (uint32_t)(uintptr_t)p; }
 
-// Rows of D elements in LDS, each RB bytes, their 32-byte pairs of chunks
-// permuted by the row so that neither eight rows at one chunk nor a transposing
-// read of four rows meets a bank twice.
+// Rows of D elements in LDS, each RB bytes, their 16-byte chunks permuted by the
+// row.  Of the 256 bytes across the banks the chunk (row, c) takes c ^ swz(row) (and
+// a place by the row where several fit): sixteen rows at one chunk meet no bank
+// twice, and neither do the four rows by 64 bytes of half a transposing read.
 template <typename T, int D>
 struct Rows {
     static constexpr int RB = D * (int)sizeof(T);
     static constexpr int NS = RB / 32;                    // chunk pairs, steps of a product over D
     static constexpr int RPL = RB >= 256 ? 1 : 256 / RB;  // rows across the banks
-    static constexpr int SW = (NS < 8 ? NS : 8) - 1;
     static constexpr int ND = D / 32;                     // tiles along D
     static constexpr bool F32 = std::is_same_v<T, float>;
-    __device__ __forceinline__ static int swz(int row) { return (row / RPL) & SW; }
-    __device__ __forceinline__ static int chunk_off(int row, int chunk) {
-        return row * RB + (((chunk >> 1) ^ swz(row)) << 5) + ((chunk & 1) << 4);
+    __device__ __forceinline__ static int swz(int row) {  // swz(row + 8) = swz(row) ^ 2, swz(row + 16) = swz(row)
+        const int x = row / RPL;
+        return RPL == 1 ? (x & 3) << 2 | (x >> 2 & 3) : RPL == 2 ? (x & 1) << 2 | (x >> 1 & 3) : x & 3;
     }
+    __device__ __forceinline__ static int chunk_off(int row, int chunk) { return row * RB + ((chunk ^ swz(row)) << 4); }
+    // The chunk that lies at byte b of a tile.
+    __device__ __forceinline__ static int chunk_at(int b) { return (b % RB / 16) ^ swz(b / RB); }
     // What a lane's reads start from.  fresh(): the same values, which the compiler
     // takes for new ones, so that it forms addresses where they are used instead of
     // keeping all of them in registers.
@@ -162,9 +184,9 @@ struct Rows {
         int l, row, col;
         __device__ __forceinline__ Lane() {
             l = threadIdx.x & 63;
-            row = (l & 31) * RB + (swz(l & 31) << 5) + ((l >> 5) << 4);
-            const int sub = (l >> 4) & 1, s = l & 15, r = 4 * (l >> 5) + (s >> 2);
-            col = r * RB + ((sub ^ swz(r)) << 5) + ((s & 3) << 3);
+            row = chunk_off(l & 31, l >> 5);
+            const int s = l & 15;
+            col = chunk_off(4 * (l >> 5) + (s >> 2), 2 * (l >> 4 & 1) + (s >> 1 & 1)) + ((s & 1) << 3);
         }
         __device__ __forceinline__ Lane fresh() const {
             Lane x = *this;
@@ -180,15 +202,15 @@ struct Rows {
     // over the rows, in the order in which an accumulator holds its rows.
     // 16 bits: rows 16 ks .. +15 of them.
     __device__ __forceinline__ static u32x4_t col16(const char *t, const Lane &ln, int r0, int ks, int dt) {
-        const char *p = t + (ln.col ^ (dt << 6)) + (r0 + 16 * ks) * RB;
-        const uint2 lo = lds_read_tr16(p), hi = lds_read_tr16(p + 8 * RB);
+        const char *p = t + (r0 + 16 * ks) * RB;
+        const uint2 lo = lds_read_tr16(p + (ln.col ^ (dt << 6))), hi = lds_read_tr16(p + (ln.col ^ (dt << 6) ^ 32) + 8 * RB);
         return u32x4_t{lo.x, lo.y, hi.x, hi.y};
     }
     // fp32: the lane's value of the row that accumulator element i stands for.
     __device__ __forceinline__ static float col32(const char *t, const Lane &ln, int r0, int i, int dt) {
-        const int m = ln.l & 31, row = 4 * (ln.l >> 5) + (i & 3);
-        const int pair = (4 * dt + (m >> 3)) ^ swz(row + 8 * (i >> 2));
-        return *reinterpret_cast<const float *>(t + row * RB + (pair << 5) + 4 * (m & 7) + (r0 + 8 * (i >> 2)) * RB);
+        const int m = ln.l & 31;
+        return *reinterpret_cast<const float *>(
+            t + chunk_off(4 * (ln.l >> 5) + (i & 3) + 8 * (i >> 2), 8 * dt + (m >> 2)) + 4 * (m & 3) + r0 * RB);
     }
 
     // acc[dt] += X^T W: rows r0 .. r0 + 31 of X, W in the accumulator layout of a
@@ -239,25 +261,8 @@ struct Rows {
     // of +inf and NaN then adds a product that overflows to +inf, what is seen of
     // -inf and NaN one to -inf: both make a NaN, and a hidden one adds 0.  seen: bit
     // i for accumulator element i.
-    // A real call on copies in memory: rare, and inlined it costs the paths beside
-    // it their registers.
-    __device__ __forceinline__ static void add_seen(f32x16_t (&acc)[ND], const char *t, int r0, const f32x16_t &w,
-                                                    uint32_t seen) {
-        f32x16_t x[ND + 1];
-#pragma unroll
-        for (int dt = 0; dt < ND; ++dt) x[dt] = acc[dt];
-        x[ND] = w;
-        add_seen_call(x, lds_addr(t), r0, seen);
-#pragma unroll
-        for (int dt = 0; dt < ND; ++dt) acc[dt] = x[dt];
-    }
-    __device__ __attribute__((noinline)) static void add_seen_call(f32x16_t *x, uint32_t lds, int r0, uint32_t seen) {
-        const char *t = (const char *)(const __attribute__((address_space(3))) char *)(uintptr_t)lds;
-        f32x16_t acc[ND];
-#pragma unroll
-        for (int dt = 0; dt < ND; ++dt) acc[dt] = x[dt];
-        const f32x16_t w = x[ND];
-        const Lane ln;
+    __device__ __forceinline__ static void add_seen(f32x16_t (&acc)[ND], const char *t, const Lane &ln, int r0,
+                                                    const f32x16_t &w, uint32_t seen) {
         constexpr float BIG = 0x1p127f;
         auto finite = [](float x) { return fabsf(x) < __builtin_inff() ? x : 0.f; };
         auto large = [](float x, float sign) {        // sign BIG where x is NaN or the infinity of that sign
@@ -314,8 +319,6 @@ struct Rows {
                     acc[dt] += z;
                 }
         }
-#pragma unroll
-        for (int dt = 0; dt < ND; ++dt) x[dt] = acc[dt];
     }
     __device__ __forceinline__ static float half_of(uint32_t x) {
         if constexpr (std::is_same_v<T, bf16_t>) return __uint_as_float(x << 16);
@@ -357,6 +360,11 @@ __device__ __forceinline__ void stage(const char *base, uint32_t bytes, const ui
 __device__ __forceinline__ void staged_barrier() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
+
+// Waits for the loads that fill x here.  Otherwise the wait would stand in the loop
+// that uses it first, and there it would wait for the staging copies as well.
+__device__ __forceinline__ void arrived(u32x4_t &x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ void arrived(float &x) { asm volatile("" : "+v"(x)); }
 
 // The two halves' values of a lane's column joined.
 __device__ __forceinline__ float half_max(float x) {

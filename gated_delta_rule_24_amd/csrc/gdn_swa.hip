@@ -30,7 +30,7 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
     constexpr int RB = R::RB, TILE = kKeys * RB, PIECES = TILE / 1024 / NW;
     extern __shared__ __align__(16) char smem[];   // two stages of K and V tiles
     SwaUnit u;
-    if (!swa_find(sh, u)) return;
+    if (!swa_find(sh, true, u)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, h = l >> 5;
     const int shift = u.Lk - u.Lq;                 // position of a token less its index
     const int t0 = u.unit * sh.tokens, t1 = min(t0 + sh.tokens, u.Lq);   // the block's tokens
@@ -49,6 +49,8 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
 #pragma unroll
     for (int s = 0; s < R::NS; ++s)
         qf[s] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const char *>(q + at * D) + 32 * s + 16 * h);
+#pragma unroll
+    for (int s = 0; s < R::NS; ++s) arrived(qf[s]);
 
     // key tiles: the sinks, then the band from `low`; one range where they meet
     int low = max(pfirst - W + 1, 0);
@@ -56,6 +58,11 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
     if (low <= sh.sinks) low = 0;
     const int ns = low > 0 ? (sh.sinks + kKeys - 1) / kKeys : 0;
     const int tiles = high > low ? ns + (high - low + kKeys - 1) / kKeys : 0;
+    // Tiles that every row of the block sees whole come first, then those that the mask
+    // cuts: a loop each, so that either keeps its registers.
+    const int whole_a = ns + max(plast - W + kKeys - low, 0) / kKeys;   // the first that no row's window begins in
+    const int whole = max(ns + (pfirst + 1 - low) / kKeys - whole_a, 0);
+    auto tile_at = [&](int x) { return x < whole ? whole_a + x : x - whole < whole_a ? x - whole : x; };
     auto first_key = [&](int it) { return it < ns ? it * kKeys : low + (it - ns) * kKeys; };
 
     const uint32_t stride = (uint32_t)sh.KV * RB;
@@ -63,12 +70,12 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
     uint32_t off[PIECES];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-        const int b = (i * NW + wave) * 1024 + l * 16, r = b / RB, c = (b % RB) / 16;
-        off[i] = r * stride + ((((c >> 1) ^ R::swz(r)) << 5) | (c & 1) << 4);
+        const int b = (i * NW + wave) * 1024 + l * 16;
+        off[i] = b / RB * stride + R::chunk_at(b) * 16;
     }
     const uint32_t lds = lds_addr(smem) + wave * 1024;
     auto load = [&](int it) {
-        const int j0 = first_key(it), n = min(u.Lk - j0, kKeys);
+        const int j0 = first_key(tile_at(it)), n = min(u.Lk - j0, kKeys);
         const int64_t b = head + (int64_t)j0 * stride;
         const uint32_t bytes = (n - 1) * stride + RB;
         const uint32_t to = lds + (it & 1) * 2 * TILE;
@@ -77,26 +84,29 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
     };
 
     f32x16_t acc[R::ND];
-#pragma unroll
-    for (int dt = 0; dt < R::ND; ++dt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[dt][i] = 0.f;
-    float m = -__builtin_inff(), sum = 0.f;        // log2 units; this lane's part of the sum
-
+    float m, sum;                                  // log2 units; this lane's part of the sum
     const typename R::Lane lane;
-    if (tiles) load(0);
-    for (int it = 0; it < tiles; ++it) {
-        staged_barrier();
-        if (it + 1 < tiles) load(it + 1);
-        if (!busy) continue;
-        const int j0 = first_key(it), jend = it < ns ? sh.sinks : high;
-        const char *kt = smem + (it & 1) * 2 * TILE, *vt = kt + TILE;
-        // 0: no row of the wave sees any of 32 keys, 2: all rows see all, 1: else
-        auto sees = [&](int j) {
-            if (j > p1 || j >= jend || (j + 31 <= p0 - W && j >= sh.sinks)) return 0;
-            return j + 31 <= p0 && j + 31 < jend && (j > p1 - W || j + 31 < sh.sinks) ? 2 : 1;
+    // All tiles.  CAREFUL: what a row does not see may be infinite or NaN.  Without it
+    // the answer is whether a tile that the mask cuts holds such a value, so that it
+    // has to be done again: that keeps the rare path's registers out of the other.
+    auto walk = [&](auto careful) {
+        constexpr bool CAREFUL = decltype(careful)::value;
+        bool again = false;
+#pragma unroll
+        for (int dt = 0; dt < R::ND; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[dt][i] = 0.f;
+        m = -__builtin_inff(), sum = 0.f;
+        // One staged tile after the other, [x0, x1) of their order.
+        auto each = [&](int x0, int x1, auto body) {
+            for (int x = x0; x < x1; ++x) {
+                staged_barrier();
+                if (x + 1 < tiles) load(x + 1);
+                if (busy) body(tile_at(x), smem + (x & 1) * 2 * TILE);
+            }
         };
-        auto process = [&](auto subs, auto masked, int r0) {
+        auto process = [&](auto subs, auto masked, const char *kt, int j0, int jend, int r0) {
+            const char *vt = kt + TILE;
             constexpr int NSUB = decltype(subs)::value;
             constexpr bool MASK = decltype(masked)::value;
             const typename R::Lane ln = lane.fresh();
@@ -144,24 +154,36 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
                     sum += S[n][i];
                 }
             if constexpr (MASK) {
-                if (__builtin_expect(R::not_finite(vt, ln, r0), 0)) {
-                    R::add_seen(acc, vt, r0, S[0], seen);
-                    return;
+                const bool bad = R::not_finite(vt, ln, r0);
+                if constexpr (CAREFUL) {
+                    if (bad) {
+                        R::add_seen(acc, vt, ln, r0, S[0], seen);
+                        return;
+                    }
                 }
+                again |= bad;
             }
 #pragma unroll
             for (int n = 0; n < NSUB; ++n) R::add(acc, vt, ln, r0 + 32 * n, S[n]);
         };
         using std::integral_constant;
-        const int s0 = sees(j0), s1 = sees(j0 + 32);
-        if (s0 == 2 && s1 == 2) {
-            process(integral_constant<int, 2>{}, std::false_type{}, 0);
-        } else {
+        if (tiles) load(0);
+        if constexpr (!CAREFUL)
+            each(0, whole, [&](int it, const char *kt) {
+                process(integral_constant<int, kKeys / 32>{}, std::false_type{}, kt, first_key(it), 0, 0);
+            });
+        each(CAREFUL ? 0 : whole, tiles, [&](int it, const char *kt) {
+            const int j0 = first_key(it), jend = it < ns ? sh.sinks : high;
 #pragma unroll 1
-            for (int r0 = 0; r0 < kKeys; r0 += 32)
-                if (sees(j0 + r0)) process(integral_constant<int, 1>{}, std::true_type{}, r0);
-        }
-    }
+            for (int r0 = 0; r0 < kKeys; r0 += 32) {
+                const int j = j0 + r0;           // 32 keys that no row of the wave sees are left out
+                if (j > p1 || j >= jend || (j + 31 <= p0 - W && j >= sh.sinks)) continue;
+                process(integral_constant<int, 1>{}, std::true_type{}, kt, j0, jend, r0);
+            }
+        });
+        return again;
+    };
+    if (__syncthreads_or(walk(std::false_type{}))) walk(std::true_type{});
 
     if (!busy) return;
     sum = half_sum(sum);

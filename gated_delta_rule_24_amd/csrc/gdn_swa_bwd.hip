@@ -37,7 +37,7 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
     constexpr int RB = R::RB, TILE = kKeys * RB, PIECES = TILE / 1024 / NW;
     extern __shared__ __align__(16) char smem[];   // two stages of K and V tiles
     SwaUnit u;
-    if (!swa_find(sh, u)) return;
+    if (!swa_find(sh, true, u)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, h = l >> 5;
     const int shift = u.Lk - u.Lq;
     const int t0 = u.unit * sh.tokens, t1 = min(t0 + sh.tokens, u.Lq);
@@ -71,13 +71,21 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
     }
     dd = half_sum(dd);
     if (on && h == 0) dsum[at] = dd;
-    const float lse2 = log2_lse(lse[at]);
+    float lse2 = log2_lse(lse[at]);
+    arrived(lse2);
+#pragma unroll
+    for (int s = 0; s < R::NS; ++s) arrived(qf[s]), arrived(gf[s]);
 
     int low = max(pfirst - W + 1, 0);
     const int high = plast + 1;
     if (low <= sh.sinks) low = 0;
     const int ns = low > 0 ? (sh.sinks + kKeys - 1) / kKeys : 0;
     const int tiles = high > low ? ns + (high - low + kKeys - 1) / kKeys : 0;
+    // Tiles that every row of the block sees whole come first, then those that the mask
+    // cuts: a loop each, so that either keeps its registers.
+    const int whole_a = ns + max(plast - W + kKeys - low, 0) / kKeys;   // the first that no row's window begins in
+    const int whole = max(ns + (pfirst + 1 - low) / kKeys - whole_a, 0);
+    auto tile_at = [&](int x) { return x < whole ? whole_a + x : x - whole < whole_a ? x - whole : x; };
     auto first_key = [&](int it) { return it < ns ? it * kKeys : low + (it - ns) * kKeys; };
 
     const uint32_t stride = (uint32_t)sh.KV * RB;
@@ -85,12 +93,12 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
     uint32_t off[PIECES];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-        const int b = (i * NW + wave) * 1024 + l * 16, r = b / RB, c = (b % RB) / 16;
-        off[i] = r * stride + ((((c >> 1) ^ R::swz(r)) << 5) | (c & 1) << 4);
+        const int b = (i * NW + wave) * 1024 + l * 16;
+        off[i] = b / RB * stride + R::chunk_at(b) * 16;
     }
     const uint32_t lds = lds_addr(smem) + wave * 1024;
     auto load = [&](int it) {
-        const int j0 = first_key(it), n = min(u.Lk - j0, kKeys);
+        const int j0 = first_key(tile_at(it)), n = min(u.Lk - j0, kKeys);
         const int64_t b = head + (int64_t)j0 * stride;
         const uint32_t bytes = (n - 1) * stride + RB;
         const uint32_t to = lds + (it & 1) * 2 * TILE;
@@ -99,25 +107,25 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
     };
 
     f32x16_t acc[R::ND];
-#pragma unroll
-    for (int dt = 0; dt < R::ND; ++dt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[dt][i] = 0.f;
-
     const typename R::Lane lane;
-    if (tiles) load(0);
-    for (int it = 0; it < tiles; ++it) {
-        staged_barrier();
-        if (it + 1 < tiles) load(it + 1);
-        if (!busy) continue;
-        const int j0 = first_key(it), jend = it < ns ? sh.sinks : high;
-        const char *kt = smem + (it & 1) * 2 * TILE, *vt = kt + TILE;
-        // 0: no row of the wave sees any of 32 keys, 2: all rows see all, 1: else
-        auto sees = [&](int j) {
-            if (j > p1 || j >= jend || (j + 31 <= p0 - W && j >= sh.sinks)) return 0;
-            return j + 31 <= p0 && j + 31 < jend && (j > p1 - W || j + 31 < sh.sinks) ? 2 : 1;
+    // All tiles, as forward: without CAREFUL the answer is whether it has to be done again.
+    auto walk = [&](auto careful) {
+        constexpr bool CAREFUL = decltype(careful)::value;
+        bool again = false;
+#pragma unroll
+        for (int dt = 0; dt < R::ND; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[dt][i] = 0.f;
+        // One staged tile after the other, [x0, x1) of their order.
+        auto each = [&](int x0, int x1, auto body) {
+            for (int x = x0; x < x1; ++x) {
+                staged_barrier();
+                if (x + 1 < tiles) load(x + 1);
+                if (busy) body(tile_at(x), smem + (x & 1) * 2 * TILE);
+            }
         };
-        auto process = [&](auto masked, int r0) {
+        auto process = [&](auto masked, const char *kt, int j0, int jend, int r0) {
+            const char *vt = kt + TILE;
             constexpr bool MASK = decltype(masked)::value;
             const typename R::Lane ln = lane.fresh();
             f32x16_t S, P;
@@ -142,22 +150,35 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
                 }
             }
             if constexpr (MASK) {
-                if (__builtin_expect(R::not_finite(kt, ln, r0), 0)) {
-                    R::add_seen(acc, kt, r0, S, seen);
-                    return;
+                const bool bad = R::not_finite(kt, ln, r0);
+                if constexpr (CAREFUL) {
+                    if (bad) {
+                        R::add_seen(acc, kt, ln, r0, S, seen);
+                        return;
+                    }
                 }
+                again |= bad;
             }
             R::add(acc, kt, ln, r0, S);
         };
-        if (sees(j0) == 2 && sees(j0 + 32) == 2) {
+        if (tiles) load(0);
+        if constexpr (!CAREFUL)
+            each(0, whole, [&](int it, const char *kt) {
 #pragma unroll
-            for (int r0 = 0; r0 < kKeys; r0 += 32) process(std::false_type{}, r0);
-        } else {
+                for (int r0 = 0; r0 < kKeys; r0 += 32) process(std::false_type{}, kt, first_key(it), 0, r0);
+            });
+        each(CAREFUL ? 0 : whole, tiles, [&](int it, const char *kt) {
+            const int j0 = first_key(it), jend = it < ns ? sh.sinks : high;
 #pragma unroll 1
-            for (int r0 = 0; r0 < kKeys; r0 += 32)
-                if (sees(j0 + r0)) process(std::true_type{}, r0);
-        }
-    }
+            for (int r0 = 0; r0 < kKeys; r0 += 32) {
+                const int j = j0 + r0;           // 32 keys that no row of the wave sees are left out
+                if (j > p1 || j >= jend || (j + 31 <= p0 - W && j >= sh.sinks)) continue;
+                process(std::true_type{}, kt, j0, jend, r0);
+            }
+        });
+        return again;
+    };
+    if (__syncthreads_or(walk(std::false_type{}))) walk(std::true_type{});
     if (busy) store_column<T, D>(dq + at * D, acc, sh.scale, on);
 }
 
@@ -176,6 +197,14 @@ __host__ __device__ __forceinline__ FarParts far_parts(int Lq, int Lk, int windo
 // First part of sequence n in the workspace: part 0 is the near one's.
 __device__ __forceinline__ int64_t far_first(int64_t q0, int n, int far) { return q0 / far + 2 * (int64_t)n; }
 
+// The two accumulators and the operands K and V of a wave are 3 D 32-bit registers
+// in 16 bits, 4 D in fp32.  Where that leaves too few of 256, dV and dK are made by
+// different blocks, the second with S once more (5 products instead of 4).
+// Measured, 4 x 4096 tokens, 16 heads on 4 of 128, window 2048, in bf16: one block for
+// both 3715 us with two waves a SIMD (registers spill) and 1195 with one.
+template <typename T, int D>
+constexpr bool kSplitKeySide = Rows<T, D>::RB >= 256;
+
 template <typename T, int D>
 __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_kernel(
     SwaShape sh, int far, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
@@ -185,14 +214,14 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
     constexpr int NW = 4, RB = R::RB, TILE = kRows * RB, PIECES = TILE / 1024 / NW;
     extern __shared__ __align__(16) char smem[];   // two stages of Q and dO tiles, of lse and D
     float *stats = reinterpret_cast<float *>(smem + 4 * TILE);
+    int *tokens = reinterpret_cast<int *>(stats + 4 * kRows);   // of a tile's rows, from its first on
     SwaUnit u;
-    if (!swa_find(sh, u)) return;
+    if (!swa_find<kSplitKeySide<T, D> ? 2 : 1>(sh, false, u)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, h = l >> 5;
     const int shift = u.Lk - u.Lq, W = sh.window;
-    const int key_tiles = (u.Lk + kSwaKeyTile - 1) / kSwaKeyTile;
     const FarParts fp = far_parts(u.Lq, u.Lk, W, sh.sinks, far);
-    const int part = u.unit - key_tiles;           // >= 0: a far part
-    const int jt = part >= 0 ? 0 : u.unit * kSwaKeyTile;
+    const int part = u.unit < fp.parts ? u.unit : -1;   // >= 0: a far part; these come first
+    const int jt = part >= 0 ? 0 : (u.unit - fp.parts) * kSwaKeyTile;
 
     // the tokens that this block takes
     int ta, tb;
@@ -215,10 +244,14 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
         kf[s] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const char *>(k) + b);
         vf[s] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const char *>(v) + b);
     }
+#pragma unroll
+    for (int s = 0; s < R::NS; ++s) arrived(kf[s]), arrived(vf[s]);
 
     // rows left over of a tile (the group's size does not divide it) are never
     // copied: they stay zeros, and their probabilities 0
     const int rows = sh.tokens * sh.G;
+    const int half = 32 / sh.G, half_end = min(31 / sh.G + 1, sh.tokens);   // tokens of rows 32 .. and to row 31
+    if (threadIdx.x < kRows) tokens[threadIdx.x] = (int)threadIdx.x < rows ? (int)threadIdx.x / sh.G : 1 << 30;
     if (rows < kRows) {
         for (int b = threadIdx.x * 16; b < (kRows - rows) * RB; b += 256 * 16)
 #pragma unroll
@@ -229,15 +262,22 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
     uint32_t off[PIECES];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-        const int b = (i * NW + wave) * 1024 + l * 16, r = b / RB, c = (b % RB) / 16;
-        off[i] = r < rows ? (r / sh.G) * stride + (r % sh.G) * RB + ((((c >> 1) ^ R::swz(r)) << 5) | (c & 1) << 4)
-                          : 0xFFFFFFFFu;
+        const int b = (i * NW + wave) * 1024 + l * 16, r = b / RB;
+        off[i] = r < rows ? (r / sh.G) * stride + (r % sh.G) * RB + R::chunk_at(b) * 16 : 0xFFFFFFFFu;
     }
     const uint32_t lds = lds_addr(smem) + wave * 1024;
+    // Tiles whose rows all see all keys of the block come first, then those that the mask
+    // cuts.
+    const int whole_a = max(jt + kSwaKeyTile - 1 - shift - ta + sh.tokens - 1, 0) / sh.tokens;
+    const int64_t whole_end = min((int64_t)jt + W - shift, (int64_t)tb) - ta;
+    const int whole = part >= 0 ? 0 : max((int)max(whole_end, (int64_t)0) / sh.tokens - whole_a, 0);
+    auto first_token = [&](int x) {
+        return ta + (x < whole ? whole_a + x : x - whole < whole_a ? x - whole : x) * sh.tokens;
+    };
     const int srow = l, stoken = srow / sh.G;      // waves 0 and 1 bring lse and D of the tile's rows
     float stat = 0.f;
     auto load = [&](int it) {
-        const int t0 = ta + it * sh.tokens, n = min(tb - t0, sh.tokens);
+        const int t0 = first_token(it), n = min(tb - t0, sh.tokens);
         const int64_t first = (u.q0 + t0) * sh.H + u.hk * sh.G, b = first * RB;
         const uint32_t bytes = (n - 1) * stride + sh.G * RB;
         const uint32_t to = lds + (it & 1) * 2 * TILE;
@@ -254,98 +294,128 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
         if (wave < 2) stats[((it & 1) * 2 + wave) * kRows + l] = stat;
     };
 
-    f32x16_t ak[R::ND], av[R::ND];
-#pragma unroll
-    for (int dt = 0; dt < R::ND; ++dt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) ak[dt][i] = av[dt][i] = 0.f;
-
     const typename R::Lane lane;
-    if (tiles) {
-        load(0);
-        put(0);
-    }
-    for (int it = 0; it < tiles; ++it) {
-        staged_barrier();
-        if (it + 1 < tiles) load(it + 1);
-        const int t0 = ta + it * sh.tokens;
-        const char *qt = smem + (it & 1) * 2 * TILE, *gt = qt + TILE;
-        const float *st = stats + (it & 1) * 2 * kRows;
-        // 0: none of 32 rows sees any of the wave's keys, 2: all see all, 1: else
-        auto sees = [&](int r0) {
-            const int a = t0 + r0 / sh.G, b = min(t0 + (r0 + 31) / sh.G, t0 + sh.tokens - 1);
-            if (!busy || r0 >= rows || a >= tb) return 0;
-            const int p0 = a + shift, p1 = min(b, tb - 1) + shift;
-            if (k0 > p1 || (k0 + 31 <= p0 - W && k0 >= sh.sinks)) return 0;
-            return k0 + 31 <= p0 && (k0 > p1 - W || k0 + 31 < sh.sinks) && b < tb ? 2 : 1;
-        };
-        auto process = [&](auto masked, int r0) {
+    // All tiles of rows, for dV, dK or both.  Without CAREFUL the answer is whether it has
+    // to be done again.
+    auto walk = [&](auto careful, auto make_v, auto make_k, f32x16_t (&av)[R::ND], f32x16_t (&ak)[R::ND]) {
+        constexpr bool CAREFUL = decltype(careful)::value, MAKE_V = decltype(make_v)::value,
+                       MAKE_K = decltype(make_k)::value;
+        bool again = false;
+#pragma unroll
+        for (int dt = 0; dt < R::ND; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (MAKE_K) ak[dt][i] = 0.f;
+                if (MAKE_V) av[dt][i] = 0.f;
+            }
+        auto process = [&](auto masked, int x, int t0, int r0) {
+            const char *qt = smem + (x & 1) * 2 * TILE, *gt = qt + TILE;
+            const float *st = stats + (x & 1) * 2 * kRows;
             constexpr bool MASK = decltype(masked)::value;
             const typename R::Lane ln = lane.fresh();
+            const float *sr = st + r0 + 4 * (ln.l >> 5);
             f32x16_t S, P;
 #pragma unroll
             for (int i = 0; i < 16; ++i) S[i] = P[i] = 0.f;
 #pragma unroll
-            for (int s = 0; s < R::NS; ++s) {
-                mma32<T>(S, R::frag(qt, ln, r0, s), kf[s]);
-                mma32<T>(P, R::frag(gt, ln, r0, s), vf[s]);
-            }
+            for (int s = 0; s < R::NS; ++s) mma32<T>(S, R::frag(qt, ln, r0, s), kf[s]);
             uint32_t seen = 0;
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
-                const int r = r0 + 8 * a + 4 * (ln.l >> 5);
-                const float4_t L = *reinterpret_cast<const float4_t *>(st + r);
-                const float4_t dd = *reinterpret_cast<const float4_t *>(st + kRows + r);
+                const float4_t L = *reinterpret_cast<const float4_t *>(sr + 8 * a);
+                int4 to{};
+                if constexpr (MASK) to = *reinterpret_cast<const int4 *>(tokens + (sr - st) + 8 * a);
+                const int tok[4] = {to.x, to.y, to.z, to.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = 4 * a + e;
-                    const float p = __builtin_amdgcn_exp2f(fmaf(S[i], sh.c, -L[e]));
-                    const float x = p * (P[i] - dd[e]);
+                    S[i] = __builtin_amdgcn_exp2f(fmaf(S[i], sh.c, -L[e]));
                     if constexpr (MASK) {
-                        const int token = t0 + (r + e) / sh.G, pos = token + shift;
-                        const bool see = r + e < rows && token < tb && key <= pos && (key > pos - W || key < sh.sinks);
-                        S[i] = see ? p : 0.f;
-                        P[i] = see ? x : 0.f;
+                        const int token = t0 + tok[e], pos = token + shift;
+                        const bool see = token < tb && key <= pos && (key > pos - W || key < sh.sinks);
+                        S[i] = see ? S[i] : 0.f;
                         seen |= (uint32_t)see << i;
-                    } else {
-                        S[i] = p;
-                        P[i] = x;
                     }
                 }
             }
+            bool bad = false;
             if constexpr (MASK) {
-                if (__builtin_expect(R::not_finite(qt, ln, r0) || R::not_finite(gt, ln, r0), 0)) {
-                    R::add_seen(av, gt, r0, S, seen);
-                    R::add_seen(ak, qt, r0, P, seen);
-                    return;
+                bad = R::not_finite(qt, ln, r0) || R::not_finite(gt, ln, r0);
+                again |= bad;
+            }
+            if constexpr (MAKE_V) {
+                if (CAREFUL && bad) R::add_seen(av, gt, ln, r0, S, seen);
+                else R::add(av, gt, ln, r0, S);
+            }
+            if constexpr (!MAKE_K) return;
+#pragma unroll
+            for (int s = 0; s < R::NS; ++s) mma32<T>(P, R::frag(gt, ln, r0, s), vf[s]);
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const float4_t dd = *reinterpret_cast<const float4_t *>(sr + kRows + 8 * a);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 4 * a + e;
+                    const float x = S[i] * (P[i] - dd[e]);
+                    P[i] = !MASK || (seen >> i & 1u) ? x : 0.f;
                 }
             }
-            R::add(av, gt, ln, r0, S);
-            R::add(ak, qt, ln, r0, P);
+            if (CAREFUL && bad) R::add_seen(ak, qt, ln, r0, P, seen);
+            else R::add(ak, qt, ln, r0, P);
         };
-        if (sees(0) == 2 && sees(32) == 2) {
-#pragma unroll
-            for (int r0 = 0; r0 < kRows; r0 += 32) process(std::false_type{}, r0);
-        } else {
-#pragma unroll 1
-            for (int r0 = 0; r0 < kRows; r0 += 32)
-                if (sees(r0)) process(std::true_type{}, r0);
+        // One staged tile after the other, [x0, x1) of their order.
+        auto each = [&](int x0, int x1, auto body) {
+            for (int x = x0; x < x1; ++x) {
+                staged_barrier();
+                if (x + 1 < tiles) load(x + 1);
+                if (busy) body(x, first_token(x));
+                if (x + 1 < tiles) put(x + 1);
+            }
+        };
+        if (tiles) {
+            load(0);
+            put(0);
         }
-        if (it + 1 < tiles) put(it + 1);
-    }
-
-    if (!busy) return;
-    const bool shared = fp.parts > 0 && jt == 0 && key < sh.sinks;   // the parts are added later
-    if (part < 0) {
-        const bool on = key < u.Lk && !shared;
-        store_column<T, D>(dk + at * D, ak, sh.scale, on);
-        store_column<T, D>(dv + at * D, av, 1.f, on);
-    }
-    if (fp.parts > 0 && k0 < sh.sinks && jt == 0) {
-        const int64_t slot = far_first(u.q0, u.n, far) + (part >= 0 ? part + 1 : 0);
-        float *to = share + ((slot * sh.KV + u.hk) * 2 * sh.sinks + key) * (int64_t)D;
-        store_column<float, D>(to, ak, sh.scale, shared && key < u.Lk);
-        store_column<float, D>(to + (int64_t)sh.sinks * D, av, 1.f, shared && key < u.Lk);
+        if constexpr (!CAREFUL)
+            each(0, whole, [&](int x, int t0) {
+#pragma unroll
+                for (int r0 = 0; r0 < kRows; r0 += 32) process(std::false_type{}, x, t0, r0);
+            });
+        each(CAREFUL ? 0 : whole, tiles, [&](int x, int t0) {
+#pragma unroll 1
+            for (int r0 = 0; r0 < kRows; r0 += 32) {
+                // 32 rows of which none sees a key of the wave are left out
+                const int a = t0 + (r0 ? half : 0), b = min(t0 + (r0 ? sh.tokens : half_end), tb) - 1;
+                if (r0 >= rows || a >= tb || k0 > b + shift || (k0 + 31 <= a + shift - W && k0 >= sh.sinks)) continue;
+                process(std::true_type{}, x, t0, r0);
+            }
+        });
+        return again;
+    };
+    auto run = [&](auto make_v, auto make_k) {
+        constexpr bool MAKE_V = decltype(make_v)::value, MAKE_K = decltype(make_k)::value;
+        f32x16_t av[R::ND], ak[R::ND];
+        if (__syncthreads_or(walk(std::false_type{}, make_v, make_k, av, ak)))
+            walk(std::true_type{}, make_v, make_k, av, ak);
+        if (!busy) return;
+        const bool shared = fp.parts > 0 && jt == 0 && key < sh.sinks;   // the parts are added later
+        if (part < 0) {
+            const bool on = key < u.Lk && !shared;
+            if (MAKE_K) store_column<T, D>(dk + at * D, ak, sh.scale, on);
+            if (MAKE_V) store_column<T, D>(dv + at * D, av, 1.f, on);
+        }
+        if (fp.parts > 0 && k0 < sh.sinks && jt == 0) {
+            const int64_t slot = far_first(u.q0, u.n, far) + (part >= 0 ? part + 1 : 0);
+            float *to = share + ((slot * sh.KV + u.hk) * 2 * sh.sinks + key) * (int64_t)D;
+            if (MAKE_K) store_column<float, D>(to, ak, sh.scale, shared && key < u.Lk);
+            if (MAKE_V) store_column<float, D>(to + (int64_t)sh.sinks * D, av, 1.f, shared && key < u.Lk);
+        }
+    };
+    if constexpr (kSplitKeySide<T, D>) {
+        if (u.role == 0) run(std::true_type{}, std::false_type{});
+        else run(std::false_type{}, std::true_type{});
+    } else {
+        run(std::true_type{}, std::true_type{});
     }
 }
 
@@ -429,10 +499,11 @@ hipError_t launch_swa_bwd(const SwaArgs &a, hipStream_t st) {
         }
         if (key_units) {
             ProfScope prof("gdn_swa_dkv", st);
-            constexpr int lds = 4 * kRows * RB + 4 * kRows * 4;
+            constexpr int lds = 4 * kRows * RB + 5 * kRows * 4;
             e = swa_lds(swa_dkv_kernel<T, D>, lds);
             if (e != hipSuccess) return e;
-            swa_dkv_kernel<T, D><<<(unsigned)((key_units * a.KV + 7) / 8 * 8), 256, lds, st>>>(
+            constexpr int roles = kSplitKeySide<T, D> ? 2 : 1;
+            swa_dkv_kernel<T, D><<<(unsigned)((key_units * a.KV * roles + 7) / 8 * 8), 256, lds, st>>>(
                 sk, far, in(a.q), in(a.k), in(a.v), a.lse, in(a.d_o), dsum, out(a.dk), out(a.dv), share);
             e = hipGetLastError();
             if (e != hipSuccess) return e;
