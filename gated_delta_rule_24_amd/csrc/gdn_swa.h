@@ -366,6 +366,18 @@ __device__ __forceinline__ void staged_barrier() {
 __device__ __forceinline__ void arrived(u32x4_t &x) { asm volatile("" : "+v"(x)); }
 __device__ __forceinline__ void arrived(float &x) { asm volatile("" : "+v"(x)); }
 
+// Whether a lane's sums are not all finite: 0 times a hidden infinity or NaN is NaN,
+// so where they are, nothing of the kind has come in.
+template <int N>
+__device__ __forceinline__ bool any_not_finite(const f32x16_t (&acc)[N]) {
+    bool bad = false;
+#pragma unroll
+    for (int dt = 0; dt < N; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) bad |= !(fabsf(acc[dt][i]) < __builtin_inff());
+    return bad;
+}
+
 // The two halves' values of a lane's column joined.
 __device__ __forceinline__ float half_max(float x) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);

@@ -86,12 +86,11 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
     f32x16_t acc[R::ND];
     float m, sum;                                  // log2 units; this lane's part of the sum
     const typename R::Lane lane;
-    // All tiles.  CAREFUL: what a row does not see may be infinite or NaN.  Without it
-    // the answer is whether a tile that the mask cuts holds such a value, so that it
-    // has to be done again: that keeps the rare path's registers out of the other.
+    // All tiles.  CAREFUL: what a row does not see may be infinite or NaN.  That is seen
+    // from sums that are not finite, and all is done again: it keeps the rare path's
+    // registers and its looks at V out of the other.
     auto walk = [&](auto careful) {
         constexpr bool CAREFUL = decltype(careful)::value;
-        bool again = false;
 #pragma unroll
         for (int dt = 0; dt < R::ND; ++dt)
 #pragma unroll
@@ -153,15 +152,11 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
                     S[n][i] = __builtin_amdgcn_exp2f(fmaf(S[n][i], sh.c, -base));
                     sum += S[n][i];
                 }
-            if constexpr (MASK) {
-                const bool bad = R::not_finite(vt, ln, r0);
-                if constexpr (CAREFUL) {
-                    if (bad) {
-                        R::add_seen(acc, vt, ln, r0, S[0], seen);
-                        return;
-                    }
+            if constexpr (CAREFUL) {
+                if (R::not_finite(vt, ln, r0)) {
+                    R::add_seen(acc, vt, ln, r0, S[0], seen);
+                    return;
                 }
-                again |= bad;
             }
 #pragma unroll
             for (int n = 0; n < NSUB; ++n) R::add(acc, vt, ln, r0 + 32 * n, S[n]);
@@ -181,9 +176,9 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
                 process(integral_constant<int, 1>{}, std::true_type{}, kt, j0, jend, r0);
             }
         });
-        return again;
     };
-    if (__syncthreads_or(walk(std::false_type{}))) walk(std::true_type{});
+    walk(std::false_type{});
+    if (__syncthreads_or(busy && any_not_finite(acc))) walk(std::true_type{});
 
     if (!busy) return;
     sum = half_sum(sum);

@@ -108,10 +108,9 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
 
     f32x16_t acc[R::ND];
     const typename R::Lane lane;
-    // All tiles, as forward: without CAREFUL the answer is whether it has to be done again.
+    // All tiles, and as forward a second time where the sums are not finite.
     auto walk = [&](auto careful) {
         constexpr bool CAREFUL = decltype(careful)::value;
-        bool again = false;
 #pragma unroll
         for (int dt = 0; dt < R::ND; ++dt)
 #pragma unroll
@@ -149,15 +148,11 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
                     S[i] = x;
                 }
             }
-            if constexpr (MASK) {
-                const bool bad = R::not_finite(kt, ln, r0);
-                if constexpr (CAREFUL) {
-                    if (bad) {
-                        R::add_seen(acc, kt, ln, r0, S, seen);
-                        return;
-                    }
+            if constexpr (CAREFUL) {
+                if (R::not_finite(kt, ln, r0)) {
+                    R::add_seen(acc, kt, ln, r0, S, seen);
+                    return;
                 }
-                again |= bad;
             }
             R::add(acc, kt, ln, r0, S);
         };
@@ -176,9 +171,9 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
                 process(std::true_type{}, kt, j0, jend, r0);
             }
         });
-        return again;
     };
-    if (__syncthreads_or(walk(std::false_type{}))) walk(std::true_type{});
+    walk(std::false_type{});
+    if (__syncthreads_or(busy && any_not_finite(acc))) walk(std::true_type{});
     if (busy) store_column<T, D>(dq + at * D, acc, sh.scale, on);
 }
 
@@ -267,12 +262,21 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
     }
     const uint32_t lds = lds_addr(smem) + wave * 1024;
     // Tiles whose rows all see all keys of the block come first, then those that the mask
-    // cuts.
-    const int whole_a = max(jt + kSwaKeyTile - 1 - shift - ta + sh.tokens - 1, 0) / sh.tokens;
-    const int64_t whole_end = min((int64_t)jt + W - shift, (int64_t)tb) - ta;
-    const int whole = part >= 0 ? 0 : max((int)max(whole_end, (int64_t)0) / sh.tokens - whole_a, 0);
+    // cuts.  Neighbouring key tiles see almost the same tokens, 128 later each: they take
+    // the first kind in the order of the tokens' residues, so that blocks that run
+    // side by side read the same rows at about the same time, out of one L2.
+    // Of a far part every full tile is of the first kind: its rows see the sinks, and
+    // the gradients of other keys are dropped.
+    int whole_a = 0, whole = (tb - ta) / sh.tokens;
+    if (part < 0) {
+        whole_a = max(jt + kSwaKeyTile - 1 - shift - ta + sh.tokens - 1, 0) / sh.tokens;
+        const int64_t end = min((int64_t)jt + W - shift, (int64_t)tb) - ta;
+        whole = max((int)max(end, (int64_t)0) / sh.tokens - whole_a, 0);
+    }
+    const int turn = whole ? (whole - (ta / sh.tokens + whole_a) % whole) % whole : 0;
     auto first_token = [&](int x) {
-        return ta + (x < whole ? whole_a + x : x - whole < whole_a ? x - whole : x) * sh.tokens;
+        const int y = x + turn < whole ? x + turn : x + turn - whole;
+        return ta + (x < whole ? whole_a + y : x - whole < whole_a ? x - whole : x) * sh.tokens;
     };
     const int srow = l, stoken = srow / sh.G;      // waves 0 and 1 bring lse and D of the tile's rows
     float stat = 0.f;
@@ -295,12 +299,10 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
     };
 
     const typename R::Lane lane;
-    // All tiles of rows, for dV, dK or both.  Without CAREFUL the answer is whether it has
-    // to be done again.
+    // All tiles of rows, for dV, dK or both.
     auto walk = [&](auto careful, auto make_v, auto make_k, f32x16_t (&av)[R::ND], f32x16_t (&ak)[R::ND]) {
         constexpr bool CAREFUL = decltype(careful)::value, MAKE_V = decltype(make_v)::value,
                        MAKE_K = decltype(make_k)::value;
-        bool again = false;
 #pragma unroll
         for (int dt = 0; dt < R::ND; ++dt)
 #pragma unroll
@@ -308,60 +310,74 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
                 if (MAKE_K) ak[dt][i] = 0.f;
                 if (MAKE_V) av[dt][i] = 0.f;
             }
-        auto process = [&](auto masked, int x, int t0, int r0) {
+        auto process = [&](auto subs, auto masked, int x, int t0, int r0) {
             const char *qt = smem + (x & 1) * 2 * TILE, *gt = qt + TILE;
             const float *st = stats + (x & 1) * 2 * kRows;
+            constexpr int NSUB = decltype(subs)::value;
             constexpr bool MASK = decltype(masked)::value;
             const typename R::Lane ln = lane.fresh();
             const float *sr = st + r0 + 4 * (ln.l >> 5);
-            f32x16_t S, P;
+            f32x16_t S[NSUB], P[NSUB];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) S[i] = P[i] = 0.f;
+            for (int n = 0; n < NSUB; ++n)
 #pragma unroll
-            for (int s = 0; s < R::NS; ++s) mma32<T>(S, R::frag(qt, ln, r0, s), kf[s]);
+                for (int i = 0; i < 16; ++i) S[n][i] = P[n][i] = 0.f;
+#pragma unroll
+            for (int s = 0; s < R::NS; ++s)
+#pragma unroll
+                for (int n = 0; n < NSUB; ++n) mma32<T>(S[n], R::frag(qt, ln, r0 + 32 * n, s), kf[s]);
             uint32_t seen = 0;
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
+            for (int a = 0; a < 4 * NSUB; ++a) {
                 const float4_t L = *reinterpret_cast<const float4_t *>(sr + 8 * a);
                 int4 to{};
                 if constexpr (MASK) to = *reinterpret_cast<const int4 *>(tokens + (sr - st) + 8 * a);
                 const int tok[4] = {to.x, to.y, to.z, to.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = 4 * a + e;
-                    S[i] = __builtin_amdgcn_exp2f(fmaf(S[i], sh.c, -L[e]));
+                    const int i = 4 * (a & 3) + e;
+                    float p = S[a >> 2][i];
+                    p = __builtin_amdgcn_exp2f(fmaf(p, sh.c, -L[e]));
                     if constexpr (MASK) {
                         const int token = t0 + tok[e], pos = token + shift;
                         const bool see = token < tb && key <= pos && (key > pos - W || key < sh.sinks);
-                        S[i] = see ? S[i] : 0.f;
+                        p = see ? p : 0.f;
                         seen |= (uint32_t)see << i;
                     }
+                    S[a >> 2][i] = p;
                 }
             }
             bool bad = false;
-            if constexpr (MASK) {
-                bad = R::not_finite(qt, ln, r0) || R::not_finite(gt, ln, r0);
-                again |= bad;
-            }
+            if constexpr (CAREFUL) bad = R::not_finite(qt, ln, r0) || R::not_finite(gt, ln, r0);
             if constexpr (MAKE_V) {
-                if (CAREFUL && bad) R::add_seen(av, gt, ln, r0, S, seen);
-                else R::add(av, gt, ln, r0, S);
+                if (CAREFUL && bad) {
+                    R::add_seen(av, gt, ln, r0, S[0], seen);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NSUB; ++n) R::add(av, gt, ln, r0 + 32 * n, S[n]);
+                }
             }
             if constexpr (!MAKE_K) return;
 #pragma unroll
-            for (int s = 0; s < R::NS; ++s) mma32<T>(P, R::frag(gt, ln, r0, s), vf[s]);
+            for (int s = 0; s < R::NS; ++s)
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
+                for (int n = 0; n < NSUB; ++n) mma32<T>(P[n], R::frag(gt, ln, r0 + 32 * n, s), vf[s]);
+#pragma unroll
+            for (int a = 0; a < 4 * NSUB; ++a) {
                 const float4_t dd = *reinterpret_cast<const float4_t *>(sr + kRows + 8 * a);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = 4 * a + e;
-                    const float x = S[i] * (P[i] - dd[e]);
-                    P[i] = !MASK || (seen >> i & 1u) ? x : 0.f;
+                    const int i = 4 * (a & 3) + e;
+                    const float y = S[a >> 2][i] * (P[a >> 2][i] - dd[e]);
+                    P[a >> 2][i] = !MASK || (seen >> i & 1u) ? y : 0.f;
                 }
             }
-            if (CAREFUL && bad) R::add_seen(ak, qt, ln, r0, P, seen);
-            else R::add(ak, qt, ln, r0, P);
+            if (CAREFUL && bad) {
+                R::add_seen(ak, qt, ln, r0, P[0], seen);
+            } else {
+#pragma unroll
+                for (int n = 0; n < NSUB; ++n) R::add(ak, qt, ln, r0 + 32 * n, P[n]);
+            }
         };
         // One staged tile after the other, [x0, x1) of their order.
         auto each = [&](int x0, int x1, auto body) {
@@ -378,8 +394,7 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
         }
         if constexpr (!CAREFUL)
             each(0, whole, [&](int x, int t0) {
-#pragma unroll
-                for (int r0 = 0; r0 < kRows; r0 += 32) process(std::false_type{}, x, t0, r0);
+                process(std::integral_constant<int, kRows / 32>{}, std::false_type{}, x, t0, 0);
             });
         each(CAREFUL ? 0 : whole, tiles, [&](int x, int t0) {
 #pragma unroll 1
@@ -387,16 +402,18 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
                 // 32 rows of which none sees a key of the wave are left out
                 const int a = t0 + (r0 ? half : 0), b = min(t0 + (r0 ? sh.tokens : half_end), tb) - 1;
                 if (r0 >= rows || a >= tb || k0 > b + shift || (k0 + 31 <= a + shift - W && k0 >= sh.sinks)) continue;
-                process(std::true_type{}, x, t0, r0);
+                process(std::integral_constant<int, 1>{}, std::true_type{}, x, t0, r0);
             }
         });
-        return again;
     };
     auto run = [&](auto make_v, auto make_k) {
         constexpr bool MAKE_V = decltype(make_v)::value, MAKE_K = decltype(make_k)::value;
         f32x16_t av[R::ND], ak[R::ND];
-        if (__syncthreads_or(walk(std::false_type{}, make_v, make_k, av, ak)))
-            walk(std::true_type{}, make_v, make_k, av, ak);
+        walk(std::false_type{}, make_v, make_k, av, ak);
+        bool bad = false;
+        if constexpr (MAKE_V) bad |= any_not_finite(av);
+        if constexpr (MAKE_K) bad |= any_not_finite(ak);
+        if (__syncthreads_or(busy && bad)) walk(std::true_type{}, make_v, make_k, av, ak);
         if (!busy) return;
         const bool shared = fp.parts > 0 && jt == 0 && key < sh.sinks;   // the parts are added later
         if (part < 0) {
