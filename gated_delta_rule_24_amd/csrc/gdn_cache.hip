@@ -84,55 +84,75 @@ __global__ __launch_bounds__(kThreads) void cache_rows_kernel(CacheShape s, cons
     }
     if (bad) return;
 
-    // rows of k, then the same of v
-    const int64_t half = (int64_t)total * s.KV, all = 2 * half;
+    // Rows of k with their heads, then the same of v; the rows of a block's piece go by
+    // its groups in turn.  A group keeps where it is, so that a step is some additions.
+    const int64_t all = 2 * (int64_t)total * s.KV;
     const int64_t turn = (int64_t)GROUPS * U, per = ((all + gridDim.x - 1) / gridDim.x + turn - 1) / turn * turn;
     const int64_t begin = blockIdx.x * per, end = min(begin + per, all);
+    if (begin >= end) return;
     const int g = tid / L, l = tid % L;
-    int n = -1, side = 0;
-    for (int64_t i0 = begin; i0 < end; i0 += turn) {
+    const int step_r = GROUPS / s.KV, step_h = GROUPS - step_r * s.KV;
+    int64_t left = end - begin - g;                // items from this one on
+    int64_t at = (begin + g) / s.KV;               // row of both sides
+    int h = (int)(begin + g - at * s.KV), side = at >= total, r = (int)(at - (side ? total : 0));
+    int n = s.N, next = 0;                         // the sequence of row r, and the first row of the next
+    int tokens0 = 0, head = 0, jump = 0, ring = 0; // its first token; rows that are not of the ring's run
+    int64_t page = 0;                              // its first row in the cache
+    auto enter = [&]() {
+        int a = 0, b = s.N;                        // the last sequence whose first row is at most r
+        while (b - a > 1) {
+            const int c = (a + b) / 2;
+            if (first[c] <= r) a = c;
+            else b = c;
+        }
+        n = a;
+        while (first[n + 1] <= r) ++n;
+        next = first[n + 1];
+        const int have = lengths ? lengths[n] : 0, slot = slots ? slots[n] : n;
+        tokens0 = cu ? cu[n] : n * s.per_seq;
+        page = ((int64_t)side * s.P + slot) * s.KV * rows;
+        if (READ) {
+            // rows o < head stand as they are, row o >= head at ring place (ring + o) mod window
+            head = have <= rows ? rows : s.sinks;
+            ring = have <= rows ? 0 : (have - s.window - s.sinks) % s.window - s.sinks;
+            jump = 0;
+        } else {
+            // the first `head` tokens are sinks, then `jump` tokens are passed over
+            const int len = (cu ? cu[n + 1] : tokens0 + s.per_seq) - tokens0, tail = min(len, s.window);
+            head = next - first[n] - tail;
+            jump = len - tail - head;
+            const int start = have + len - tail - s.sinks;
+            ring = (start > 0 ? start % s.window : start) - head;
+        }
+    };
+    for (; __any(left > 0); left -= turn) {
         float x[U][8];
-        int64_t to[U], row_at[U];                // elements of k or v, rows of the cache
+        int64_t to[U], row_at[U];                  // elements of k or v, rows of the cache
         int sides[U];
         float scale[U];
         u32x4_t raw[U][sizeof(T) / 2];
         uint2 raw8[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t i = i0 + (int64_t)u * GROUPS + g;
             to[u] = -1;
             scale[u] = 0.f;
-            if (i >= end) continue;
-            const int sd = i >= half;
-            const int64_t item = i - (sd ? half : 0);
-            const int r = (int)(item / s.KV), h = (int)(item - (int64_t)r * s.KV);
-            if (n < 0 || sd != side || r < first[n]) {
-                int a = 0, b = s.N;              // the last sequence whose first row is at most r
-                while (b - a > 1) {
-                    const int c = (a + b) / 2;
-                    if (first[c] <= r) a = c;
-                    else b = c;
-                }
-                n = a, side = sd;
-            }
-            while (first[n + 1] <= r) ++n;
-            const int o = r - first[n], have = lengths ? lengths[n] : 0, slot = slots ? slots[n] : n;
-            const int64_t t0 = cu ? cu[n] : (int64_t)n * s.per_seq;
-            int t, row;
+            if (left - (int64_t)u * GROUPS <= 0) continue;
+            if (n == s.N || r >= next) enter();
+            const int o = r - first[n], t = READ ? o : o < head ? o : o + jump;
+            int row;
             if (READ) {
-                t = o;
-                row = have <= rows || o < s.sinks
-                          ? o
-                          : cache_row(have - s.window + (o - s.sinks), s.window, s.sinks);
+                int x0 = ring + o;
+                if (x0 >= s.window) x0 -= s.window;
+                row = o < head ? o : s.sinks + x0;
             } else {
-                const int len = (cu ? cu[n + 1] : (int)(t0 + s.per_seq)) - (int)t0, tail = min(len, s.window);
-                const int head = first[n + 1] - first[n] - tail;
-                t = o < head ? o : len - tail + (o - head);
-                row = cache_row(have + t, s.window, s.sinks);
+                // tokens before the ring's rows are sinks, in their own rows; ring + o < 0 too
+                int x0 = ring + o;
+                if (x0 >= s.window) x0 -= s.window;
+                row = o < head ? (lengths ? lengths[n] : 0) + o : s.sinks + x0;
             }
-            to[u] = ((t0 + t) * s.KV + h) * D;
-            row_at[u] = (((int64_t)sd * s.P + slot) * s.KV + h) * rows + row;
-            sides[u] = sd;
+            to[u] = (((int64_t)tokens0 + t) * s.KV + h) * D;
+            row_at[u] = page + (int64_t)h * rows + row;
+            sides[u] = side;
             if (READ) {
                 if constexpr (Q8) {
                     raw8[u] = *reinterpret_cast<const uint2 *>(static_cast<const char *>(cache) + row_at[u] * D + 8 * l);
@@ -144,11 +164,15 @@ __global__ __launch_bounds__(kThreads) void cache_rows_kernel(CacheShape s, cons
                             static_cast<const char *>(cache) + (row_at[u] * D + 8 * l) * (int64_t)sizeof(T) + 16 * e);
                 }
             } else {
-                const T *from = (sd ? v : k) + to[u] + 8 * l;
+                const T *from = (side ? v : k) + to[u] + 8 * l;
 #pragma unroll
                 for (int e = 0; e < (int)sizeof(T) / 2; ++e)
                     raw[u][e] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(from) + e);
             }
+            h += step_h;
+            r += step_r;
+            if (h >= s.KV) h -= s.KV, ++r;
+            if (r >= total) r -= total, ++side, n = s.N;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {

@@ -45,7 +45,7 @@ hipError_t launch_swa_fwd(const SwaArgs &a, hipStream_t stream);
 hipError_t launch_swa_bwd(const SwaArgs &a, hipStream_t stream);
 
 // Tokens of far queries in one part of the sinks' key gradient.
-inline int swa_far_chunk(int window) { return window + kSwaKeyTile < 1024 ? 1024 : window + kSwaKeyTile; }
+inline int swa_far_chunk(int window) { return window + kSwaKeyTile < 256 ? 256 : window + kSwaKeyTile; }
 
 // Builds the tables of units of a packed batch, int2 {sequence, unit of the
 // sequence}: tiles of `tokens` query tokens, and for the backward pass the far

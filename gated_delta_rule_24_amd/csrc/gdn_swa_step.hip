@@ -20,6 +20,7 @@ namespace gdn {
 
 constexpr int kTile = 32;             // rows of a wave's tile
 constexpr int kStepWaves = 4;
+constexpr int kMaxSplits = 1024;      // parts of a sequence's rows: a lane each in the join
 
 struct StepShape {
     int32_t P, KV, H, G, window, sinks, N, splits, per;   // per: rows of a part
@@ -51,27 +52,8 @@ __device__ __forceinline__ void mma16(float4_t &acc, u32x4_t a, u32x4_t b) {
     }
 }
 
-// The new token's row of k or v into the cache, by D / 8 lanes.
 template <typename T, bool Q8, int D>
-__device__ __forceinline__ void put_row(const T *__restrict__ from, char *cache, float *scales, int64_t row, int l) {
-    float x[8];
-    load8_f32(from + 8 * l, x);
-    if constexpr (Q8) {
-        const float sc = e4m3_scale(row_amax<D / 8>(x)), inv = e4m3_inverse(sc);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= inv;
-        *reinterpret_cast<uint2 *>(cache + row * D + 8 * l) = to_e4m3(x);
-        if (l == 0) scales[row] = sc;
-    } else {
-        const u32x4_t *f = reinterpret_cast<const u32x4_t *>(from + 8 * l);
-        u32x4_t *t = reinterpret_cast<u32x4_t *>(cache + (row * D + 8 * l) * (int64_t)sizeof(T));
-#pragma unroll
-        for (int e = 0; e < (int)sizeof(T) / 2; ++e) t[e] = f[e];
-    }
-}
-
-template <typename T, bool Q8, int D>
-__global__ __launch_bounds__(64 * kStepWaves) void swa_step_kernel(
+__global__ __launch_bounds__(64 * kStepWaves, (Rows<T, D>::RB > 256 ? 2 : 4)) void swa_step_kernel(
     StepShape s, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, char *cache, float *scales,
     const int32_t *__restrict__ lengths, const int32_t *__restrict__ slots, T *__restrict__ o,
     float *__restrict__ parts, int32_t *__restrict__ status) {
@@ -82,6 +64,8 @@ __global__ __launch_bounds__(64 * kStepWaves) void swa_step_kernel(
     using R = Rows<T, D>;
     __shared__ __align__(16) char s_v[kStepWaves][kTile * RB];   // V tiles; then the waves' O
     __shared__ float s_m[kStepWaves][16], s_l[kStepWaves][16], s_ks[Q8 ? kStepWaves : 1][2 * kTile];
+    __shared__ __align__(16) char s_new[2][Q8 ? RC : 16];        // the new token's rows as the cache holds them
+    __shared__ float s_newscale[2];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, m = l & 15, hq = l >> 4;
     const int n = blockIdx.x / s.KV, hk = blockIdx.x - n * s.KV, split = blockIdx.y;
     const int rows = s.window + s.sinks;
@@ -99,29 +83,53 @@ __global__ __launch_bounds__(64 * kStepWaves) void swa_step_kernel(
         if (tid == 0) status[0] = s.N, status[1] = bad;
     }
     if (n >= s.N) return;                         // no sequences: one block, for the status
+
+    constexpr int L = D / 8;
+    const bool second = tid >= L;                 // lanes of the new token's rows: k's, then v's
+    Raw8<T> fresh;
+    const T *from = (second ? v : k) + ((int64_t)n * s.KV + hk) * D + 8 * (tid % L);
+    if (Q8 && tid < 2 * L) fresh.load(from);      // does not depend on the slot
     const int slot = slots ? slots[n] : n, pos = lengths[n];
     int bad = slot < 0 || slot >= s.P || pos < 0 || pos >= kCacheMaxLength;
-    if (slots) {                                  // another sequence of the call on this slot
-        int twice = 0;
-        for (int i = tid; i < s.N; i += NT) twice |= i != n && slots[i] == slot;
-        bad |= __syncthreads_or(twice);
-    }
-    const int live = bad ? 0 : min(pos + 1, rows);
-    const int r0 = split * s.per, r1 = min(r0 + s.per, live);
-    const int64_t head = ((int64_t)(bad ? 0 : slot) * s.KV + hk) * rows, side = (int64_t)s.P * s.KV * rows;
-
-    if (!bad) {
-        const int row = cache_row(pos, s.window, s.sinks);
-        if (row >= r0 && row < r1) {              // the block that reads the row writes it
-            constexpr int L = D / 8;
-            if (tid < 2 * L) {
-                const int64_t from = ((int64_t)n * s.KV + hk) * D;
-                const bool second = tid >= L;
-                put_row<T, Q8, D>((second ? v : k) + from, cache, scales, head + row + (second ? side : 0), tid % L);
-            }
-            __syncthreads();
+    const int put = bad ? 0 : cache_row(pos, s.window, s.sinks);
+    const int r0 = split * s.per;
+    uint2 put8{};
+    float putscale = 1.f;
+    // The block that reads the new token's row writes it.  In 8 bits it takes it from
+    // LDS, as memory may still hold the row that it replaces; else it waits for the
+    // store (256 sequences, 2052 rows: 8 bits 106 us so, 112 with the wait; bf16 190,
+    // for want of registers, and 181).
+    if (tid < 2 * L && put >= r0 && put < r0 + s.per) {
+        if constexpr (Q8) {
+            float x[8];
+            fresh.to_f32(x);
+            putscale = e4m3_scale(row_amax<L>(x));
+            const float inv = e4m3_inverse(putscale);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= inv;
+            put8 = to_e4m3(x);
+            *reinterpret_cast<uint2 *>(&s_new[second][8 * (tid % L)]) = put8;
+            s_newscale[second] = putscale;
         }
     }
+    int twice = 0;                                // another sequence of the call on this slot
+    if (slots)
+        for (int i = tid; i < s.N; i += NT) twice |= i != n && slots[i] == slot;
+    bad |= __syncthreads_or(twice);
+    const int live = bad ? 0 : min(pos + 1, rows), r1 = min(r0 + s.per, live);
+    const int64_t head = ((int64_t)(bad ? 0 : slot) * s.KV + hk) * rows, side = (int64_t)s.P * s.KV * rows;
+    const bool mine = put >= r0 && put < r1;
+    if (mine && tid < 2 * L) {
+        const int64_t row = head + put + (second ? side : 0);
+        if constexpr (Q8) {
+            *reinterpret_cast<uint2 *>(cache + row * D + 8 * (tid % L)) = put8;
+            if (tid % L == 0) scales[row] = putscale;
+        } else {
+            fresh.load(from);
+            fresh.store_lds(reinterpret_cast<T *>(cache) + row * D + 8 * (tid % L));
+        }
+    }
+    if (!Q8 && mine) __syncthreads();
 
     // the heads' queries, as columns; heads past the group repeat its last
     const int64_t qat = ((int64_t)n * s.H + hk * s.G + min(m, s.G - 1)) * D;
@@ -140,6 +148,10 @@ __global__ __launch_bounds__(64 * kStepWaves) void swa_step_kernel(
     for (int dt = 0; dt < ND; ++dt) acc[dt] = float4_t{0.f, 0.f, 0.f, 0.f};
     float top = -__builtin_inff(), sum = 0.f;
     char *vt = s_v[wave];
+    // 16 bytes (8) at byte b of row r of k or v, from LDS where it is the new one
+    auto renew = [&](auto &x, int r, int which, int b) {
+        if (r == put) x = *reinterpret_cast<const std::remove_reference_t<decltype(x)> *>(&s_new[which][b]);
+    };
     const char *kbase = cache + head * RC, *vbase = kbase + side * RC;
 
     for (int t0 = r0 + wave * kTile; t0 < r1; t0 += kStepWaves * kTile) {
@@ -152,16 +164,22 @@ __global__ __launch_bounds__(64 * kStepWaves) void swa_step_kernel(
             vr[i] = *reinterpret_cast<const u32x4_t *>(vbase + (int64_t)min(r, r1 - 1) * RC + 16 * (l % VL));
             if (r >= r1) vr[i] = u32x4_t{0u, 0u, 0u, 0u};
         }
+        const bool newest = Q8 && mine && put >= t0 && put < t0 + kTile;
+        if (newest)
+#pragma unroll
+            for (int i = 0; i < VN; ++i) renew(vr[i], t0 + i * VR + l / VL, 1, 16 * (l % VL));
         float sc[2][4], vs = 1.f;
         if constexpr (Q8) {
             // lane x < 32: scale of K's row, x >= 32: of V's
             const int r = min(t0 + (l & 31), r1 - 1);
             vs = scales[head + r + (l >= 32 ? side : 0)];
+            if (newest && r == put) vs = s_newscale[l >= 32];
         }
         float4_t S[2] = {float4_t{0.f, 0.f, 0.f, 0.f}, float4_t{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-            const char *kr = kbase + (int64_t)min(t0 + 16 * a + m, r1 - 1) * RC;
+            const int kr_row = min(t0 + 16 * a + m, r1 - 1);
+            const char *kr = kbase + (int64_t)kr_row * RC;
             if constexpr (!Q8) {
                 u32x4_t f[NS];
 #pragma unroll
@@ -172,6 +190,9 @@ __global__ __launch_bounds__(64 * kStepWaves) void swa_step_kernel(
                 u32x4_t f[D / 64];
 #pragma unroll
                 for (int x = 0; x < D / 64; ++x) f[x] = *reinterpret_cast<const u32x4_t *>(kr + 64 * x + 16 * hq);
+                if (newest)
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x) renew(f[x], kr_row, 0, 64 * x + 16 * hq);
 #pragma unroll
                 for (int x = 0; x < D / 64; ++x) {
                     if constexpr (F32) {
@@ -196,7 +217,8 @@ __global__ __launch_bounds__(64 * kStepWaves) void swa_step_kernel(
                     }
                 }
             } else {
-                const uint2 f = *reinterpret_cast<const uint2 *>(kr + 8 * hq);
+                uint2 f = *reinterpret_cast<const uint2 *>(kr + 8 * hq);
+                if (newest) renew(f, kr_row, 0, 8 * hq);
                 if constexpr (F32) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
@@ -310,10 +332,10 @@ __global__ __launch_bounds__(64 * kStepWaves) void swa_step_kernel(
     sum += __shfl_xor(sum, 32, 64);
     __syncthreads();
     if (hq == 0) s_m[wave][m] = top, s_l[wave][m] = sum;
-    float *mine = reinterpret_cast<float *>(vt);   // [16 heads][D], half of a 16-bit V tile's rows
+    float *own_o = reinterpret_cast<float *>(vt);   // [16 heads][D], half of a 16-bit V tile's rows
 #pragma unroll
     for (int dt = 0; dt < ND; ++dt)
-        *reinterpret_cast<float4_t *>(mine + m * D + 16 * dt + 4 * hq) = acc[dt];
+        *reinterpret_cast<float4_t *>(own_o + m * D + 16 * dt + 4 * hq) = acc[dt];
     __syncthreads();
     const int64_t out = ((int64_t)n * s.H + hk * s.G) * D;
     const bool whole = s.splits == 1;
@@ -340,34 +362,50 @@ __global__ __launch_bounds__(64 * kStepWaves) void swa_step_kernel(
     }
 }
 
-// Joins the parts of one (sequence, query head) in their order.
-template <typename T>
-__global__ __launch_bounds__(256) void swa_step_join_kernel(StepShape s, int D, const float *__restrict__ parts,
-                                                            T *__restrict__ o) {
-    const int n = blockIdx.x / s.KV, hk = blockIdx.x - n * s.KV;
+// Joins the parts of one (sequence, query head): groups of D lanes take the parts in
+// turn and join in LDS, in a fixed order.
+template <typename T, int D>
+__global__ __launch_bounds__(1024) void swa_step_join_kernel(StepShape s, const float *__restrict__ parts,
+                                                             T *__restrict__ o) {
+    __shared__ float s_w[kMaxSplits], s_x[1024], s_m[16], s_z[16];
+    const int tid = threadIdx.x, g = blockIdx.x % s.G, unit = blockIdx.x / s.G, n = unit / s.KV, hk = unit - n * s.KV;
+    const int nt = blockDim.x, waves = (nt + 63) / 64, groups = nt / D;
     const int64_t step = (int64_t)s.G * (D + 2);
-    const float *from = parts + (int64_t)blockIdx.x * s.splits * step;
-    const int64_t out = ((int64_t)n * s.H + hk * s.G) * D;
-    const int i = blockIdx.y * 256 + threadIdx.x, g = i / D;
-    if (i >= s.G * D) return;
+    const float *from = parts + (int64_t)unit * s.splits * step + 2 * g;
     float up = -__builtin_inff(), z = 0.f, x = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < s.splits; ++p) up = fmaxf(up, from[p * step + 2 * g]);
+    for (int p = tid; p < s.splits; p += nt) up = fmaxf(up, from[p * step]);
+    for (int d = 32; d >= 1; d >>= 1) up = fmaxf(up, __shfl_xor(up, d, 64));
+    if ((tid & 63) == 0) s_m[tid >> 6] = up;
+    __syncthreads();
+    for (int w = 0; w < waves; ++w) up = fmaxf(up, s_m[w]);
     const float base = up == -__builtin_inff() ? 0.f : up;
-#pragma unroll 4
-    for (int p = 0; p < s.splits; ++p) {
-        const float f = __builtin_amdgcn_exp2f(from[p * step + 2 * g] - base);
-        z += f * from[p * step + 2 * g + 1];
-        x += f * from[p * step + 2 * s.G + i];
+    for (int p = tid; p < s.splits; p += nt) {
+        const float f = __builtin_amdgcn_exp2f(from[p * step] - base);
+        s_w[p] = f;
+        z = fmaf(f, from[p * step + 1], z);
     }
-    o[out + i] = round_to<T>(z == 0.f ? 0.f : x / z);
+    for (int d = 32; d >= 1; d >>= 1) z += __shfl_xor(z, d, 64);
+    if ((tid & 63) == 0) s_z[tid >> 6] = z;
+    __syncthreads();
+    z = 0.f;
+    for (int w = 0; w < waves; ++w) z += s_z[w];
+    const int d = tid % D, q = tid / D;
+    from += 2 * (s.G - g) + g * D + d;
+#pragma unroll 8
+    for (int p = q; p < s.splits; p += groups) x = fmaf(s_w[p], from[p * step], x);
+    s_x[tid] = x;
+    __syncthreads();
+    if (q) return;
+    x = 0.f;
+    for (int i = 0; i < groups; ++i) x += s_x[i * D + d];
+    o[((int64_t)n * s.H + hk * s.G + g) * D + d] = round_to<T>(z == 0.f ? 0.f : x / z);
 }
 
 // Enough blocks for the GPU, each with a tile for every wave at least.
 int swa_step_splits(const SwaStepArgs &a) {
     const int64_t rows = (int64_t)a.c.window + a.c.sinks, units = std::max<int64_t>((int64_t)a.c.N * a.c.KV, 1);
     const int64_t most = std::max<int64_t>(rows / (kStepWaves * kTile), 1);
-    return (int)std::max<int64_t>(std::min<int64_t>(1024 / units, std::min<int64_t>(most, 1024)), 1);
+    return (int)std::max<int64_t>(std::min<int64_t>(1024 / units, std::min<int64_t>(most, kMaxSplits)), 1);
 }
 
 size_t swa_step_workspace(const SwaStepArgs &a) {
@@ -397,8 +435,9 @@ hipError_t launch_swa_step(const SwaStepArgs &a, hipStream_t st) {
         hipError_t e = hipGetLastError();
         if (e != hipSuccess || s.splits == 1 || c.N == 0) return e;
         ProfScope prof("gdn_swa_step_join", st);
-        swa_step_join_kernel<T><<<dim3(c.N * c.KV, (s.G * D + 255) / 256), 256, 0, st>>>(s, D, parts,
-                                                                                       static_cast<T *>(a.o));
+        // eight parts to a group of lanes
+        const int nt = std::max(D * std::max(std::min((s.splits + 7) / 8, 1024 / D), 1), 64);
+        swa_step_join_kernel<T, D><<<c.N * a.H, nt, 0, st>>>(s, parts, static_cast<T *>(a.o));
         return hipGetLastError();
     };
     return swa_with<true>(c.dtype, c.D, [&](auto t, auto dim) {
