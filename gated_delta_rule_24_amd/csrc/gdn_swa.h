@@ -44,8 +44,9 @@ SwaWorkspace swa_workspace_layout(const SwaArgs &a, bool bwd);
 hipError_t launch_swa_fwd(const SwaArgs &a, hipStream_t stream);
 hipError_t launch_swa_bwd(const SwaArgs &a, hipStream_t stream);
 
-// Tokens of far queries in one part of the sinks' key gradient.
-inline int swa_far_chunk(int window) { return window + kSwaKeyTile < 256 ? 256 : window + kSwaKeyTile; }
+// Tokens of far queries in one part of the sinks' key gradient: as many as the near
+// part of a key tile has.
+inline int swa_far_chunk(int window) { return window + kSwaKeyTile; }
 
 // Builds the tables of units of a packed batch, int2 {sequence, unit of the
 // sequence}: tiles of `tokens` query tokens, and for the backward pass the far

@@ -436,10 +436,13 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
     }
 }
 
-// Adds the parts' shares of the sinks' gradients, in their order.
+// Adds the parts' shares of the sinks' gradients: 32 neighbouring elements by 32 groups
+// of lanes, which take the parts in turn and join in LDS, in a fixed order.
+constexpr int kSinkLanes = 32;
 template <typename T>
-__global__ __launch_bounds__(256) void swa_sinks_kernel(SwaShape sh, int far, int D, const float *__restrict__ share,
-                                                        T *__restrict__ dk, T *__restrict__ dv) {
+__global__ __launch_bounds__(1024) void swa_sinks_kernel(SwaShape sh, int far, int D, const float *__restrict__ share,
+                                                         T *__restrict__ dk, T *__restrict__ dv) {
+    __shared__ float sum[32][kSinkLanes + 1];
     if (sh.cu && sh.meta[1]) return;
     const int n = blockIdx.x / sh.KV, hk = blockIdx.x - n * sh.KV;
     int64_t q0 = (int64_t)n * sh.T, k0 = (int64_t)n * sh.Tk;
@@ -450,19 +453,24 @@ __global__ __launch_bounds__(256) void swa_sinks_kernel(SwaShape sh, int far, in
     }
     const FarParts fp = far_parts(Lq, Lk, sh.window, sh.sinks, far);
     if (fp.parts == 0) return;
-    const int i = blockIdx.y * 256 + threadIdx.x, size = min(sh.sinks, Lk) * D;
-    if (i >= size) return;
-    const int64_t step = (int64_t)sh.KV * 2 * sh.sinks * D;
-    const float *from = share + far_first(q0, n, far) * step + (int64_t)hk * 2 * sh.sinks * D + i;
-    float a = 0.f, b = 0.f;
-#pragma unroll 8
-    for (int p = 0; p <= fp.parts; ++p) {
-        a += from[p * step];
-        b += from[p * step + (int64_t)sh.sinks * D];
-    }
-    const int64_t to = ((k0 + i / D) * sh.KV + hk) * D + i % D;
-    dk[to] = round_to<T>(a);
-    dv[to] = round_to<T>(b);
+    // dK's elements, then dV's; D is a multiple of 32, so a block has one of them
+    const int x = threadIdx.x % kSinkLanes, g = threadIdx.x / kSinkLanes, all = sh.sinks * D;
+    const int i = blockIdx.y * kSinkLanes + x, e = i < all ? i : i - all;
+    const int64_t step = (int64_t)sh.KV * 2 * all;
+    const float *from = share + far_first(q0, n, far) * step + (int64_t)hk * 2 * all + i;
+    const bool on = e / D < Lk;
+    float a = 0.f;
+    if (on)
+#pragma unroll 4
+        for (int p = g; p <= fp.parts; p += 32) a += from[p * step];
+    sum[g][x] = a;
+    __syncthreads();
+    if (g || !on) return;
+    a = 0.f;
+#pragma unroll
+    for (int p = 0; p < 32; ++p) a += sum[p][x];
+    T *to = i < all ? dk : dv;
+    to[((k0 + e / D) * sh.KV + hk) * D + e % D] = round_to<T>(a);
 }
 
 hipError_t launch_swa_bwd(const SwaArgs &a, hipStream_t st) {
@@ -527,8 +535,8 @@ hipError_t launch_swa_bwd(const SwaArgs &a, hipStream_t st) {
         }
         if (join) {
             ProfScope prof("gdn_swa_sinks", st);
-            const dim3 grid((unsigned)(a.N * a.KV), (unsigned)((a.sinks * D + 255) / 256));
-            swa_sinks_kernel<T><<<grid, 256, 0, st>>>(s, far, D, share, out(a.dk), out(a.dv));
+            const dim3 grid((unsigned)(a.N * a.KV), (unsigned)(2 * a.sinks * D / kSinkLanes));
+            swa_sinks_kernel<T><<<grid, 1024, 0, st>>>(s, far, D, share, out(a.dk), out(a.dv));
             e = hipGetLastError();
         }
         return e;
