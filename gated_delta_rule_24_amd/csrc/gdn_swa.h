@@ -199,6 +199,27 @@ struct Rows {
     __device__ __forceinline__ static u32x4_t frag(const char *t, const Lane &ln, int r0, int s) {
         return *reinterpret_cast<const u32x4_t *>(t + (ln.row ^ (s << 5)) + r0 * RB);
     }
+    // S[n] += the product over D of rows r0 + 32 n .. +31 with the operand b, N tiles side by
+    // side.  The reads go in batches, each ahead of the products of the one before it:
+    // left to itself the compiler puts a read right in front of its product.
+    template <int N>
+    __device__ __forceinline__ static void dot(f32x16_t (&S)[N], const char *t, const Lane &ln, int r0,
+                                               const u32x4_t (&b)[NS]) {
+        constexpr int ALL = N * NS, BATCH = F32 ? 2 : 8;
+        auto read = [&](int i) { return frag(t, ln, r0 + 32 * (i % N), i / N); };
+        u32x4_t f[2][BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH && i < ALL; ++i) f[0][i] = read(i);
+#pragma unroll
+        for (int i0 = 0; i0 < ALL; i0 += BATCH) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < BATCH && i0 + BATCH + i < ALL; ++i) f[(i0 / BATCH + 1) & 1][i] = read(i0 + BATCH + i);
+#pragma unroll
+            for (int i = 0; i < BATCH && i0 + i < ALL; ++i)
+                mma32<T>(S[(i0 + i) % N], f[(i0 / BATCH) & 1][i], b[(i0 + i) / N]);
+        }
+    }
     // Columns 32 dt .. +31 of rows r0 .. r0 + 31 as the A operand of a product
     // over the rows, in the order in which an accumulator holds its rows.
     // 16 bits: rows 16 ks .. +15 of them.
@@ -326,6 +347,21 @@ struct Rows {
         else return (float)__builtin_bit_cast(_Float16, (uint16_t)x);
     }
 };
+
+// Asks for an order of the block's instructions: the LDS reads of AHEAD products
+// (READS each) before the first of N products, then with each product the reads of
+// the one that far behind it.
+template <int READS, int N, int AHEAD>
+__device__ __forceinline__ void reads_ahead() {
+    constexpr int DS_READ = 0x100, MFMA = 0x8, FIRST = AHEAD < N ? AHEAD : N;
+    __builtin_amdgcn_sched_group_barrier(DS_READ, READS * FIRST, 0);
+#pragma unroll
+    for (int i = 0; i < N - FIRST; ++i) {
+        __builtin_amdgcn_sched_group_barrier(MFMA, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(DS_READ, READS, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(MFMA, FIRST, 0);
+}
 
 // ---- staging ---------------------------------------------------------------------
 

@@ -114,10 +114,7 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
             for (int n = 0; n < NSUB; ++n)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) S[n][i] = 0.f;
-#pragma unroll
-            for (int s = 0; s < R::NS; ++s)
-#pragma unroll
-                for (int n = 0; n < NSUB; ++n) mma32<T>(S[n], R::frag(kt, ln, r0 + 32 * n, s), qf[s]);
+            R::dot(S, kt, ln, r0, qf);
             uint32_t seen = 0;
             if constexpr (MASK) {
 #pragma unroll
@@ -160,6 +157,7 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
             }
 #pragma unroll
             for (int n = 0; n < NSUB; ++n) R::add(acc, vt, ln, r0 + 32 * n, S[n]);
+            if constexpr (!MASK && !R::F32) reads_ahead<2, NSUB * 2 * R::ND, 4>();
         };
         using std::integral_constant;
         if (tiles) load(0);

@@ -322,10 +322,7 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
             for (int n = 0; n < NSUB; ++n)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) S[n][i] = P[n][i] = 0.f;
-#pragma unroll
-            for (int s = 0; s < R::NS; ++s)
-#pragma unroll
-                for (int n = 0; n < NSUB; ++n) mma32<T>(S[n], R::frag(qt, ln, r0 + 32 * n, s), kf[s]);
+            R::dot(S, qt, ln, r0, kf);
             uint32_t seen = 0;
 #pragma unroll
             for (int a = 0; a < 4 * NSUB; ++a) {
@@ -358,10 +355,7 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
                 }
             }
             if constexpr (!MAKE_K) return;
-#pragma unroll
-            for (int s = 0; s < R::NS; ++s)
-#pragma unroll
-                for (int n = 0; n < NSUB; ++n) mma32<T>(P[n], R::frag(gt, ln, r0 + 32 * n, s), vf[s]);
+            R::dot(P, gt, ln, r0, vf);
 #pragma unroll
             for (int a = 0; a < 4 * NSUB; ++a) {
                 const float4_t dd = *reinterpret_cast<const float4_t *>(sr + kRows + 8 * a);
