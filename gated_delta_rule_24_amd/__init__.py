@@ -615,6 +615,9 @@ def state_move_check(status: torch.Tensor) -> int:
 
 # ---- windowed attention and its resident cache --------------------------------------
 
+_INT32 = 2 ** 31 - 1
+
+
 @functools.lru_cache(maxsize=256)
 def _swa_desc(which, *fields):
     """Descriptor of these sizes and types, and the workspace size of gdn_swa_<which>."""
@@ -624,16 +627,18 @@ def _swa_desc(which, *fields):
     return d, int(n.value)
 
 
-def _swa_call(which, q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, scale, workspace):
-    """Device, shapes, descriptor and workspace of a swa_fwd or swa_bwd call."""
-    dev = _cuda(q, "q")
-    _need(q, "q", _FLOATS, dev, 4)
-    B, T, H, d = shape = tuple(q.shape)
-    _need(k, "k", (q.dtype,), dev, 4)
+def _swa_call(which, q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, scale):
+    """Device, q's shape, key offsets, descriptor and workspace size of a swa_fwd or swa_bwd call."""
+    dev, types = _cuda(q, "q"), (q.dtype,)
+    if q.dtype not in _FLOATS or q.dim() != 4 or not q.is_contiguous():
+        _need(q, "q", _FLOATS, dev, 4)
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        _need(k, "k", types, dev, 4)
+    B, T, H, d = shape = q.shape
     Tk, KV = k.shape[1], k.shape[2]
     kshape = (B, Tk, KV, d)
-    _shaped(k, "k", kshape, (q.dtype,), dev)
-    _shaped(v, "v", kshape, (q.dtype,), dev)
+    _shaped(k, "k", kshape, types, dev)
+    _shaped(v, "v", kshape, types, dev)
     N = B
     if cu_seqlens is None:
         if cu_seqlens_k is not None:
@@ -647,9 +652,11 @@ def _swa_call(which, q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, scale, wo
             cu_seqlens_k = cu_seqlens
         else:
             _shaped(cu_seqlens_k, "cu_seqlens_k", (N + 1,), (torch.int32,), dev)
-    desc, need = _swa_desc(which, B, T, Tk, H, KV, d, N, window, sinks, _DT[q.dtype],
+    if not -_INT32 <= sinks <= _INT32:
+        raise ValueError(f"sinks {sinks} is no 32-bit number")
+    desc, need = _swa_desc(which, B, T, Tk, H, KV, d, N, max(min(window, _INT32), -_INT32), sinks, _DT[q.dtype],
                            d ** -0.5 if scale is None else scale)
-    return dev, shape, kshape, cu_seqlens_k, desc, *_workspace(workspace, need, dev)
+    return dev, shape, cu_seqlens_k, desc, need
 
 
 def swa_fwd_workspace_size(B, T, Tk, H, KV, d, num_seqs, window, sinks=0, dtype=torch.bfloat16) -> int:
@@ -667,13 +674,16 @@ def swa_fwd(q, k, v, window, sinks=0, cu_seqlens=None, cu_seqlens_k=None, *, sca
     scale: None for 1 / sqrt(d).  Returns (o [B,T,H,d], lse [B,T,H] fp32 or
     None without `lse`).
     """
-    dev, shape, _, cu_k, desc, workspace, size = _swa_call("fwd", q, k, v, window, sinks, cu_seqlens, cu_seqlens_k,
-                                                           scale, workspace)
+    dev, shape, cu_k, desc, size = _swa_call("fwd", q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, scale)
     if o is None:
-        o = torch.empty(shape, dtype=q.dtype, device=dev)
+        o = torch.empty_like(q)
     else:
         _shaped(o, "o", shape, (q.dtype,), dev)
     lse = torch.empty(shape[:3], dtype=torch.float32, device=dev) if lse else None
+    if cu_seqlens is None:
+        workspace, size = None, 0
+    else:
+        workspace, size = _workspace(workspace, size, dev)
     _call("gdn_swa_fwd", dev, desc, _addr(q), _addr(k), _addr(v), _addr(cu_seqlens), _addr(cu_k), _addr(o),
           _addr(lse), _addr(workspace), size)
     return o, lse
@@ -690,13 +700,12 @@ def swa_bwd(d_o, q, k, v, o, lse, window, sinks=0, cu_seqlens=None, cu_seqlens_k
     and lse as it returned them; d_o [B,T,H,d] in their dtype.  Returns (dq, dk,
     dv) in that dtype.
     """
-    dev, shape, kshape, cu_k, desc, workspace, size = _swa_call("bwd", q, k, v, window, sinks, cu_seqlens, cu_seqlens_k,
-                                                                scale, workspace)
+    dev, shape, cu_k, desc, size = _swa_call("bwd", q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, scale)
     _shaped(d_o, "d_o", shape, (q.dtype,), dev)
     _shaped(o, "o", shape, (q.dtype,), dev)
     _shaped(lse, "lse", shape[:3], (torch.float32,), dev)
-    dq = torch.empty(shape, dtype=q.dtype, device=dev)
-    dk, dv = (torch.empty(kshape, dtype=q.dtype, device=dev) for _ in range(2))
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
+    workspace, size = _workspace(workspace, size, dev)
     _call("gdn_swa_bwd", dev, desc, _addr(d_o), _addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), _addr(cu_seqlens),
           _addr(cu_k), _addr(dq), _addr(dk), _addr(dv), _addr(workspace), size)
     return dq, dk, dv
@@ -813,16 +822,19 @@ def swa_step(cache, q, k, v, lengths, sinks=0, scales=None, slots=None, *, scale
     when all layers have run.  A sequence with slot -1 is left out, its o is
     zeros.  Returns o [N,H,d]."""
     dev, desc = _cache_call(cache, scales, slots, lengths, sinks)
-    _need(q, "q", _FLOATS, dev, 3)
-    N, H, d = shape = tuple(q.shape)
-    _shaped(k, "k", (N, desc.kv_heads, d), (q.dtype,), dev)
-    _shaped(v, "v", (N, desc.kv_heads, d), (q.dtype,), dev)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.dtype not in _FLOATS or not q.is_contiguous() \
+            or q.device != dev:
+        _need(q, "q", _FLOATS, dev, 3)
+    N, H, d = shape = q.shape
+    kshape = (N, desc.kv_heads, d)
+    _shaped(k, "k", kshape, (q.dtype,), dev)
+    _shaped(v, "v", kshape, (q.dtype,), dev)
     if d != desc.dim:
         raise ValueError(f"q must be [N, H, {desc.dim}], got {shape}")
     if lengths is None or lengths.shape[0] != N:
         raise ValueError(f"lengths must have {N} entries")
     if o is None:
-        o = torch.empty(shape, dtype=q.dtype, device=dev)
+        o = torch.empty_like(q)
     else:
         _shaped(o, "o", shape, (q.dtype,), dev)
     if status is not None:

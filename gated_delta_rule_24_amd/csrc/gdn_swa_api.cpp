@@ -24,6 +24,14 @@ gdn_status check_heads(int32_t heads, int32_t kv_heads) {
     return GDN_OK;
 }
 
+SwaArgs swa_args(const gdn_swa_desc &d) {
+    SwaArgs a{};
+    a.B = d.batch, a.T = d.seqlen, a.Tk = d.keylen, a.N = d.num_seqs, a.H = d.heads, a.KV = d.kv_heads, a.D = d.dim;
+    // positions are below 2^30: a longer window sees as much, and sums with it stay in 32 bits
+    a.window = std::min(d.window, 1 << 30), a.sinks = d.sinks, a.dtype = d.dtype, a.scale = d.scale;
+    return a;
+}
+
 gdn_status check_swa_desc(const gdn_swa_desc *d, bool bwd) {
     if (!d) return fail(GDN_ERR_NULL, "desc is NULL");
     if (!valid_dtype(d->dtype)) return fail(GDN_ERR_DTYPE, "unknown dtype code %d", d->dtype);
@@ -40,25 +48,22 @@ gdn_status check_swa_desc(const gdn_swa_desc *d, bool bwd) {
     if (d->sinks > kSwaMaxSinks)
         return fail(GDN_ERR_UNSUPPORTED, "sinks %d not built (at most %d)", d->sinks, kSwaMaxSinks);
     if (!(std::isfinite(d->scale) && d->scale > 0.f)) return fail(GDN_ERR_UNSUPPORTED, "scale must be finite and > 0");
+    // a block for each unit and key head, two where the backward pass splits its key side
+    const SwaWorkspace w = swa_workspace_layout(swa_args(*d), bwd);
+    if (std::max(w.row_units, 2 * w.key_units) * (int64_t)d->kv_heads >= INT32_MAX - 7)
+        return fail(GDN_ERR_SHAPE, "too many sequences, tokens and kv_heads");
     if (d->flags) return fail(GDN_ERR_UNSUPPORTED, "unknown flags 0x%x", d->flags);
     return GDN_OK;
 }
 
-SwaArgs swa_args(const gdn_swa_desc &d) {
-    SwaArgs a{};
-    a.B = d.batch, a.T = d.seqlen, a.Tk = d.keylen, a.N = d.num_seqs, a.H = d.heads, a.KV = d.kv_heads, a.D = d.dim;
-    // positions are below 2^30: a longer window sees as much, and sums with it stay in 32 bits
-    a.window = std::min(d.window, 1 << 30), a.sinks = d.sinks, a.dtype = d.dtype, a.scale = d.scale;
-    return a;
-}
-
+// need: 0 where no workspace is read.
 gdn_status check_swa_layout(const gdn_swa_desc &d, const int32_t *cu, const int32_t *cuk, const void *workspace,
                             size_t workspace_bytes, size_t need) {
     if (!cu != !cuk) return fail(GDN_ERR_NULL, "cu_seqlens and cu_seqlens_k are given together or not at all");
     if (cu && d.batch != 1) return fail(GDN_ERR_SHAPE, "cu_seqlens requires batch == 1 (got %d)", d.batch);
     if (!cu && d.num_seqs != d.batch)
         return fail(GDN_ERR_SHAPE, "without cu_seqlens num_seqs must equal batch (%d != %d)", d.num_seqs, d.batch);
-    if (!workspace) return fail(GDN_ERR_WORKSPACE, "workspace is NULL");
+    if (need && !workspace) return fail(GDN_ERR_WORKSPACE, "workspace is NULL");
     if (workspace_bytes < need)
         return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, this call needs %zu", workspace_bytes, need);
     return GDN_OK;
@@ -172,7 +177,7 @@ gdn_status gdn_swa_fwd(const gdn_swa_desc *desc, const void *q, const void *k, c
     if (s != GDN_OK) return s;
     const gdn_swa_desc &d = *desc;
     SwaArgs a = swa_args(d);
-    const size_t need = swa_workspace_layout(a, false).total;
+    const size_t need = cu_seqlens ? swa_workspace_layout(a, false).total : 0;
     s = check_swa_layout(d, cu_seqlens, cu_seqlens_k, workspace, workspace_bytes, need);
     if (s != GDN_OK) return s;
     const size_t rows = (size_t)d.batch * d.seqlen * d.heads, keys = (size_t)d.batch * d.keylen * d.kv_heads;
@@ -184,7 +189,7 @@ gdn_status gdn_swa_fwd(const gdn_swa_desc *desc, const void *q, const void *k, c
                         {"cu_seqlens_k", cu_seqlens_k, offs, false, false, 4},
                         {"o", o, rows * row, rows > 0, true, 16},
                         {"lse", lse, rows * 4, false, true, 4},
-                        {"workspace", workspace, need, true, true, 16}};
+                        {"workspace", workspace, need, false, true, 16}};
     s = check_args(args, 8);
     if (s == GDN_OK) s = check_overlap(args, 8);
     if (s != GDN_OK) return s;

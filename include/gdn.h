@@ -605,8 +605,9 @@ gdn_status gdn_state_move(int32_t layers, int32_t slots, int64_t page_bytes, int
  *   sinks      S: 0..128
  *   dtype      of q, k, v, o and their gradients.  Products of 16-bit types run
  *              on the 16-bit matrix cores and add in fp32; the probabilities
- *              (and, backward, the scores' gradients) are rounded to dtype as
- *              operands.  Scores, maxima, sums and lse are fp32.
+ *              (and, backward, the scores' gradients, which FP16 holds below
+ *              65504) are rounded to dtype as operands.  Scores, maxima, sums
+ *              and lse are fp32.
  *   scale      finite and > 0
  *   flags      0
  * A sequence's queries are its last: the query i stands at position
@@ -655,7 +656,8 @@ gdn_status gdn_swa_bwd_workspace_size(const gdn_swa_desc *desc, size_t *bytes);
  *                 ...) reports them (1 to 3 as there, 4 to 6 for the keys').
  *   o             [B, T, H, d]    dtype (written)
  *   lse           [B, T, H]       fp32 or NULL (not returned), natural log
- *   workspace     at least gdn_swa_fwd_workspace_size bytes
+ *   workspace     at least gdn_swa_fwd_workspace_size bytes; may be NULL without
+ *                 cu_seqlens
  * Equal calls give equal bits.  q, k, v, o and the workspace must be 16-byte
  * aligned, the offsets and lse 4-byte.  o, lse and the workspace must not overlap
  * anything else.

@@ -29,7 +29,7 @@ BAD = [(dict(dtype=3), 3), (dict(dtype=-1), 3), (dict(batch=0), 2), (dict(seqlen
        (dict(heads=7), 2), (dict(heads=34, kv_heads=2), 5), (dict(heads=1040, kv_heads=65), 5), (dict(dim=96), 5),
        (dict(dim=512), 5), (dict(dim=256, dtype=0), 5), (dict(sinks=129), 5), (dict(scale=0.0), 5),
        (dict(scale=-1.0), 5), (dict(scale=float("inf")), 5), (dict(scale=float("nan")), 5), (dict(flags=1), 5),
-       (dict(batch=1 << 15, seqlen=1 << 15), 2), (dict(batch=1 << 15, keylen=1 << 15), 2)]
+       (dict(batch=1, num_seqs=1 << 30, heads=64, kv_heads=64), 2), (dict(batch=1 << 15, seqlen=1 << 15), 2), (dict(batch=1 << 15, keylen=1 << 15), 2)]
 
 
 @pytest.mark.parametrize("kw,code", BAD)
@@ -60,13 +60,15 @@ def test_fwd_refusals(lib):
     assert call(d=desc(window=0)) == 2
     for name in "qkvo":
         assert call(**{name: None}) == 1 and call(**{name: F + 8}) == 4, name
-    assert call(lse=E + 2) == 4 and call(ws=None) == 6 and call(size=8) == 6 and call(ws=WS + 4) == 4
+    assert call(lse=E + 2) == 4
     assert call(cu=F) == 1 and call(cuk=F) == 1                          # one without the other
     assert call(cu=F, cuk=G) == 2                                        # packed with batch 2
     one = desc(batch=1, num_seqs=3)
+    assert call(d=one, cu=F, cuk=G, ws=None) == 6 and call(d=one, cu=F, cuk=G, size=8) == 6
+    assert call(d=one, cu=F, cuk=G, ws=WS + 4) == 4 and call(d=one, cu=F, cuk=G, ws=A) == 8
     assert call(d=one, cu=F + 2, cuk=G) == 4 and call(d=one, cu=F, cuk=G + 1) == 4
     assert call(d=desc(num_seqs=3)) == 2
-    assert call(o=A) == 8 and call(o=B + 64) == 8 and call(lse=D_ + 16) == 8 and call(lse=C) == 8 and call(ws=A) == 8
+    assert call(o=A) == 8 and call(o=B + 64) == 8 and call(lse=D_ + 16) == 8 and call(lse=C) == 8
     assert b"overlaps" in lib.gdn_last_error_message()
 
 

@@ -196,3 +196,30 @@ def test_equal_calls_other_streams_and_graphs():
         o, lse = gdn.swa_fwd(*t, 50, 4, c)
         want = gdn.swa_bwd(g, *t, o, lse, 50, 4, c)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp32", 128), ("fp32", 64)])
+def test_graphs_of_the_wide_kernels(dtype, d):
+    """Kernels with more than 64 KiB of LDS, and those whose key side is split, captured and replayed."""
+    t, _ = inputs(32, 2, 300, 300, 4, 2, d, dtype)
+    g = torch.randn_like(t[0])
+    graph = torch.cuda.CUDAGraph()
+    o, lse = gdn.swa_fwd(*t, 40, 3)
+    gdn.swa_bwd(g, *t, o, lse, 40, 3)
+    with torch.cuda.graph(graph):
+        o, lse = gdn.swa_fwd(*t, 40, 3)
+        got = gdn.swa_bwd(g, *t, o, lse, 40, 3)
+    for seed in range(3):
+        for y in (*t, g):
+            y.copy_(torch.randn(y.shape, generator=torch.Generator("cuda").manual_seed(seed), device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        o2, lse2 = gdn.swa_fwd(*t, 40, 3)
+        want = gdn.swa_bwd(g, *t, o2, lse2, 40, 3)
+        assert torch.equal(o, o2) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_keys_that_repeat_the_queries_tensor():
+    """One tensor as q, k and v, as the gradients of a shared projection need it."""
+    t, x = inputs(40, 1, 70, 70, 2, 2, 32, "fp32")
+    check([t[0]] * 3, [x[0]] * 3, "fp32", 16, 1, label="q = k = v")
