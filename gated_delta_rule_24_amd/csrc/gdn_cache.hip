@@ -1,7 +1,10 @@
 // The resident cache of windowed attention, written and read back:
 //   position p of a sequence sits in row p (p < sinks), else sinks + (p - sinks) mod window
 // Rows are moved whole, in the cache's own type or as e4m3 with a power of two
-// per row (gdn_cache.h).  Both directions are bound by HBM.
+// per row (gdn_cache.h).  Both directions are bound by HBM.  Measured (MI355X, a copy of
+// 2 GiB 4.84 TB/s): 256 sequences' 8-bit rows read back to bf16, 4 heads of 128, 317 us
+// (1.5 GB, 4.7 TB/s); 64 prompts' last rows written in 8 bits 54 us (246 MB, 4.6), 2386
+// tokens of 256 sequences in bf16 8 to 9 us, most of it the look at the indices.
 //
 // Every block checks lengths, slots and offsets itself (a few KiB, in L2), so a bad
 // one makes all of them write nothing without a second launch; the same pass sums

@@ -39,7 +39,7 @@ struct SwaWorkspace {
     size_t off_rows, off_keys, off_dsum, off_far;
     size_t total;
 };
-int swa_row_tile(const SwaArgs &a, bool bwd);
+int swa_row_tile(const SwaArgs &a);
 SwaWorkspace swa_workspace_layout(const SwaArgs &a, bool bwd);
 hipError_t launch_swa_fwd(const SwaArgs &a, hipStream_t stream);
 hipError_t launch_swa_bwd(const SwaArgs &a, hipStream_t stream);

@@ -11,6 +11,16 @@
 // 16-byte LDS reads, V by transposing ones).  Q and O^T stay in registers.  The
 // waves of a block share tiles of 64 keys, copied straight to LDS one tile ahead.
 // Only tiles that the mask cuts are masked; tiles that it hides are not visited.
+//
+// Measured (MI355X; a bf16 8192^3 product 1.23 PFLOP/s, a copy 5.35 TB/s): 50408 packed
+// tokens, 16 heads of 128, window 2048, bf16: 810 to 860 us from one GPU to another, 0.85
+// PFLOP/s of visible pairs.  The matrix cores are busy 42% of the time and the vector units about as
+// long (per 64 keys and wave 32 products of 32 cycles, 127 vector instructions, 32
+// exponentials of 16 cycles): two waves a SIMD, all that the registers allow, overlap
+// the two in part.  Reads of LDS meet no bank twice (before the swizzle of gdn_swa.h:
+// 1245 us instead of 966).  256 sequences of 9 tokens behind 2052 keys: 202 us, 5.4 TB/s.
+// Tried and not kept: tiles of 32 keys (885 us instead of 835; three waves a SIMD
+// spill), raised wave priority in the products (845 to 850 instead of 839).
 #include "gdn_ops.h"
 #include "gdn_swa.h"
 
@@ -273,16 +283,20 @@ hipError_t launch_swa_table(const SwaArgs &a, bool bwd, int tokens, int32_t *met
     return hipGetLastError();
 }
 
-// Rows of a block's tile: two waves where the sequences' rows fill no more than
-// that on average.
-int swa_row_tile(const SwaArgs &a, bool) {
-    const int64_t rows = (int64_t)a.B * a.T * (a.H / a.KV);
-    return rows <= 64 * (int64_t)a.N ? 64 : 128;
+// Rows of a block's tile, 32 to a wave.  Half as many where that still leaves CUs without
+// a block.  Measured with 128 and 64 rows, forward: 3 x 333 tokens, 6 heads on 2 of 64,
+// window 100 (48 blocks) 13.0 and 11.5 us; 256 sequences of 9 tokens on 2061 keys, 16 heads
+// on 4 of 128 (1324 blocks, a third of their rows used) 202 and 232 us; of 25 tokens 245
+// and 297; 50408 packed tokens, 16 heads of 128, 860 and 1183 us.  dQ of 1237 tokens, 4 heads
+// on 2 of 32 in fp32, 20.7 and 17.5 us.
+int swa_row_tile(const SwaArgs &a) {
+    const int64_t blocks = ((int64_t)a.B * a.T / (128 / (a.H / a.KV)) + a.N) * a.KV;
+    return blocks < 256 ? 64 : 128;
 }
 
 SwaWorkspace swa_workspace_layout(const SwaArgs &a, bool bwd) {
     SwaWorkspace w{};
-    const int tokens = swa_row_tile(a, bwd) / (a.H / a.KV);
+    const int tokens = swa_row_tile(a) / (a.H / a.KV);
     const int64_t T = (int64_t)a.B * a.T, Tk = (int64_t)a.B * a.Tk, far = far_tokens(a);
     const bool table = a.B == 1;                  // a packed batch, or one sequence
     w.row_units = T / tokens + a.N;
@@ -307,7 +321,7 @@ SwaWorkspace swa_workspace_layout(const SwaArgs &a, bool bwd) {
 
 hipError_t launch_swa_fwd(const SwaArgs &a, hipStream_t st) {
     const SwaWorkspace w = swa_workspace_layout(a, false);
-    const int rows = swa_row_tile(a, false), G = a.H / a.KV;
+    const int rows = swa_row_tile(a), G = a.H / a.KV;
     SwaShape s{};
     s.T = a.T, s.Tk = a.Tk, s.H = a.H, s.KV = a.KV, s.G = G, s.window = a.window, s.sinks = a.sinks;
     s.tokens = rows / G;

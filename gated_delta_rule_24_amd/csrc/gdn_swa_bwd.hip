@@ -14,6 +14,15 @@
 // dK^T += Q^T dS.  All later tokens see the sinks: what lies past the window of the
 // first key tile is cut into parts, each a block of its own whose share of the sinks'
 // gradients goes to the workspace in fp32, and a last kernel adds the parts.
+//
+// Measured (MI355X): 4 x 4096 tokens, 16 heads on 4 of 128, window 2048, 4 sinks, bf16: query
+// side 295 us (1.05 PFLOP/s over its three products, the matrix cores busy 44%), key side
+// 610 to 650 (0.82 over its five, busy 38%).  32768 tokens, 16 heads on 8 of 64, 16 sinks,
+// fp16: 435 and 665 to 715.  Both are bound by what two waves a SIMD overlap of products,
+// exponentials and LDS reads; the key side also has two or three times as many units
+// of unequal length as blocks fit.  Key side, of the same first case: far parts of the
+// sinks without masks 965 -> 757 us, no looks for values that are not finite in masked
+// tiles 757 -> 614, reads in batches 650 -> 628 (another GPU).
 #include "gdn_ops.h"
 #include "gdn_swa.h"
 
@@ -195,10 +204,12 @@ __device__ __forceinline__ int64_t far_first(int64_t q0, int n, int far) { retur
 // The two accumulators and the operands K and V of a wave are 3 D 32-bit registers
 // in 16 bits, 4 D in fp32.  Where that leaves too few of 256, dV and dK are made by
 // different blocks, the second with S once more (5 products instead of 4).
-// Measured, 4 x 4096 tokens, 16 heads on 4 of 128, window 2048, in bf16: one block for
-// both 3715 us with two waves a SIMD (registers spill) and 1195 with one.
+// Measured, 4 x 4096 tokens, 16 heads on 4 of 128, window 2048, in bf16: different blocks
+// 1118 us, one block for both 3715 with two waves a SIMD (registers spill) and 1195 with
+// one; since then the split form has come to 610 to 650.  4096 tokens, 16 heads on 8 of 64,
+// in fp32: 817 us split, 684 not.
 template <typename T, int D>
-constexpr bool kSplitKeySide = Rows<T, D>::RB >= 256;
+constexpr bool kSplitKeySide = D == 128;
 
 template <typename T, int D>
 __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_kernel(
@@ -469,7 +480,7 @@ __global__ __launch_bounds__(1024) void swa_sinks_kernel(SwaShape sh, int far, i
 
 hipError_t launch_swa_bwd(const SwaArgs &a, hipStream_t st) {
     const SwaWorkspace w = swa_workspace_layout(a, true);
-    const int rows = swa_row_tile(a, true), G = a.H / a.KV, far = swa_far_chunk(a.window);
+    const int rows = swa_row_tile(a), G = a.H / a.KV, far = swa_far_chunk(a.window);
     char *ws = static_cast<char *>(a.workspace);
     float *dsum = reinterpret_cast<float *>(ws + w.off_dsum), *share = reinterpret_cast<float *>(ws + w.off_far);
     SwaShape s{};

@@ -11,6 +11,13 @@
 // query's type exactly; their scales multiply the scores and the probabilities.
 // The waves join in LDS; where a sequence's rows are split over blocks, these leave
 // (maximum, sum, O) in the workspace, and a second kernel joins them.
+//
+// Measured (MI355X, a copy 5.35 TB/s), 16 heads on 4 of 128: 256 sequences of 1029 to 2052
+// rows in 8 bits 99 to 103 us (515 MB, 5.1 TB/s), in bf16 181 (997 MB, 5.5); of up to 8192
+// rows in 8 bits 375 (2.05 GB, 5.5).  Two sequences of up to 65536 rows, fp16, 43 us and
+// 5 for the join (268 MB).  What is left are the first loads, behind those of slot and
+// length, and the last blocks.  128 registers, so that four blocks fit a CU: with 160
+// the bf16 case takes 205 us.
 #include "gdn_cache.h"
 #include "gdn_swa.h"
 
@@ -401,7 +408,10 @@ __global__ __launch_bounds__(1024) void swa_step_join_kernel(StepShape s, const 
     o[((int64_t)n * s.H + hk * s.G + g) * D + d] = round_to<T>(z == 0.f ? 0.f : x / z);
 }
 
-// Enough blocks for the GPU, each with a tile for every wave at least.
+// Enough blocks for the GPU, each with a tile for every wave at least.  Measured for
+// 1024, 2048 and 4096 blocks, kernel and join: 256 sequences above 113, 142 and 157 us
+// (no join with 1024), 64 sequences 42, 51 and 61, 16 sequences 24 each, two of 65536 rows
+// 64, 68 and 73.
 int swa_step_splits(const SwaStepArgs &a) {
     const int64_t rows = (int64_t)a.c.window + a.c.sinks, units = std::max<int64_t>((int64_t)a.c.N * a.c.KV, 1);
     const int64_t most = std::max<int64_t>(rows / (kStepWaves * kTile), 1);
