@@ -30,6 +30,10 @@ namespace gdn {
 
 constexpr int kKeys = 64;            // keys of a staged tile
 constexpr float kSlack = 8.f;        // log2: how far scores may pass the maximum that is subtracted
+// Probabilities are taken times 2^kLift: in fp16 the small ones, which many keys may
+// share, would be subnormal or 0.  Their sum has the same factor.
+template <typename T>
+constexpr float kLift = std::is_same_v<T, _Float16> ? 15.f - kSlack : 0.f;
 
 template <typename T, int D, int NW>
 __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_fwd_kernel(SwaShape sh, const T *__restrict__ q,
@@ -151,7 +155,7 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
 #pragma unroll
                     for (int i = 0; i < 16; ++i) acc[dt][i] *= f;
             }
-            const float base = m == -__builtin_inff() ? 0.f : m;
+            const float base = (m == -__builtin_inff() ? 0.f : m) - kLift<T>;
 #pragma unroll
             for (int n = 0; n < NSUB; ++n)
 #pragma unroll
@@ -192,7 +196,7 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
     sum = half_sum(sum);
     store_column<T, D>(o + at * D, acc, sum == 0.f ? 0.f : 1.f / sum, on);
     if (lse && on && h == 0)
-        lse[at] = sum == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+        lse[at] = sum == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(sum) - kLift<T>) * 0.6931471805599453f;
 }
 
 // ---- packed batches: the table of units ---------------------------------------------

@@ -34,6 +34,11 @@ struct StepShape {
     float c;                          // scale log2(e)
 };
 
+// Probabilities are taken times 2^kLift: in fp16 the small ones, which many rows may
+// share, would be subnormal or 0.  Their sum has the same factor.
+template <typename T>
+constexpr float kLift = std::is_same_v<T, _Float16> ? 14.f : 0.f;
+
 // Two neighbouring e4m3 values of a word as two 16-bit values, exact.
 template <typename T>
 __device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
@@ -153,7 +158,7 @@ __global__ __launch_bounds__(64 * kStepWaves, (Rows<T, D>::RB > 256 ? 2 : 4)) vo
     float4_t acc[ND];
 #pragma unroll
     for (int dt = 0; dt < ND; ++dt) acc[dt] = float4_t{0.f, 0.f, 0.f, 0.f};
-    float top = -__builtin_inff(), sum = 0.f;
+    float top = -__builtin_inff(), sum = 0.f, unit = 0.f;   // unit: fp16 on 8 bits, largest scale of V yet
     char *vt = s_v[wave];
     // 16 bytes (8) at byte b of row r of k or v, from LDS where it is the new one
     auto renew = [&](auto &x, int r, int which, int b) {
@@ -275,6 +280,28 @@ __global__ __launch_bounds__(64 * kStepWaves, (Rows<T, D>::RB > 256 ? 2 : 4)) vo
 #pragma unroll
                 for (int i = 0; i < 4; ++i) S[a][i] *= x[i], sc[a][i] = y[i];
             }
+            // fp16 does not hold every scale: V counts in units of the largest so far, a
+            // power of two whose inverse is normal
+            if constexpr (std::is_same_v<T, _Float16>) {
+                float most = unit;
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) most = fmaxf(most, sc[a][i]);
+                most = fmaxf(most, __shfl_xor(most, 16, 64));
+                most = fmaxf(most, __shfl_xor(most, 32, 64));
+                most = __uint_as_float(__float_as_uint(fminf(most, 0x1p126f)) & 0x7F800000u);
+                const float inv = e4m3_inverse(most);
+                if (__any(most > unit)) {
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt) acc[dt] *= unit * inv;
+                }
+                unit = most;
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[a][i] *= inv;
+            }
         }
         asm volatile("" ::: "memory");
         // lane (m, hq): head m, rows 16 a + 4 hq + i
@@ -295,7 +322,7 @@ __global__ __launch_bounds__(64 * kStepWaves, (Rows<T, D>::RB > 256 ? 2 : 4)) vo
 #pragma unroll
             for (int dt = 0; dt < ND; ++dt) acc[dt] *= f;
         }
-        const float base = top == -__builtin_inff() ? 0.f : top;
+        const float base = (top == -__builtin_inff() ? 0.f : top) - kLift<T>;
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
@@ -333,6 +360,10 @@ __global__ __launch_bounds__(64 * kStepWaves, (Rows<T, D>::RB > 256 ? 2 : 4)) vo
         }
         asm volatile("" ::: "memory");            // the next tile's V is written behind these reads
     }
+
+    if constexpr (Q8 && std::is_same_v<T, _Float16>)
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) acc[dt] *= unit;
 
     // the waves join
     sum += __shfl_xor(sum, 16, 64);
