@@ -291,6 +291,12 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
     };
     const int srow = l, stoken = srow / sh.G;      // waves 0 and 1 bring lse and D of the tile's rows
     float stat = 0.f;
+    // dV takes fp16 probabilities times 2^15: the small ones, which many rows may share, would
+    // be subnormal or 0.  A block that makes dK too lowers dP and D instead of their product:
+    // the difference is then one fma (a product more took 32768 tokens from 1235 to 1271 us)
+    constexpr bool LIFT = std::is_same_v<T, _Float16>;
+    const float lift = LIFT && (!kSplitKeySide<T, D> || u.role == 0) ? 15.f : 0.f;
+    constexpr float UNLIFT = LIFT ? 0x1p-15f : 1.f, lower = kSplitKeySide<T, D> ? 1.f : UNLIFT;
     auto load = [&](int it) {
         const int t0 = first_token(it), n = min(tb - t0, sh.tokens);
         const int64_t first = (u.q0 + t0) * sh.H + u.hk * sh.G, b = first * RB;
@@ -301,7 +307,7 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
         if (wave < 2) {
             const bool there = srow < rows && stoken < n;
             const int64_t a = first + (there ? (int64_t)stoken * sh.H + srow % sh.G : 0);
-            stat = wave == 0 ? log2_lse(lse[a]) : dsum[a];
+            stat = wave == 0 ? log2_lse(lse[a]) - lift : dsum[a] * lower;
             if (!there) stat = wave == 0 ? __builtin_inff() : 0.f;
         }
     };
@@ -373,7 +379,8 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = 4 * (a & 3) + e;
-                    const float y = S[a >> 2][i] * (P[a >> 2][i] - dd[e]);
+                    const float less = LIFT && MAKE_V ? fmaf(P[a >> 2][i], UNLIFT, -dd[e]) : P[a >> 2][i] - dd[e];
+                    const float y = S[a >> 2][i] * less;
                     P[a >> 2][i] = !MASK || (seen >> i & 1u) ? y : 0.f;
                 }
             }
@@ -418,19 +425,20 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
         bool bad = false;
         if constexpr (MAKE_V) bad |= any_not_finite(av);
         if constexpr (MAKE_K) bad |= any_not_finite(ak);
+        bad &= part < 0 || key < sh.sinks;        // other keys' sums are dropped
         if (__syncthreads_or(busy && bad)) walk(std::true_type{}, make_v, make_k, av, ak);
         if (!busy) return;
         const bool shared = fp.parts > 0 && jt == 0 && key < sh.sinks;   // the parts are added later
         if (part < 0) {
             const bool on = key < u.Lk && !shared;
             if (MAKE_K) store_column<T, D>(dk + at * D, ak, sh.scale, on);
-            if (MAKE_V) store_column<T, D>(dv + at * D, av, 1.f, on);
+            if (MAKE_V) store_column<T, D>(dv + at * D, av, UNLIFT, on);
         }
         if (fp.parts > 0 && k0 < sh.sinks && jt == 0) {
             const int64_t slot = far_first(u.q0, u.n, far) + (part >= 0 ? part + 1 : 0);
             float *to = share + ((slot * sh.KV + u.hk) * 2 * sh.sinks + key) * (int64_t)D;
             if (MAKE_K) store_column<float, D>(to, ak, sh.scale, shared && key < u.Lk);
-            if (MAKE_V) store_column<float, D>(to + (int64_t)sh.sinks * D, av, 1.f, shared && key < u.Lk);
+            if (MAKE_V) store_column<float, D>(to + (int64_t)sh.sinks * D, av, UNLIFT, shared && key < u.Lk);
         }
     };
     if constexpr (kSplitKeySide<T, D>) {

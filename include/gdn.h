@@ -606,9 +606,9 @@ gdn_status gdn_state_move(int32_t layers, int32_t slots, int64_t page_bytes, int
  *   dtype      of q, k, v, o and their gradients.  Products of 16-bit types run
  *              on the 16-bit matrix cores and add in fp32; the probabilities
  *              (and, backward, the scores' gradients, which FP16 holds below
- *              65504) are rounded to dtype as operands, forward with a power of
- *              two that keeps FP16's small ones.  Scores, maxima, sums and lse
- *              are fp32.
+ *              65504) are rounded to dtype as operands, the probabilities of o
+ *              and dV with a power of two that keeps FP16's small ones.
+ *              Scores, maxima, sums and lse are fp32.
  *   scale      finite and > 0
  *   flags      0
  * A sequence's queries are its last: the query i stands at position

@@ -69,3 +69,25 @@ def test_values_of_any_size_in_turn(dtype):
     o = gdn.swa_step(c, q, new, new, torch.full((1,), n - 1, dtype=torch.int32, device="cuda"), 0, s)
     want = (size[:-1].sum() + 1) / n
     within(o, np.full(o.shape, want), bound(n, dtype, want), dtype, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sinks", [0, 40])
+def test_gradient_of_values(dtype, d, sinks):
+    """dV of the small keys, p dO: one product of a rounded probability.  512 queries, the last of them with a gradient;
+    with sinks the keys before the window are seen too."""
+    n, gap, size = 511, 14, 1024.0
+    (q, k, v), _ = case(n, d, gap, 512.0, dtype)
+    q = q.expand(1, n + 1, 1, d).contiguous()
+    do = torch.zeros_like(q)
+    do[:, -1] = size
+    window = 100 if sinks else n + 1
+    o, lse = gdn.swa_fwd(q, k, v, window, sinks, scale=1.0)
+    dv = gdn.swa_bwd(do, q, k, v, o, lse, window, sinks, scale=1.0)[2][0, :, 0]
+    seen = [j for j in range(1, n + 1) if n - j < window or j < sinks]
+    w = np.exp(-float(gap))
+    want = size * w / (1 + len(seen) * w)
+    within(dv[seen], np.full((len(seen), d), want), bound(n, dtype, want), dtype, f"{dtype} d{d} sinks {sinks}")
+    hidden = [j for j in range(1, n + 1) if j not in seen]
+    assert not dv[hidden].any()
