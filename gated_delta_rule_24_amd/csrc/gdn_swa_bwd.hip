@@ -38,6 +38,21 @@ __device__ __forceinline__ float log2_lse(float lse) {
     return lse == -__builtin_inff() ? __builtin_inff() : lse * 1.4426950408889634f;
 }
 
+// fp16 holds dS only from 2^-24 to 65504, and many small ones may make up dQ and dK (of
+// 32768 keys and 2^-10 of d_o, dQ was 3.7% off).  It is taken times a power of two per row of
+// dQ or dK, at first 2^64, lowered with the sums so far where an element comes near the
+// end of fp16's range; the store takes it out again.  Lowered to [2^12, 2^13), so that
+// the next larger ones seldom ask for it again: elements down to 2^-26 of the largest are
+// rounded once.  Measured, 32768 tokens, 16 heads on 8 of 64, query and key side:
+// 447 and 699 us with dS as it is, 468 and 720 so; 4 x 4096 tokens, 16 heads on 4 of 128, 320
+// and 652, 335 and 681.
+constexpr int kLiftDs = 64;
+constexpr float kMostDs = 60000.f;
+__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// By how many powers an element of size t has to be lowered.
+__device__ __forceinline__ int lower_ds(float t) { return t < kMostDs ? 0 : (int)(__float_as_uint(t) >> 23) - 139; }
+__device__ __forceinline__ float inverse_power(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
+
 template <typename T, int D, int NW>
 __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dq_kernel(
     SwaShape sh, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v, const T *__restrict__ o,
@@ -82,6 +97,8 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
     if (on && h == 0) dsum[at] = dd;
     float lse2 = log2_lse(lse[at]);
     arrived(lse2);
+    constexpr bool LIFT = std::is_same_v<T, _Float16>;
+    float unit, base;                              // of dS; lse2 less its log2
 #pragma unroll
     for (int s = 0; s < R::NS; ++s) arrived(qf[s]), arrived(gf[s]);
 
@@ -124,6 +141,7 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
         for (int dt = 0; dt < R::ND; ++dt)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[dt][i] = 0.f;
+        unit = LIFT ? power_of_2(kLiftDs) : 1.f, base = LIFT ? lse2 - kLiftDs : lse2;
         // One staged tile after the other, [x0, x1) of their order.
         auto each = [&](int x0, int x1, auto body) {
             for (int x = x0; x < x1; ++x) {
@@ -147,7 +165,7 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
             uint32_t seen = 0;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float x = __builtin_amdgcn_exp2f(fmaf(S[i], sh.c, -lse2)) * (P[i] - dd);
+                const float x = __builtin_amdgcn_exp2f(fmaf(S[i], sh.c, -base)) * (P[i] - dd);
                 if constexpr (MASK) {
                     const int j = j0 + r0 + 4 * (ln.l >> 5) + 8 * (i >> 2) + (i & 3);
                     const bool see = j <= pos && j < jend && (j > pos - W || j < sh.sinks);
@@ -155,6 +173,20 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
                     seen |= (uint32_t)see << i;
                 } else {
                     S[i] = x;
+                }
+            }
+            if constexpr (LIFT) {
+                float t = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) t = fmaxf(t, fabsf(S[i]));
+                if (__any(t >= kMostDs)) {
+                    const int less = lower_ds(half_max(t));
+                    const float f = power_of_2(-less);
+                    unit *= f;
+                    base += less;
+                    S *= f;
+#pragma unroll
+                    for (int dt = 0; dt < R::ND; ++dt) acc[dt] *= f;
                 }
             }
             if constexpr (CAREFUL) {
@@ -183,7 +215,7 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
     };
     walk(std::false_type{});
     if (__syncthreads_or(busy && any_not_finite(acc))) walk(std::true_type{});
-    if (busy) store_column<T, D>(dq + at * D, acc, sh.scale, on);
+    if (busy) store_column<T, D>(dq + at * D, acc, LIFT ? sh.scale * inverse_power(unit) : sh.scale, on);
 }
 
 // Where the far parts of a sequence begin: tokens from `reach` on are past the
@@ -292,11 +324,10 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
     const int srow = l, stoken = srow / sh.G;      // waves 0 and 1 bring lse and D of the tile's rows
     float stat = 0.f;
     // dV takes fp16 probabilities times 2^15: the small ones, which many rows may share, would
-    // be subnormal or 0.  A block that makes dK too lowers dP and D instead of their product:
-    // the difference is then one fma (a product more took 32768 tokens from 1235 to 1271 us)
+    // be subnormal or 0
     constexpr bool LIFT = std::is_same_v<T, _Float16>;
-    const float lift = LIFT && (!kSplitKeySide<T, D> || u.role == 0) ? 15.f : 0.f;
-    constexpr float UNLIFT = LIFT ? 0x1p-15f : 1.f, lower = kSplitKeySide<T, D> ? 1.f : UNLIFT;
+    const int lift = LIFT && (!kSplitKeySide<T, D> || u.role == 0) ? 15 : 0;
+    constexpr float UNLIFT = LIFT ? 0x1p-15f : 1.f;
     auto load = [&](int it) {
         const int t0 = first_token(it), n = min(tb - t0, sh.tokens);
         const int64_t first = (u.q0 + t0) * sh.H + u.hk * sh.G, b = first * RB;
@@ -307,7 +338,7 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
         if (wave < 2) {
             const bool there = srow < rows && stoken < n;
             const int64_t a = first + (there ? (int64_t)stoken * sh.H + srow % sh.G : 0);
-            stat = wave == 0 ? log2_lse(lse[a]) - lift : dsum[a] * lower;
+            stat = wave == 0 ? log2_lse(lse[a]) - lift : LIFT ? -dsum[a] : dsum[a];
             if (!there) stat = wave == 0 ? __builtin_inff() : 0.f;
         }
     };
@@ -316,6 +347,7 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
     };
 
     const typename R::Lane lane;
+    float unit = 1.f;                              // of dS
     // All tiles of rows, for dV, dK or both.
     auto walk = [&](auto careful, auto make_v, auto make_k, f32x16_t (&av)[R::ND], f32x16_t (&ak)[R::ND]) {
         constexpr bool CAREFUL = decltype(careful)::value, MAKE_V = decltype(make_v)::value,
@@ -327,6 +359,8 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
                 if (MAKE_K) ak[dt][i] = 0.f;
                 if (MAKE_V) av[dt][i] = 0.f;
             }
+        // what other lanes of a far part make is dropped
+        if constexpr (LIFT) unit = part < 0 || key < sh.sinks ? power_of_2(kLiftDs) : 0.f;
         auto process = [&](auto subs, auto masked, int x, int t0, int r0) {
             const char *qt = smem + (x & 1) * 2 * TILE, *gt = qt + TILE;
             const float *st = stats + (x & 1) * 2 * kRows;
@@ -372,16 +406,39 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
                 }
             }
             if constexpr (!MAKE_K) return;
+            if constexpr (LIFT) {                  // dP - D at once, for the product that the power of two costs
+#pragma unroll
+                for (int a = 0; a < 4 * NSUB; ++a) {
+                    const float4_t dd = *reinterpret_cast<const float4_t *>(sr + kRows + 8 * a);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) P[a >> 2][4 * (a & 3) + e] = dd[e];
+                }
+            }
             R::dot(P, gt, ln, r0, vf);
 #pragma unroll
             for (int a = 0; a < 4 * NSUB; ++a) {
-                const float4_t dd = *reinterpret_cast<const float4_t *>(sr + kRows + 8 * a);
+                float4_t dd{};
+                if constexpr (!LIFT) dd = *reinterpret_cast<const float4_t *>(sr + kRows + 8 * a);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = 4 * (a & 3) + e;
-                    const float less = LIFT && MAKE_V ? fmaf(P[a >> 2][i], UNLIFT, -dd[e]) : P[a >> 2][i] - dd[e];
-                    const float y = S[a >> 2][i] * less;
+                    const float y = LIFT ? S[a >> 2][i] * unit * P[a >> 2][i] : S[a >> 2][i] * (P[a >> 2][i] - dd[e]);
                     P[a >> 2][i] = !MASK || (seen >> i & 1u) ? y : 0.f;
+                }
+            }
+            if constexpr (LIFT) {
+                float t = 0.f;
+#pragma unroll
+                for (int n = 0; n < NSUB; ++n)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) t = fmaxf(t, fabsf(P[n][i]));
+                if (__any(t >= kMostDs)) {
+                    const float f = power_of_2(-lower_ds(half_max(t)));
+                    unit *= f;
+#pragma unroll
+                    for (int n = 0; n < NSUB; ++n) P[n] *= f;
+#pragma unroll
+                    for (int dt = 0; dt < R::ND; ++dt) ak[dt] *= f;
                 }
             }
             if (CAREFUL && bad) {
@@ -428,16 +485,17 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
         bad &= part < 0 || key < sh.sinks;        // other keys' sums are dropped
         if (__syncthreads_or(busy && bad)) walk(std::true_type{}, make_v, make_k, av, ak);
         if (!busy) return;
+        const float scale = LIFT ? sh.scale * inverse_power(unit * power_of_2(lift)) : sh.scale;
         const bool shared = fp.parts > 0 && jt == 0 && key < sh.sinks;   // the parts are added later
         if (part < 0) {
             const bool on = key < u.Lk && !shared;
-            if (MAKE_K) store_column<T, D>(dk + at * D, ak, sh.scale, on);
+            if (MAKE_K) store_column<T, D>(dk + at * D, ak, scale, on);
             if (MAKE_V) store_column<T, D>(dv + at * D, av, UNLIFT, on);
         }
         if (fp.parts > 0 && k0 < sh.sinks && jt == 0) {
             const int64_t slot = far_first(u.q0, u.n, far) + (part >= 0 ? part + 1 : 0);
             float *to = share + ((slot * sh.KV + u.hk) * 2 * sh.sinks + key) * (int64_t)D;
-            if (MAKE_K) store_column<float, D>(to, ak, sh.scale, shared && key < u.Lk);
+            if (MAKE_K) store_column<float, D>(to, ak, scale, shared && key < u.Lk);
             if (MAKE_V) store_column<float, D>(to + (int64_t)sh.sinks * D, av, UNLIFT, shared && key < u.Lk);
         }
     };

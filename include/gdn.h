@@ -605,11 +605,11 @@ gdn_status gdn_state_move(int32_t layers, int32_t slots, int64_t page_bytes, int
  *   sinks      S: 0..128
  *   dtype      of q, k, v, o and their gradients.  Products of 16-bit types run
  *              on the 16-bit matrix cores and add in fp32; the probabilities
- *              (and, backward, the scores' gradients, which FP16 holds below
- *              65504) are rounded to dtype as operands, the probabilities of o
- *              and dV with a power of two that keeps FP16's small ones: down to
- *              2^-28 of a query's largest they are rounded once, what is less is
- *              off by at most 2^-39 of the largest.
+ *              (and, backward, the scores' gradients) are rounded to dtype as
+ *              operands, in FP16 with a power of two that keeps the small ones:
+ *              probabilities down to 2^-28 of a query's largest, and gradients
+ *              down to 2^-26 of the largest of a row of dQ or dK, are rounded
+ *              once, what is less is off by at most 2^-39 (2^-37) of the largest.
  *              Scores, maxima, sums and lse are fp32.
  *   scale      finite and > 0
  *   flags      0

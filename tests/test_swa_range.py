@@ -1,9 +1,9 @@
 """Windowed attention over the range of its numbers: probabilities and gradients of scores far below the largest of
 their row, scores and scales of any size.  Closed forms in 64 bits.
 
-FP16 holds a power of two down to 2^-14 with all its bits.  Operands are taken times a power of two that puts the
-largest of a row at 2^14 or above (below 2^16), so what is down to 2^-28 of the largest is rounded once (HALF), and what is
-less by at most 2^-25 of that unit, 2^-39 of the largest.
+FP16 holds numbers down to 2^-14 with all their bits.  Operands are taken times a power of two that puts the largest
+probability of a row at 2^14 or above, the largest gradient of a score at 2^12 or above (below 2^16), so what is down to
+2^-28 (2^-26) of the largest is rounded once (HALF), and what is less is off by 2^-25 at most: 2^-39 (2^-37) of it.
 """
 import numpy as np
 import pytest
@@ -11,7 +11,9 @@ import torch
 
 import gated_delta_rule_24_amd as gdn
 
-from .op_util import HALF, U, within
+from .op_util import HALF, TINY, U, host, within
+from .swa_terms import gradients
+from .test_swa import inputs
 from .test_swa_small_weights import bound, case
 
 pytestmark = pytest.mark.gpu
@@ -59,3 +61,71 @@ def test_forward_maxima_that_move(dtype, order):
     want = (w * value).sum() / w.sum()
     within(o, np.full(o.shape, want), ((n + 72 + n / 16) * U + 2 * HALF[dtype]) * want, dtype, f"{dtype} {order}")
     assert abs(lse.item() - (s.max() + np.log(w.sum()))) <= (n + 72) * U + 8 * U * 10
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("sinks", [0, 40])
+@pytest.mark.parametrize("size", [2.0 ** -10, 2.0 ** -4, 2.0 ** 10])
+def test_gradient_of_small_scores(dtype, d, sinks, size):
+    """dQ and dK where d_o reaches many small probabilities alone.  One query of the last has a gradient, in column 0,
+    where the small keys' values are 1 and the large key's is 0:  dS_j = p_j (size - D),  dS_0 = -p_0 D,  D = size o.
+    Column 2 of the small keys makes dQ, column 1 of the query dK; neither is in a score.  The terms have one sign: one rounding
+    of dS, and one of o in D: bound()."""
+    n, gap, big = 511, 14.0, 2.0 ** 14
+    (q, k, v), _ = case(n, d, gap, 1.0, dtype)
+    q = q.expand(1, n + 1, 1, d).contiguous()
+    q[..., 1], k[:, 1:, :, 2], v[..., 1:] = big, big, 0.0
+    do = torch.zeros_like(q)
+    do[:, -1, :, 0] = size
+    window = 100 if sinks else n + 1
+    o, lse = gdn.swa_fwd(q, k, v, window, sinks, scale=1.0)
+    dq, dk, _ = gdn.swa_bwd(do, q, k, v, o, lse, window, sinks, scale=1.0)
+    seen = [j for j in range(1, n + 1) if n - j < window or j < sinks]
+    large = 1.0 if sinks or window > n else 0.0                  # whether the last query sees key 0
+    w = np.exp(-gap)
+    m = len(seen)
+    total = large + m * w
+    D = size * m * w / total
+    ds = w / total * (size - D)
+    label = f"{dtype} d{d} sinks {sinks} size {size}"
+    within(dq[0, -1, 0, 2:3], np.array([m * ds * big]), bound(n, dtype, m * ds * big), dtype, f"{label} dq")
+    within(dk[0, seen, 0, 1], np.full(m, ds * big), bound(n, dtype, ds * big), dtype, f"{label} dk")
+    within(dk[0, :1, 0, 1], np.array([-D * large / total * big]), bound(n, dtype, D * big), dtype, f"{label} dk of the large")
+    hidden = [j for j in range(1, n + 1) if j not in seen]
+    assert not dk[0, hidden].any() and not dq[0, :-1].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_gradient_of_large_scores(dtype, d):
+    """dS past 65504, with results that the type holds: all exact."""
+    q, k, v = (torch.zeros(1, 2, 1, d, device="cuda", dtype=x.dtype) for x in case(1, d, 1, 1.0, dtype)[0])
+    q[..., 1], k[0, 0, 0, 2], k[0, 1, 0, 2], v[0, 0, 0, 0], v[0, 1, 0, 0] = 2.0 ** -6, 2.0 ** -6, -2.0 ** -6, 4.0, -4.0
+    do = torch.zeros_like(q)
+    do[0, 1, 0, 0] = 2.0 ** 15
+    o, lse = gdn.swa_fwd(q, k, v, 2, scale=1.0)
+    dq, dk, dv = gdn.swa_bwd(do, q, k, v, o, lse, 2, scale=1.0)
+    # p = 1/2 twice up to the rounding of lse: 4 U
+    for got, want in ((dq[0, 1, 0, 2], 2.0 ** 11), (dk[0, 0, 0, 1], 2.0 ** 10), (dk[0, 1, 0, 1], -2.0 ** 10),
+                      (dv[0, 0, 0, 0], 2.0 ** 14), (dv[0, 1, 0, 0], 2.0 ** 14)):
+        within(got, np.array(want), 8 * U * abs(want), dtype, f"{dtype} d{d}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d,keys,size", [(128, 32768, 2.0 ** -6), (128, 32768, 2.0 ** -10), (64, 32768, 2.0 ** -10),
+                                         (32, 8192, 2.0 ** -12), (64, 8192, 2.0 ** 6)])
+def test_gradient_over_many_keys(dtype, d, keys, size):
+    """Some queries that see all of many keys, and gradients of the size that training meets in fp16.  Element by element,
+    and by root mean square: two roundings, of dS and of the result, at most HALF / sqrt 3 each, and the fp16 result's
+    subnormal step."""
+    T, H = 48, 2
+    t, x = inputs(d + keys, 1, T, keys, H, 1, d, dtype)
+    do = (torch.randn(1, T, H, d, generator=torch.Generator("cuda").manual_seed(7), device="cuda") * size).to(t[0].dtype)
+    o, lse = gdn.swa_fwd(*t, keys)
+    got = gdn.swa_bwd(do, *t, o, lse, keys)
+    want = gradients(host(do), *x, host(o), host(lse), keys, h=HALF[dtype])
+    for name, g, (w, room) in zip(("dq", "dk", "dv"), got, want):
+        within(g, w, room, dtype, f"{dtype} d{d} {keys} keys {size} {name}")
+        off, rms = (np.sqrt(np.mean(y ** 2)) for y in (host(g) - w, w))
+        assert off <= HALF[dtype] * rms + TINY[dtype] / 2, (name, off / rms)
