@@ -38,6 +38,7 @@ struct StepShape {
 // share, would be subnormal or 0.  Their sum has the same factor.
 template <typename T>
 constexpr float kLift = std::is_same_v<T, _Float16> ? 14.f : 0.f;
+constexpr float kLiftUnits = 0x1p14f, kLeastUnit = 0x1p-100f;
 
 // Two neighbouring e4m3 values of a word as two 16-bit values, exact.
 template <typename T>
@@ -70,6 +71,11 @@ __global__ __launch_bounds__(64 * kStepWaves, (Rows<T, D>::RB > 256 ? 2 : 4)) vo
     const int32_t *__restrict__ lengths, const int32_t *__restrict__ slots, T *__restrict__ o,
     float *__restrict__ parts, int32_t *__restrict__ status) {
     constexpr bool F32 = std::is_same_v<T, float>;
+    // fp16 on 8 bits holds neither every scale nor every product of one with a
+    // probability: V's weights (probability times scale) count in units of the largest
+    // so far, a power of two, of which they are less than two, taken times kLiftUnits
+    constexpr bool UNITS = Q8 && std::is_same_v<T, _Float16>;
+    constexpr float LIFT = UNITS ? 0.f : kLift<T>;
     constexpr int NT = 64 * kStepWaves, RB = D * (int)sizeof(T);
     constexpr int RC = Q8 ? D : RB;               // bytes of a cache row
     constexpr int NS = RB / 64, ND = D / 16;      // steps of the product over D, tiles along D
@@ -158,7 +164,7 @@ __global__ __launch_bounds__(64 * kStepWaves, (Rows<T, D>::RB > 256 ? 2 : 4)) vo
     float4_t acc[ND];
 #pragma unroll
     for (int dt = 0; dt < ND; ++dt) acc[dt] = float4_t{0.f, 0.f, 0.f, 0.f};
-    float top = -__builtin_inff(), sum = 0.f, unit = 0.f;   // unit: fp16 on 8 bits, largest scale of V yet
+    float top = -__builtin_inff(), sum = 0.f, unit = kLeastUnit;
     char *vt = s_v[wave];
     // 16 bytes (8) at byte b of row r of k or v, from LDS where it is the new one
     auto renew = [&](auto &x, int r, int which, int b) {
@@ -280,28 +286,6 @@ __global__ __launch_bounds__(64 * kStepWaves, (Rows<T, D>::RB > 256 ? 2 : 4)) vo
 #pragma unroll
                 for (int i = 0; i < 4; ++i) S[a][i] *= x[i], sc[a][i] = y[i];
             }
-            // fp16 does not hold every scale: V counts in units of the largest so far, a
-            // power of two whose inverse is normal
-            if constexpr (std::is_same_v<T, _Float16>) {
-                float most = unit;
-#pragma unroll
-                for (int a = 0; a < 2; ++a)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) most = fmaxf(most, sc[a][i]);
-                most = fmaxf(most, __shfl_xor(most, 16, 64));
-                most = fmaxf(most, __shfl_xor(most, 32, 64));
-                most = __uint_as_float(__float_as_uint(fminf(most, 0x1p126f)) & 0x7F800000u);
-                const float inv = e4m3_inverse(most);
-                if (__any(most > unit)) {
-#pragma unroll
-                    for (int dt = 0; dt < ND; ++dt) acc[dt] *= unit * inv;
-                }
-                unit = most;
-#pragma unroll
-                for (int a = 0; a < 2; ++a)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[a][i] *= inv;
-            }
         }
         asm volatile("" ::: "memory");
         // lane (m, hq): head m, rows 16 a + 4 hq + i
@@ -319,10 +303,14 @@ __global__ __launch_bounds__(64 * kStepWaves, (Rows<T, D>::RB > 256 ? 2 : 4)) vo
             const float up = fmaxf(top, big), f = top == up ? 1.f : __builtin_amdgcn_exp2f(top - up);
             top = up;
             sum *= f;
+            if constexpr (UNITS) {
+                unit *= f;
+            } else {
 #pragma unroll
-            for (int dt = 0; dt < ND; ++dt) acc[dt] *= f;
+                for (int dt = 0; dt < ND; ++dt) acc[dt] *= f;
+            }
         }
-        const float base = (top == -__builtin_inff() ? 0.f : top) - kLift<T>;
+        const float base = (top == -__builtin_inff() ? 0.f : top) - LIFT;
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
@@ -333,6 +321,26 @@ __global__ __launch_bounds__(64 * kStepWaves, (Rows<T, D>::RB > 256 ? 2 : 4)) vo
                 if constexpr (Q8)
                     S[a][i] = t0 + 16 * a + 4 * hq + i < r1 ? S[a][i] * sc[a][i] : 0.f;
             }
+        if constexpr (UNITS) {
+            float most = fmaxf(unit, kLeastUnit);
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) most = fmaxf(most, S[a][i]);
+            most = fmaxf(most, __shfl_xor(most, 16, 64));
+            most = fmaxf(most, __shfl_xor(most, 32, 64));
+            most = __uint_as_float(__float_as_uint(most) & 0x7F800000u);
+            const float inv = e4m3_inverse(most);
+            if (__any(most != unit)) {
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) acc[dt] *= unit * inv;
+            }
+            unit = most;
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[a][i] *= inv * kLiftUnits;
+        }
         if constexpr (F32) {
 #pragma unroll
             for (int a = 0; a < 2; ++a)
@@ -361,9 +369,9 @@ __global__ __launch_bounds__(64 * kStepWaves, (Rows<T, D>::RB > 256 ? 2 : 4)) vo
         asm volatile("" ::: "memory");            // the next tile's V is written behind these reads
     }
 
-    if constexpr (Q8 && std::is_same_v<T, _Float16>)
+    if constexpr (UNITS)
 #pragma unroll
-        for (int dt = 0; dt < ND; ++dt) acc[dt] *= unit;
+        for (int dt = 0; dt < ND; ++dt) acc[dt] *= unit / kLiftUnits;
 
     // the waves join
     sum += __shfl_xor(sum, 16, 64);

@@ -11,7 +11,7 @@ import torch
 
 import gated_delta_rule_24_amd as gdn
 
-from .op_util import HALF, TINY, U, host, within
+from .op_util import DT, HALF, TINY, U, host, within
 from .swa_terms import gradients
 from .test_swa import inputs
 from .test_swa_small_weights import bound, case
@@ -129,3 +129,40 @@ def test_gradient_over_many_keys(dtype, d, keys, size):
         within(g, w, room, dtype, f"{dtype} d{d} {keys} keys {size} {name}")
         off, rms = (np.sqrt(np.mean(y ** 2)) for y in (host(g) - w, w))
         assert off <= HALF[dtype] * rms + TINY[dtype] / 2, (name, off / rms)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("at", [0, 40, 690])
+def test_step_beside_an_outlying_scale(dtype, d, at):
+    """8-bit rows whose scale is 2^-14, and one of scale 2^20 that hardly counts, in a column of its own, first, among
+    them or last.  The weights (probability times scale) have their own largest, e^-40 2^20 or 2^-14: no row's rounding is
+    more than HALF of what it adds, and the terms have one sign."""
+    if dtype == "fp32" and d == 256:
+        pytest.skip("fp32 is built to 128")
+    n = 700
+    g = np.random.default_rng(at)
+    value = g.integers(8, 16, n) / 8.0                           # e4m3 holds these
+    c = torch.zeros(2, 1, 1, n, d, device="cuda")
+    s = torch.ones(2, 1, 1, n, device="cuda")
+    c[0, 0, 0, :, 0] = 0.9375                                    # e^-2.5 of a few rows', no power of two
+    c[0, 0, 0, 3::16, 0] = 1.0
+    s[0, 0, 0, :] = torch.where(torch.arange(n, device="cuda") == at, 2.0 ** -60, 1.0)    # its score is 0
+    c[1, 0, 0, :, 0] = torch.from_numpy(value)
+    c[1, 0, 0, at] = 0.0
+    c[1, 0, 0, at, d - 1] = 1.5
+    s[1, 0, 0, :] = torch.where(torch.arange(n, device="cuda") == at, 2.0 ** 20, 2.0 ** -14)
+    q = torch.zeros(1, 1, d, dtype=DT[dtype], device="cuda")
+    q[..., 0] = 40.0
+    score = 40.0 * host(c)[0, 0, 0, :, 0] * host(s)[0, 0, 0]
+    new = torch.zeros(1, 1, d, dtype=DT[dtype], device="cuda")
+    new[..., 0] = 1.0                                            # the row that is written: score 40
+    o = gdn.swa_step(c.to(torch.float8_e4m3fn), q, new, new * 2.0 ** -14, torch.full((1,), n - 1, dtype=torch.int32, device="cuda"),
+                     0, s, scale=1.0)
+    score[-1] = 40.0
+    w = np.exp(score - 40.0)
+    v = host(c)[1, 0, 0] * host(s)[1, 0, 0][:, None]
+    v[-1] = 0.0
+    v[-1, 0] = 2.0 ** -14
+    want = (w @ v) / w.sum()
+    within(o[0, 0], want, bound(n, dtype, want), dtype, f"{dtype} d{d} at {at}")
