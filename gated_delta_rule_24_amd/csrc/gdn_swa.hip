@@ -39,6 +39,7 @@ template <typename T>
 constexpr float kSlack = std::is_same_v<T, _Float16> ? 0.9f : 8.f;
 template <typename T>
 constexpr float kLift = std::is_same_v<T, _Float16> ? 15.f : 0.f;
+constexpr float kFarScores = 0x1p18f;   // log2: past this a maximum's rounding is no longer a small power
 
 template <typename T, int D, int NW>
 __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_fwd_kernel(SwaShape sh, const T *__restrict__ q,
@@ -104,10 +105,12 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
 
     f32x16_t acc[R::ND];
     float m, sum;                                  // log2 of what sums count in; this lane's part of the sum
+    bool far = false;                              // m is the largest score itself, subtracted before the scale
     const typename R::Lane lane;
-    // All tiles.  CAREFUL: what a row does not see may be infinite or NaN.  That is seen
-    // from sums that are not finite, and all is done again: it keeps the rare path's
-    // registers and its looks at V out of the other.
+    // All tiles.  CAREFUL: what a row does not see may be infinite or NaN, and scores may
+    // be so large that the maximum less its rounding is far from 0.  That is seen from
+    // sums that are not finite and from the maximum, and all is done again: it keeps the
+    // rare path's registers and its looks at V out of the other.
     auto walk = [&](auto careful) {
         constexpr bool CAREFUL = decltype(careful)::value;
 #pragma unroll
@@ -151,9 +154,9 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
                 for (int i = 0; i < 16; ++i) top = fmaxf(top, S[n][i]);
             top = half_max(top);
             // the largest exponent as it is taken below, so that no rounding of m adds to it
-            if (__any(fmaf(top, sh.c, -m) > kLift<T> + kSlack<T>)) {
-                const float up = fmaxf(m, fmaf(top, sh.c, -kLift<T>));
-                const float f = m == up ? 1.f : __builtin_amdgcn_exp2f(m - up);
+            if (__any(CAREFUL && far ? top > m : fmaf(top, sh.c, -m) > kLift<T> + kSlack<T>)) {
+                const float up = fmaxf(m, CAREFUL && far ? top : fmaf(top, sh.c, -kLift<T>));
+                const float f = m == up ? 1.f : __builtin_amdgcn_exp2f((m - up) * (CAREFUL && far ? sh.c : 1.f));
                 m = up;
                 sum *= f;
 #pragma unroll
@@ -166,7 +169,8 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
             for (int n = 0; n < NSUB; ++n)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    S[n][i] = __builtin_amdgcn_exp2f(fmaf(S[n][i], sh.c, -base));
+                    const float x = CAREFUL && far ? fmaf(S[n][i] - base, sh.c, kLift<T>) : fmaf(S[n][i], sh.c, -base);
+                    S[n][i] = __builtin_amdgcn_exp2f(x);
                     sum += S[n][i];
                 }
             if constexpr (CAREFUL) {
@@ -196,7 +200,10 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
         });
     };
     walk(std::false_type{});
-    if (__syncthreads_or(busy && any_not_finite(acc))) walk(std::true_type{});
+    const bool large = fabsf(m) > kFarScores && fabsf(m) < __builtin_inff();
+    far = __syncthreads_or(busy && large);
+    if (__syncthreads_or(busy && any_not_finite(acc)) || far) walk(std::true_type{});
+    if (far) m = fmaf(m, sh.c, -kLift<T>);
 
     if (!busy) return;
     sum = half_sum(sum);

@@ -298,9 +298,9 @@ __global__ __launch_bounds__(64 * kStepWaves, (Rows<T, D>::RB > 256 ? 2 : 4)) vo
                 big = fmaxf(big, S[a][i]);
             }
         big = fmaxf(big, __shfl_xor(big, 16, 64));
-        big = fmaxf(big, __shfl_xor(big, 32, 64)) * s.c;
+        big = fmaxf(big, __shfl_xor(big, 32, 64));
         if (__any(big > top)) {
-            const float up = fmaxf(top, big), f = top == up ? 1.f : __builtin_amdgcn_exp2f(top - up);
+            const float up = fmaxf(top, big), f = top == up ? 1.f : __builtin_amdgcn_exp2f((top - up) * s.c);
             top = up;
             sum *= f;
             if constexpr (UNITS) {
@@ -310,12 +310,13 @@ __global__ __launch_bounds__(64 * kStepWaves, (Rows<T, D>::RB > 256 ? 2 : 4)) vo
                 for (int dt = 0; dt < ND; ++dt) acc[dt] *= f;
             }
         }
-        const float base = (top == -__builtin_inff() ? 0.f : top) - LIFT;
+        // the largest score itself, subtracted before the scale: no rounding of it counts
+        const float base = top == -__builtin_inff() ? 0.f : top;
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                S[a][i] = __builtin_amdgcn_exp2f(fmaf(S[a][i], s.c, -base));
+                S[a][i] = __builtin_amdgcn_exp2f(fmaf(S[a][i] - base, s.c, LIFT));
                 sum += S[a][i];
                 // the scale joins before the rounding; a row that is not there has none
                 if constexpr (Q8)
@@ -395,7 +396,7 @@ __global__ __launch_bounds__(64 * kStepWaves, (Rows<T, D>::RB > 256 ? 2 : 4)) vo
         float x = 0.f, z = 0.f;
 #pragma unroll
         for (int w = 0; w < kStepWaves; ++w) {
-            const float f = __builtin_amdgcn_exp2f(s_m[w][g] - base);
+            const float f = __builtin_amdgcn_exp2f((s_m[w][g] - base) * s.c);
             z += f * s_l[w][g];
             x += f * reinterpret_cast<const float *>(s_v[w])[i];
         }
@@ -426,7 +427,7 @@ __global__ __launch_bounds__(1024) void swa_step_join_kernel(StepShape s, const 
     for (int w = 0; w < waves; ++w) up = fmaxf(up, s_m[w]);
     const float base = up == -__builtin_inff() ? 0.f : up;
     for (int p = tid; p < s.splits; p += nt) {
-        const float f = __builtin_amdgcn_exp2f(from[p * step] - base);
+        const float f = __builtin_amdgcn_exp2f((from[p * step] - base) * s.c);
         s_w[p] = f;
         z = fmaf(f, from[p * step + 1], z);
     }

@@ -610,7 +610,9 @@ gdn_status gdn_state_move(int32_t layers, int32_t slots, int64_t page_bytes, int
  *              probabilities down to 2^-28 of a query's largest, and gradients
  *              down to 2^-26 of the largest of a row of dQ or dK, are rounded
  *              once, what is less is off by at most 2^-39 (2^-37) of the largest.
- *              Scores, maxima, sums and lse are fp32.
+ *              Scores, maxima, sums and lse are fp32.  (The gradient takes its
+ *              probabilities from lse: they are off by its rounding, 2^-23 |lse|
+ *              relative, which matters for scores past 2^14 or so.)
  *   scale      finite and > 0
  *   flags      0
  * A sequence's queries are its last: the query i stands at position

@@ -10,10 +10,11 @@ import pytest
 import torch
 
 import gated_delta_rule_24_amd as gdn
+from oracle import attention as A
 
-from .op_util import DT, HALF, TINY, U, host, within
+from .op_util import DT, HALF, TINY, U, cu_tensor, host, within
 from .swa_terms import gradients
-from .test_swa import inputs
+from .test_swa import errors, inputs
 from .test_swa_small_weights import bound, case
 
 pytestmark = pytest.mark.gpu
@@ -166,3 +167,69 @@ def test_step_beside_an_outlying_scale(dtype, d, at):
     v[-1, 0] = 2.0 ** -14
     want = (w @ v) / w.sum()
     within(o[0, 0], want, bound(n, dtype, want), dtype, f"{dtype} d{d} at {at}")
+
+
+def large(dtype, d, size, sign, n):
+    """n keys whose scores are sign size - step j, exact in fp32, and the values: (q, k, v, scores)."""
+    step = max(1.0, size * 2.0 ** -23)
+    a = 2.0 ** (np.log2(size) // 2)
+    q, k, v = (torch.zeros(1, t, 1, d, device="cuda") for t in (1, n, n))
+    q[..., 0], q[..., 1] = a, 2.0 ** (np.log2(step) // 2)
+    k[..., 0] = sign * size / a
+    k[0, :, 0, 1] = -torch.arange(n, device="cuda") % 7 * (step / 2.0 ** (np.log2(step) // 2))
+    g = np.random.default_rng(n)
+    v[0, :, 0] = torch.from_numpy(g.uniform(0.5, 2.0, (n, d)))
+    q, k, v = (x.to(DT[dtype]) for x in (q, k, v))
+    return q, k, v, host(k)[0, :, 0] @ host(q)[0, 0, 0]
+
+
+LARGE = [(2.0 ** 16, "fp16"), (2.0 ** 20, "fp16"), (2.0 ** 24, "fp16"), (2.0 ** 25, "fp16"), (2.0 ** 26, "fp16"),
+         (2.0 ** 27, "fp16"), (2.0 ** 28, "fp16"), (2.0 ** 29, "fp16"), (2.0 ** 20, "bf16"), (2.0 ** 26, "bf16"),
+         (2.0 ** 31, "bf16"), (2.0 ** 32, "bf16"), (2.0 ** 34, "bf16"), (2.0 ** 40, "bf16"), (2.0 ** 20, "fp32"),
+         (2.0 ** 31, "fp32"), (2.0 ** 33, "fp32"), (2.0 ** 60, "fp32")]
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size,dtype", LARGE)
+@pytest.mark.parametrize("d,n", [(64, 300), (128, 33)])
+def test_large_scores(size, dtype, sign, d, n):
+    """Scores as large as products of the type are, which fp32 holds exactly, and differ by few of their units: the softmax is of
+    the differences.  Its exponents are below 6 size 2^-23 log2 e, off by 2 U of that; past 40 the exponential is below the rest's
+    rounding.  lse: two roundings of its size more."""
+    q, k, v, s = large(dtype, d, size, sign, n)
+    x = s - s.max()
+    w = np.exp(x)
+    want = (w @ host(v)[0, :, 0]) / w.sum()
+    room = 2 * ((n + 72 + 40 * 4) * U + HALF[dtype]) * want
+    o, lse = gdn.swa_fwd(q, k, v, n, scale=1.0)
+    within(o[0, 0, 0], want, room, dtype, f"{dtype} d{d} {sign * size}")
+    assert abs(lse.item() - (s.max() + np.log(w.sum()))) <= 8 * U * size
+    c = torch.zeros(2, 1, 1, n, d, device="cuda", dtype=DT[dtype])
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gdn.cache_write(c, k[:, :-1].contiguous(), v[:, :-1].contiguous(), zero)
+    o = gdn.swa_step(c, q[:, 0], k[:, -1], v[:, -1], zero + n - 1, scale=1.0)
+    within(o[0, 0], want, room, dtype, f"step {dtype} d{d} {sign * size}")
+
+
+def test_large_scores_beside_small_ones():
+    """Rows of either kind in one tile, in packed sequences, with sinks and hidden values that are not finite."""
+    T, d = 200, 64
+    t, x = inputs(77, 1, T, T, 2, 1, d, "fp32")
+    t[0][0, 50:60] *= 2.0 ** 24
+    t[0][0, 130] *= -2.0 ** 33
+    cu = [0, 90, 200]
+    o, lse = gdn.swa_fwd(*t, 30, 2, cu_tensor(cu))
+    q, k, v = (host(y) for y in t)
+    # fp32's scores themselves are off: those rows by what their own scores say, the others as ever
+    calm = np.ones(T, bool)
+    calm[50:60] = calm[130] = False
+    ro, rl = A.attention(q, k, v, 30, 2, cu)
+    within(o[0, calm], ro[0, calm], 2 * (errors(q[0, calm], k, d ** -0.5) + 200 * U) * np.abs(v).max(), "fp32", "calm rows")
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    seen = [90, 91, *range(101, 131)]                            # one key takes all of row 130
+    best = seen[int(np.argmax(q[0, 130, 0] @ k[0, seen, 0].T))]
+    within(o[0, 130, 0], v[0, best, 0], 0.0, "fp32", "one key")
+    v2 = t[2].clone()
+    v2[0, 150:] = float("nan")
+    again, _ = gdn.swa_fwd(t[0], t[1], v2, 30, 2, cu_tensor(cu))
+    within(again[0, :150], host(o)[0, :150], 64 * U * np.abs(v).max(), "fp32", "hidden values")
