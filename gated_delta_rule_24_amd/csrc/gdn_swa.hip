@@ -202,11 +202,17 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
     walk(std::false_type{});
     const bool large = fabsf(m) > kFarScores && fabsf(m) < __builtin_inff();
     far = __syncthreads_or(busy && large);
-    if (__syncthreads_or(busy && any_not_finite(acc)) || far) walk(std::true_type{});
+    const bool again = __syncthreads_or(busy && any_not_finite(acc)) || far;
+    if (again) walk(std::true_type{});
     if (far) m = fmaf(m, sh.c, -kLift<T>);
 
     if (!busy) return;
     sum = half_sum(sum);
+    if (again && sum == 0.f)                       // nothing but scores of -inf: no value counts
+#pragma unroll
+        for (int dt = 0; dt < R::ND; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[dt][i] = 0.f;
     store_column<T, D>(o + at * D, acc, sum == 0.f ? 0.f : 1.f / sum, on);
     if (lse && on && h == 0)
         lse[at] = sum == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;

@@ -168,7 +168,8 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
                 const float x = __builtin_amdgcn_exp2f(fmaf(S[i], sh.c, -base)) * (P[i] - dd);
                 if constexpr (MASK) {
                     const int j = j0 + r0 + 4 * (ln.l >> 5) + 8 * (i >> 2) + (i & 3);
-                    const bool see = j <= pos && j < jend && (j > pos - W || j < sh.sinks);
+                    bool see = j <= pos && j < jend && (j > pos - W || j < sh.sinks);
+                    if constexpr (CAREFUL) see &= lse2 != __builtin_inff();   // a row without weights has no gradient
                     S[i] = see ? x : 0.f;
                     seen |= (uint32_t)see << i;
                 } else {
@@ -388,7 +389,8 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
                     p = __builtin_amdgcn_exp2f(fmaf(p, sh.c, -L[e]));
                     if constexpr (MASK) {
                         const int token = t0 + tok[e], pos = token + shift;
-                        const bool see = token < tb && key <= pos && (key > pos - W || key < sh.sinks);
+                        bool see = token < tb && key <= pos && (key > pos - W || key < sh.sinks);
+                        if constexpr (CAREFUL) see &= L[e] != __builtin_inff();
                         p = see ? p : 0.f;
                         seen |= (uint32_t)see << i;
                     }

@@ -1,0 +1,52 @@
+"""Windowed attention with values that are not finite: what has no weight adds nothing, forward and backward."""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_24_amd as gdn
+from oracle import attention as A
+
+from .op_util import DT, HALF, U, cu_tensor, host, within
+from .swa_terms import gradients
+from .test_swa import errors, inputs
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("d,T,window,sinks", [(64, 100, 40, 2), (128, 300, 70, 0), (32, 600, 20, 33)])
+@pytest.mark.parametrize("cu", [False, True])
+def test_rows_whose_scores_are_all_minus_infinity(dtype, d, T, window, sinks, cu):
+    """They count as rows that see nothing: o is 0, lse -inf, and they give no gradient, whatever their values and the
+    gradient of their o are.  The others' results are the formula's."""
+    cu = [0, 37, 37, T] if cu else None
+    c = cu_tensor(cu)
+    t, _ = inputs(d + T, 1, T, T, 4, 2, d, dtype)
+    q, k, v = (y.clone() for y in t)
+    k.abs_()
+    gone = [3, 36, 50, T - 30, T - 1]
+    q[0, gone, 1] = -INF                                         # one head of those rows; the last's sees inf too
+    q[0, T - 1, 0] = -INF
+    v[0, T - 1, 0, 5] = INF
+    o, lse = gdn.swa_fwd(q, k, v, window, sinks, c)
+    x = [host(y) for y in (q, k, v)]
+    with np.errstate(invalid="ignore"):
+        ro, rl = A.attention(*x, window, sinks, cu)
+    assert (host(lse)[0, gone, 1] == -np.inf).all() and not o[0, gone, 1].any() and not o[0, T - 1, 0].any()
+    clean = [np.where(np.isfinite(y), y, 0.0) for y in x]
+    e = errors(clean[0], clean[1], d ** -0.5) + (window + sinks + 8) * U
+    within(o, ro, 2 * (e + HALF[dtype]) * np.abs(clean[2]).max(), dtype, "o")
+
+    do = torch.randn(q.shape, generator=torch.Generator("cuda").manual_seed(d), device="cuda").to(DT[dtype])
+    do[0, 50, 1, 3] = float("nan")                               # of a row that is gone
+    do[0, 3, 1, 2] = INF
+    got = gdn.swa_bwd(do, q, k, v, o, lse, window, sinks, c)
+    assert not got[0][0, gone, 1].any()
+    g = host(do)
+    g[~np.isfinite(g)] = 0.0
+    finite = [np.where(np.isfinite(y), y, 0.0) for y in x]
+    for name, y, (w, room) in zip(("dq", "dk", "dv"), got,
+                                  gradients(g, *finite, host(o), host(lse), window, sinks, cu, h=HALF[dtype])):
+        within(y, w, room, dtype, name)
