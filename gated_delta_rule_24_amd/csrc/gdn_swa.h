@@ -67,6 +67,14 @@ struct SwaShape {
     float scale;
 };
 
+// A launch counts its threads along x in 32 bits: blocks past 2^20 go on along y.
+constexpr int kGridBits = 20;
+inline dim3 swa_grid(int64_t blocks) {
+    blocks = (blocks + 7) / 8 * 8;
+    if (blocks <= 1 << kGridBits) return dim3((unsigned)blocks);
+    return dim3(1u << kGridBits, (unsigned)((blocks + (1 << kGridBits) - 1) >> kGridBits));
+}
+
 struct SwaUnit {
     int unit, hk, role;              // unit of the sequence, key head, which of `roles`
     int64_t q0, k0;                  // the sequence's first query and key
@@ -86,14 +94,15 @@ __device__ __forceinline__ bool swa_find(const SwaShape &s, bool last_first, Swa
         units = s.meta[0];
     }
     const int64_t total = (int64_t)units * s.KV * ROLES;
-    const int64_t per = (total + 7) / 8, i = blockIdx.x >> 3;
-    int64_t at = (blockIdx.x & 7) * per + i;
+    const uint32_t block = blockIdx.y << kGridBits | blockIdx.x;
+    const int64_t per = (total + 7) / 8, i = block >> 3;
+    int64_t at = (block & 7) * per + i;
     if (i >= per || at >= total) return false;
     const int pairs = s.cu ? 0 : units / max(s.per_seq, 1) * s.KV;
     if (pairs % 8 == 0 && !s.cu) {   // whole (sequence, key head) pairs to an XCD: the longest units of all of them first
         const int share = pairs / 8 * ROLES;
         const int x = (int)(i / share), y = (int)(i - (int64_t)x * share);
-        const int pair = (blockIdx.x & 7) * (pairs / 8) + y / ROLES;
+        const int pair = (block & 7) * (pairs / 8) + y / ROLES;
         u.role = y % ROLES;
         u.hk = pair % s.KV;
         u.n = pair / s.KV;

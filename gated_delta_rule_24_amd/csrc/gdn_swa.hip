@@ -368,11 +368,10 @@ hipError_t launch_swa_fwd(const SwaArgs &a, hipStream_t st) {
         constexpr int D = decltype(dim)::value;
         auto go = [&](auto waves) {
             constexpr int NW = decltype(waves)::value;
-            const unsigned blocks = (unsigned)((units * a.KV + 7) / 8 * 8);
             constexpr int lds = 4 * kKeys * Rows<T, D>::RB;
             hipError_t e = swa_lds(swa_fwd_kernel<T, D, NW>, lds);
             if (e != hipSuccess) return e;
-            swa_fwd_kernel<T, D, NW><<<blocks, 64 * NW, lds, st>>>(
+            swa_fwd_kernel<T, D, NW><<<swa_grid(units * a.KV), 64 * NW, lds, st>>>(
                 s, static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.v),
                 static_cast<T *>(a.o), a.lse);
             return hipGetLastError();

@@ -513,11 +513,13 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
 // of lanes, which take the parts in turn and join in LDS, in a fixed order.
 constexpr int kSinkLanes = 32;
 template <typename T>
-__global__ __launch_bounds__(1024) void swa_sinks_kernel(SwaShape sh, int far, int D, const float *__restrict__ share,
+__global__ __launch_bounds__(1024) void swa_sinks_kernel(SwaShape sh, int pairs, int far, int D, const float *__restrict__ share,
                                                          T *__restrict__ dk, T *__restrict__ dv) {
     __shared__ float sum[32][kSinkLanes + 1];
     if (sh.cu && sh.meta[1]) return;
-    const int n = blockIdx.x / sh.KV, hk = blockIdx.x - n * sh.KV;
+    const int pair = (int)(blockIdx.z << kGridBits | blockIdx.x);   // sequence, key head
+    if (pair >= pairs) return;
+    const int n = pair / sh.KV, hk = pair - n * sh.KV;
     int64_t q0 = (int64_t)n * sh.T, k0 = (int64_t)n * sh.Tk;
     int Lq = sh.T, Lk = sh.Tk;
     if (sh.cu) {
@@ -588,7 +590,7 @@ hipError_t launch_swa_bwd(const SwaArgs &a, hipStream_t st) {
                 constexpr int NW = decltype(waves)::value, lds = 4 * kKeys * RB;
                 hipError_t x = swa_lds(swa_dq_kernel<T, D, NW>, lds);
                 if (x != hipSuccess) return x;
-                swa_dq_kernel<T, D, NW><<<(unsigned)((units * a.KV + 7) / 8 * 8), 64 * NW, lds, st>>>(
+                swa_dq_kernel<T, D, NW><<<swa_grid(units * a.KV), 64 * NW, lds, st>>>(
                     s, in(a.q), in(a.k), in(a.v), in(a.o), a.lse, in(a.d_o), out(a.dq), dsum);
                 return hipGetLastError();
             };
@@ -601,15 +603,16 @@ hipError_t launch_swa_bwd(const SwaArgs &a, hipStream_t st) {
             e = swa_lds(swa_dkv_kernel<T, D>, lds);
             if (e != hipSuccess) return e;
             constexpr int roles = kSplitKeySide<T, D> ? 2 : 1;
-            swa_dkv_kernel<T, D><<<(unsigned)((key_units * a.KV * roles + 7) / 8 * 8), 256, lds, st>>>(
+            swa_dkv_kernel<T, D><<<swa_grid(key_units * a.KV * roles), 256, lds, st>>>(
                 sk, far, in(a.q), in(a.k), in(a.v), a.lse, in(a.d_o), dsum, out(a.dk), out(a.dv), share);
             e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
         if (join) {
             ProfScope prof("gdn_swa_sinks", st);
-            const dim3 grid((unsigned)(a.N * a.KV), (unsigned)(2 * a.sinks * D / kSinkLanes));
-            swa_sinks_kernel<T><<<grid, 1024, 0, st>>>(s, far, D, share, out(a.dk), out(a.dv));
+            const int pairs = a.N * a.KV;
+            const dim3 all = swa_grid(pairs), grid(all.x, (unsigned)(2 * a.sinks * D / kSinkLanes), all.y);
+            swa_sinks_kernel<T><<<grid, 1024, 0, st>>>(s, pairs, far, D, share, out(a.dk), out(a.dv));
             e = hipGetLastError();
         }
         return e;
