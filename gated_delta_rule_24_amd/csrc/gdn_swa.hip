@@ -323,7 +323,7 @@ SwaWorkspace swa_workspace_layout(const SwaArgs &a, bool bwd) {
     const int64_t T = (int64_t)a.B * a.T, Tk = (int64_t)a.B * a.Tk, far = far_tokens(a);
     const bool table = a.B == 1;                  // a packed batch, or one sequence
     w.row_units = T / tokens + a.N;
-    w.far_units = a.sinks ? T / far + a.N : 0;
+    w.far_units = a.sinks ? Tk / far : 0;         // a sequence has keys / far at most
     w.key_units = Tk / kSwaKeyTile + a.N + w.far_units;
     size_t at = 256;
     auto take = [&](size_t bytes) {
@@ -335,8 +335,8 @@ SwaWorkspace swa_workspace_layout(const SwaArgs &a, bool bwd) {
     if (bwd) {
         w.off_keys = take(table ? (size_t)w.key_units * 8 : 0);
         w.off_dsum = take((size_t)T * a.H * 4);
-        // every part of the sinks' tile, the near one included: dK and dV of the sinks in fp32
-        w.off_far = take(a.sinks ? (size_t)(w.far_units + a.N) * a.KV * 2 * a.sinks * a.D * 4 : 0);
+        // every part of the sinks' tile, the near ones included: dK and dV of the sinks in fp32
+        w.off_far = take((size_t)(2 * w.far_units) * a.KV * 2 * a.sinks * a.D * 4);
     }
     w.total = at;
     return w;

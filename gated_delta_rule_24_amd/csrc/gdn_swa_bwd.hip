@@ -231,8 +231,10 @@ __host__ __device__ __forceinline__ FarParts far_parts(int Lq, int Lk, int windo
     f.parts = sinks && Lk > 0 ? (Lq - f.reach + far - 1) / far : 0;
     return f;
 }
-// First part of sequence n in the workspace: part 0 is the near one's.
-__device__ __forceinline__ int64_t far_first(int64_t q0, int n, int far) { return q0 / far + 2 * (int64_t)n; }
+// First part in the workspace of a sequence that has any: part 0 is the near one's.  Its keys are
+// then `far` or more, and its parts at most keys / far: with the near one not more than
+// twice that, so by its first key no two sequences share a place.
+__device__ __forceinline__ int64_t far_first(int64_t k0, int far) { return 2 * (k0 / far); }
 
 // The two accumulators and the operands K and V of a wave are 3 D 32-bit registers
 // in 16 bits, 4 D in fp32.  Where that leaves too few of 256, dV and dK are made by
@@ -495,7 +497,7 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
             if (MAKE_V) store_column<T, D>(dv + at * D, av, UNLIFT, on);
         }
         if (fp.parts > 0 && k0 < sh.sinks && jt == 0) {
-            const int64_t slot = far_first(u.q0, u.n, far) + (part >= 0 ? part + 1 : 0);
+            const int64_t slot = far_first(u.k0, far) + (part >= 0 ? part + 1 : 0);
             float *to = share + ((slot * sh.KV + u.hk) * 2 * sh.sinks + key) * (int64_t)D;
             if (MAKE_K) store_column<float, D>(to, ak, scale, shared && key < u.Lk);
             if (MAKE_V) store_column<float, D>(to + (int64_t)sh.sinks * D, av, UNLIFT, shared && key < u.Lk);
@@ -520,10 +522,10 @@ __global__ __launch_bounds__(1024) void swa_sinks_kernel(SwaShape sh, int pairs,
     const int pair = (int)(blockIdx.z << kGridBits | blockIdx.x);   // sequence, key head
     if (pair >= pairs) return;
     const int n = pair / sh.KV, hk = pair - n * sh.KV;
-    int64_t q0 = (int64_t)n * sh.T, k0 = (int64_t)n * sh.Tk;
+    int64_t k0 = (int64_t)n * sh.Tk;
     int Lq = sh.T, Lk = sh.Tk;
     if (sh.cu) {
-        q0 = sh.cu[n], Lq = sh.cu[n + 1] - sh.cu[n];
+        Lq = sh.cu[n + 1] - sh.cu[n];
         k0 = sh.cuk[n], Lk = sh.cuk[n + 1] - sh.cuk[n];
     }
     const FarParts fp = far_parts(Lq, Lk, sh.window, sh.sinks, far);
@@ -532,7 +534,7 @@ __global__ __launch_bounds__(1024) void swa_sinks_kernel(SwaShape sh, int pairs,
     const int x = threadIdx.x % kSinkLanes, g = threadIdx.x / kSinkLanes, all = sh.sinks * D;
     const int i = blockIdx.y * kSinkLanes + x, e = i < all ? i : i - all;
     const int64_t step = (int64_t)sh.KV * 2 * all;
-    const float *from = share + far_first(q0, n, far) * step + (int64_t)hk * 2 * all + i;
+    const float *from = share + far_first(k0, far) * step + (int64_t)hk * 2 * all + i;
     const bool on = e / D < Lk;
     float a = 0.f;
     if (on)
