@@ -266,28 +266,8 @@ struct Rows {
         }
     }
 
-    // Whether rows r0 .. r0 + 31 hold an infinity or a NaN (the same answer in all lanes).
-    __device__ __forceinline__ static bool not_finite(const char *t, const Lane &ln, int r0) {
-        uint32_t bad = 0;
-#pragma unroll 4
-        for (int b = 0; b < 32 * RB; b += 1024) {
-            const u32x4_t x = *reinterpret_cast<const u32x4_t *>(t + r0 * RB + b + ln.l * 16);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (F32) {
-                    bad |= (x[e] & 0x7F800000u) == 0x7F800000u;
-                } else {
-                    constexpr uint32_t M = std::is_same_v<T, bf16_t> ? 0x7F80u : 0x7C00u;
-                    bad |= (x[e] & M) == M;
-                    bad |= ((x[e] >> 16) & M) == M;
-                }
-            }
-        }
-        return __any(bad != 0);
-    }
-
     // add() for a tile that hides some of its (row, column) pairs and whose rows
-    // are not all finite: a hidden pair has weight 0, and 0 times infinity must
+    // may not be finite: a hidden pair has weight 0, and 0 times infinity must
     // not count.  The rows' finite values go through add()'s product.  What is seen
     // of +inf and NaN then adds a product that overflows to +inf, what is seen of
     // -inf and NaN one to -inf: both make a NaN, and a hidden one adds 0.  seen: bit

@@ -110,7 +110,8 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
     // All tiles.  CAREFUL: what a row does not see may be infinite or NaN, and scores may
     // be so large that the maximum less its rounding is far from 0.  That is seen from
     // sums that are not finite and from the maximum, and all is done again: it keeps the
-    // rare path's registers and its looks at V out of the other.
+    // rare path's registers and its looks at V out of the other.  It takes the same steps, 32
+    // keys at a time: rows that see nothing of the kind come out with the same bits.
     auto walk = [&](auto careful) {
         constexpr bool CAREFUL = decltype(careful)::value;
 #pragma unroll
@@ -126,6 +127,39 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
                 if (busy) body(tile_at(x), smem + (x & 1) * 2 * TILE);
             }
         };
+        // A row's maximum follows a tile's largest score.  That is the row's own matter: no bit
+        // of its sums comes from the wave's other rows.
+        auto raise = [&](float top) {
+            // the largest exponent as it is taken below, so that no rounding of m adds to it
+            const bool over = CAREFUL && far ? top > m : fmaf(top, sh.c, -m) > kLift<T> + kSlack<T>;
+            if (__any(over)) {
+                const float up = !over ? m : CAREFUL && far ? top : fmaf(top, sh.c, -kLift<T>);
+                const float f = over ? __builtin_amdgcn_exp2f((m - up) * (CAREFUL && far ? sh.c : 1.f)) : 1.f;
+                m = up;
+                sum *= f;
+#pragma unroll
+                for (int dt = 0; dt < R::ND; ++dt)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[dt][i] *= f;
+            }
+        };
+        // Scores of the 32 keys from j0 + r0 on: -inf where the row does not see them.
+        auto mask = [&](f32x16_t &S, int j0, int jend, int r0, const typename R::Lane &ln) {
+            uint32_t seen = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int j = j0 + r0 + 4 * (ln.l >> 5) + 8 * (i >> 2) + (i & 3);
+                const bool see = j <= pos && j < jend && (j > pos - W || j < sh.sinks);
+                S[i] = see ? S[i] : -__builtin_inff();
+                seen |= (uint32_t)see << i;
+            }
+            return seen;
+        };
+        auto largest = [](float top, const f32x16_t &S) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, S[i]);
+            return top;
+        };
         auto process = [&](auto subs, auto masked, const char *kt, int j0, int jend, int r0) {
             const char *vt = kt + TILE;
             constexpr int NSUB = decltype(subs)::value;
@@ -138,31 +172,12 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
                 for (int i = 0; i < 16; ++i) S[n][i] = 0.f;
             R::dot(S, kt, ln, r0, qf);
             uint32_t seen = 0;
-            if constexpr (MASK) {
+            if constexpr (MASK) seen = mask(S[0], j0, jend, r0, ln);
+            if constexpr (!CAREFUL) {
+                float top = S[0][0];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int j = j0 + r0 + 4 * (ln.l >> 5) + 8 * (i >> 2) + (i & 3);
-                    const bool see = j <= pos && j < jend && (j > pos - W || j < sh.sinks);
-                    S[0][i] = see ? S[0][i] : -__builtin_inff();
-                    seen |= (uint32_t)see << i;
-                }
-            }
-            float top = S[0][0];
-#pragma unroll
-            for (int n = 0; n < NSUB; ++n)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, S[n][i]);
-            top = half_max(top);
-            // the largest exponent as it is taken below, so that no rounding of m adds to it
-            if (__any(CAREFUL && far ? top > m : fmaf(top, sh.c, -m) > kLift<T> + kSlack<T>)) {
-                const float up = fmaxf(m, CAREFUL && far ? top : fmaf(top, sh.c, -kLift<T>));
-                const float f = m == up ? 1.f : __builtin_amdgcn_exp2f((m - up) * (CAREFUL && far ? sh.c : 1.f));
-                m = up;
-                sum *= f;
-#pragma unroll
-                for (int dt = 0; dt < R::ND; ++dt)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[dt][i] *= f;
+                for (int n = 0; n < NSUB; ++n) top = largest(top, S[n]);
+                raise(half_max(top));
             }
             const float base = m == -__builtin_inff() ? 0.f : m;
 #pragma unroll
@@ -174,10 +189,8 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
                     sum += S[n][i];
                 }
             if constexpr (CAREFUL) {
-                if (R::not_finite(vt, ln, r0)) {
-                    R::add_seen(acc, vt, ln, r0, S[0], seen);
-                    return;
-                }
+                R::add_seen(acc, vt, ln, r0, S[0], seen);
+                return;
             }
 #pragma unroll
             for (int n = 0; n < NSUB; ++n) R::add(acc, vt, ln, r0 + 32 * n, S[n]);
@@ -185,19 +198,42 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
         };
         using std::integral_constant;
         if (tiles) load(0);
-        if constexpr (!CAREFUL)
+        // 32 keys that no row of the wave sees are left out
+        auto left_out = [&](int j, int jend) { return j > p1 || j >= jend || (j + 31 <= p0 - W && j >= sh.sinks); };
+        if constexpr (CAREFUL) {
+            int x = 0;
+            each(0, tiles, [&](int it, const char *kt) {
+                const bool all = x++ < whole;      // of such a tile 64 keys have one maximum
+                const int j0 = first_key(it), jend = it < ns ? sh.sinks : high;
+#pragma unroll 1
+                for (int r0 = 0; r0 < kKeys; r0 += 32) {
+                    if (left_out(j0 + r0, jend)) continue;
+                    float top = -__builtin_inff();
+#pragma unroll 1
+                    for (int r = all ? 0 : r0; r < (all ? kKeys : r0 + 32); r += 32) {
+                        const typename R::Lane ln = lane.fresh();
+                        f32x16_t S[1];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) S[0][i] = 0.f;
+                        R::dot(S, kt, ln, r, qf);
+                        mask(S[0], j0, jend, r, ln);
+                        top = largest(top, S[0]);
+                    }
+                    raise(half_max(top));
+                    process(integral_constant<int, 1>{}, std::true_type{}, kt, j0, jend, r0);
+                }
+            });
+        } else {
             each(0, whole, [&](int it, const char *kt) {
                 process(integral_constant<int, kKeys / 32>{}, std::false_type{}, kt, first_key(it), 0, 0);
             });
-        each(CAREFUL ? 0 : whole, tiles, [&](int it, const char *kt) {
-            const int j0 = first_key(it), jend = it < ns ? sh.sinks : high;
+            each(whole, tiles, [&](int it, const char *kt) {
+                const int j0 = first_key(it), jend = it < ns ? sh.sinks : high;
 #pragma unroll 1
-            for (int r0 = 0; r0 < kKeys; r0 += 32) {
-                const int j = j0 + r0;           // 32 keys that no row of the wave sees are left out
-                if (j > p1 || j >= jend || (j + 31 <= p0 - W && j >= sh.sinks)) continue;
-                process(integral_constant<int, 1>{}, std::true_type{}, kt, j0, jend, r0);
-            }
-        });
+                for (int r0 = 0; r0 < kKeys; r0 += 32)
+                    if (!left_out(j0 + r0, jend)) process(integral_constant<int, 1>{}, std::true_type{}, kt, j0, jend, r0);
+            });
+        }
     };
     walk(std::false_type{});
     const bool large = fabsf(m) > kFarScores && fabsf(m) < __builtin_inff();

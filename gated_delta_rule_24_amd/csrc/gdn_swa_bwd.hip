@@ -33,9 +33,10 @@ namespace gdn {
 constexpr int kKeys = 64;            // keys of a staged tile, query side
 constexpr int kRows = 64;            // rows of a staged tile, key side
 
-__device__ __forceinline__ float log2_lse(float lse) {
+// In one rounding, so that all places that take it have the same bits.
+__device__ __forceinline__ float log2_lse(float lse, float lift = 0.f) {
     // a row that saw nothing: every probability 0
-    return lse == -__builtin_inff() ? __builtin_inff() : lse * 1.4426950408889634f;
+    return lse == -__builtin_inff() ? __builtin_inff() : fmaf(lse, 1.4426950408889634f, -lift);
 }
 
 // fp16 holds dS only from 2^-24 to 65504, and many small ones may make up dQ and dK (of
@@ -190,13 +191,8 @@ __global__ __launch_bounds__(64 * NW, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_
                     for (int dt = 0; dt < R::ND; ++dt) acc[dt] *= f;
                 }
             }
-            if constexpr (CAREFUL) {
-                if (R::not_finite(kt, ln, r0)) {
-                    R::add_seen(acc, kt, ln, r0, S, seen);
-                    return;
-                }
-            }
-            R::add(acc, kt, ln, r0, S);
+            if constexpr (CAREFUL) R::add_seen(acc, kt, ln, r0, S, seen);
+            else R::add(acc, kt, ln, r0, S);
         };
         if (tiles) load(0);
         if constexpr (!CAREFUL)
@@ -341,7 +337,7 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
         if (wave < 2) {
             const bool there = srow < rows && stoken < n;
             const int64_t a = first + (there ? (int64_t)stoken * sh.H + srow % sh.G : 0);
-            stat = wave == 0 ? log2_lse(lse[a]) - lift : LIFT ? -dsum[a] : dsum[a];
+            stat = wave == 0 ? log2_lse(lse[a], lift) : LIFT ? -dsum[a] : dsum[a];
             if (!there) stat = wave == 0 ? __builtin_inff() : 0.f;
         }
     };
@@ -364,11 +360,22 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
             }
         // what other lanes of a far part make is dropped
         if constexpr (LIFT) unit = part < 0 || key < sh.sinks ? power_of_2(kLiftDs) : 0.f;
-        auto process = [&](auto subs, auto masked, int x, int t0, int r0) {
+        // The unit follows a tile's largest dS; returns by what its elements are to be lowered.
+        auto lower = [&](float t) {
+            const float f = power_of_2(-lower_ds(half_max(t)));
+            unit *= f;
+#pragma unroll
+            for (int dt = 0; dt < R::ND; ++dt) ak[dt] *= f;
+            return f;
+        };
+        // CAREFUL: `look` asks for the largest dS of each key alone, and the unit follows it
+        // before the sums are made.
+        float peak = 0.f;
+        auto process = [&](auto subs, auto masked, auto looks, int x, int t0, int r0) {
             const char *qt = smem + (x & 1) * 2 * TILE, *gt = qt + TILE;
             const float *st = stats + (x & 1) * 2 * kRows;
             constexpr int NSUB = decltype(subs)::value;
-            constexpr bool MASK = decltype(masked)::value;
+            constexpr bool MASK = decltype(masked)::value, LOOK = decltype(looks)::value;
             const typename R::Lane ln = lane.fresh();
             const float *sr = st + r0 + 4 * (ln.l >> 5);
             f32x16_t S[NSUB], P[NSUB];
@@ -399,10 +406,8 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
                     S[a >> 2][i] = p;
                 }
             }
-            bool bad = false;
-            if constexpr (CAREFUL) bad = R::not_finite(qt, ln, r0) || R::not_finite(gt, ln, r0);
-            if constexpr (MAKE_V) {
-                if (CAREFUL && bad) {
+            if constexpr (MAKE_V && !LOOK) {
+                if constexpr (CAREFUL) {
                     R::add_seen(av, gt, ln, r0, S[0], seen);
                 } else {
 #pragma unroll
@@ -436,16 +441,17 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
                 for (int n = 0; n < NSUB; ++n)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) t = fmaxf(t, fabsf(P[n][i]));
-                if (__any(t >= kMostDs)) {
-                    const float f = power_of_2(-lower_ds(half_max(t)));
-                    unit *= f;
+                if constexpr (LOOK) {
+                    peak = fmaxf(peak, t);
+                    return;
+                }
+                if (!CAREFUL && __any(t >= kMostDs)) {
+                    const float f = lower(t);
 #pragma unroll
                     for (int n = 0; n < NSUB; ++n) P[n] *= f;
-#pragma unroll
-                    for (int dt = 0; dt < R::ND; ++dt) ak[dt] *= f;
                 }
             }
-            if (CAREFUL && bad) {
+            if constexpr (CAREFUL) {
                 R::add_seen(ak, qt, ln, r0, P[0], seen);
             } else {
 #pragma unroll
@@ -465,19 +471,39 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
             load(0);
             put(0);
         }
-        if constexpr (!CAREFUL)
-            each(0, whole, [&](int x, int t0) {
-                process(std::integral_constant<int, kRows / 32>{}, std::false_type{}, x, t0, 0);
-            });
-        each(CAREFUL ? 0 : whole, tiles, [&](int x, int t0) {
+        // 32 rows of which none sees a key of the wave are left out
+        auto left_out = [&](int t0, int r0) {
+            const int a = t0 + (r0 ? half : 0), b = min(t0 + (r0 ? sh.tokens : half_end), tb) - 1;
+            return r0 >= rows || a >= tb || k0 > b + shift || (k0 + 31 <= a + shift - W && k0 >= sh.sinks);
+        };
+        using std::integral_constant;
+        if constexpr (CAREFUL) {
+            each(0, tiles, [&](int x, int t0) {
+                const bool all = x < whole;        // of such a tile 64 rows have one largest dS
 #pragma unroll 1
-            for (int r0 = 0; r0 < kRows; r0 += 32) {
-                // 32 rows of which none sees a key of the wave are left out
-                const int a = t0 + (r0 ? half : 0), b = min(t0 + (r0 ? sh.tokens : half_end), tb) - 1;
-                if (r0 >= rows || a >= tb || k0 > b + shift || (k0 + 31 <= a + shift - W && k0 >= sh.sinks)) continue;
-                process(std::integral_constant<int, 1>{}, std::true_type{}, x, t0, r0);
-            }
-        });
+                for (int r0 = 0; r0 < kRows; r0 += 32) {
+                    if (left_out(t0, r0)) continue;
+                    if constexpr (LIFT && MAKE_K) {
+                        peak = 0.f;
+#pragma unroll 1
+                        for (int r = all ? 0 : r0; r < (all ? rows : r0 + 32); r += 32)
+                            process(integral_constant<int, 1>{}, std::true_type{}, std::true_type{}, x, t0, r);
+                        if (__any(peak >= kMostDs)) lower(peak);
+                    }
+                    process(integral_constant<int, 1>{}, std::true_type{}, std::false_type{}, x, t0, r0);
+                }
+            });
+        } else {
+            each(0, whole, [&](int x, int t0) {
+                process(integral_constant<int, kRows / 32>{}, std::false_type{}, std::false_type{}, x, t0, 0);
+            });
+            each(whole, tiles, [&](int x, int t0) {
+#pragma unroll 1
+                for (int r0 = 0; r0 < kRows; r0 += 32)
+                    if (!left_out(t0, r0))
+                        process(integral_constant<int, 1>{}, std::true_type{}, std::false_type{}, x, t0, r0);
+            });
+        }
     };
     auto run = [&](auto make_v, auto make_k) {
         constexpr bool MAKE_V = decltype(make_v)::value, MAKE_K = decltype(make_k)::value;

@@ -620,8 +620,8 @@ gdn_status gdn_state_move(int32_t layers, int32_t slots, int64_t page_bytes, int
  * it has already (keylen > seqlen; what was read back of a full cache, sinks
  * and then the window, serves as it is).  A query that sees no key has o = 0,
  * lse = -inf and no gradient.  What a query does not see does not reach it,
- * not-a-number and infinite values included.  Visible scores that are all
- * -inf count as none.
+ * not-a-number and infinite values included: no bit of its results changes.
+ * Visible scores that are all -inf count as none.
  */
 typedef struct {
     int32_t batch;

@@ -50,3 +50,38 @@ def test_rows_whose_scores_are_all_minus_infinity(dtype, d, T, window, sinks, cu
     for name, y, (w, room) in zip(("dq", "dk", "dv"), got,
                                   gradients(g, *finite, host(o), host(lse), window, sinks, cu, h=HALF[dtype])):
         within(y, w, room, dtype, name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), INF, -INF])
+def test_hidden_values_beside_whole_tiles(dtype, d, bad):
+    """What a query does not see changes no bit of its output or gradients, where its tile is one that other rows see
+    it in and most key tiles are seen whole."""
+    T, window, sinks = 700, 300, 3
+    t, _ = inputs(d, 1, T, T, 2, 1, d, dtype)
+    g = torch.randn(t[0].shape, generator=torch.Generator("cuda").manual_seed(9), device="cuda").to(DT[dtype])
+    o, lse = gdn.swa_fwd(*t, window, sinks)
+    clean = gdn.swa_bwd(g, *t, o, lse, window, sinks)
+    j = torch.arange(T, device="cuda")
+    for where in (200, 333, 650):
+        sees = (j >= where) & (j - where < window)               # queries that see key `where`
+        keys = (j <= where) & ((where - j < window) | (j < sinks))            # keys that query `where` sees
+        for what in ("k", "v", "q", "g"):
+            q, k, v, gg = (y.clone() for y in (*t, g))
+            {"k": k, "v": v, "q": q, "g": gg}[what][0, where, 0, 5] = bad
+            o2, lse2 = gdn.swa_fwd(q, k, v, window, sinks)
+            dq, dk, dv = gdn.swa_bwd(gg, q, k, v, o2, lse2, window, sinks)
+            if what in "kv":
+                rows = sees[None, :, None].expand(1, T, 2)
+                shared = torch.zeros_like(j, dtype=torch.bool)   # keys that some query of those sees
+                for i in torch.nonzero(sees)[:, 0].tolist():
+                    shared |= (j <= i) & ((i - j < window) | (j < sinks))
+                cols = shared
+            else:
+                rows = torch.zeros(1, T, 2, dtype=torch.bool, device="cuda")
+                rows[0, where, 0] = True
+                cols = keys
+            same = (torch.equal(o2[~rows], o[~rows]), torch.equal(lse2[~rows], lse[~rows]), torch.equal(dq[~rows], clean[0][~rows]),
+                    torch.equal(dk[0, ~cols], clean[1][0, ~cols]), torch.equal(dv[0, ~cols], clean[2][0, ~cols]))
+            assert all(same), (what, where, same)
