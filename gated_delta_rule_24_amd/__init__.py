@@ -618,6 +618,11 @@ def state_move_check(status: torch.Tensor) -> int:
 _INT32 = 2 ** 31 - 1
 
 
+def _scale(d, scale):
+    """1 / sqrt(d) for None; heads of no elements are the library's to refuse."""
+    return scale if scale is not None else max(d, 1) ** -0.5
+
+
 @functools.lru_cache(maxsize=256)
 def _swa_desc(which, *fields):
     """Descriptor of these sizes and types, and the workspace size of gdn_swa_<which>."""
@@ -655,7 +660,7 @@ def _swa_call(which, q, k, v, window, sinks, cu_seqlens, cu_seqlens_k, scale):
     if not -_INT32 <= sinks <= _INT32:
         raise ValueError(f"sinks {sinks} is no 32-bit number")
     desc, need = _swa_desc(which, B, T, Tk, H, KV, d, N, max(min(window, _INT32), -_INT32), sinks, _DT[q.dtype],
-                           d ** -0.5 if scale is None else scale)
+                           _scale(d, scale))
     return dev, shape, cu_seqlens_k, desc, need
 
 
@@ -845,7 +850,7 @@ def swa_step(cache, q, k, v, lengths, sinks=0, scales=None, slots=None, *, scale
         workspace, size = _workspace(workspace, need, dev)
     else:
         workspace = None
-    _call("gdn_swa_step", dev, desc, N, H, _DT[q.dtype], d ** -0.5 if scale is None else scale, _addr(q), _addr(k),
+    _call("gdn_swa_step", dev, desc, N, H, _DT[q.dtype], _scale(d, scale), _addr(q), _addr(k),
           _addr(v), _addr(lengths), _addr(slots), _addr(cache), _addr(scales), _addr(o), _addr(workspace), size,
           _addr(status))
     return o
