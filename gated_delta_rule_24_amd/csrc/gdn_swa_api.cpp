@@ -24,6 +24,12 @@ gdn_status check_heads(int32_t heads, int32_t kv_heads) {
     return GDN_OK;
 }
 
+// Scores are taken times scale log2(e).
+gdn_status check_scale(float scale) {
+    if (scale > 0.f && std::isfinite(scale * 1.4426950408889634f)) return GDN_OK;
+    return fail(GDN_ERR_UNSUPPORTED, "scale must be > 0 and at most 2^127");
+}
+
 SwaArgs swa_args(const gdn_swa_desc &d) {
     SwaArgs a{};
     a.B = d.batch, a.T = d.seqlen, a.Tk = d.keylen, a.N = d.num_seqs, a.H = d.heads, a.KV = d.kv_heads, a.D = d.dim;
@@ -47,7 +53,8 @@ gdn_status check_swa_desc(const gdn_swa_desc *d, bool bwd) {
         return fail(GDN_ERR_UNSUPPORTED, "dim %d not built here (32, 64, 128%s)", d->dim, most == 256 ? ", 256" : "");
     if (d->sinks > kSwaMaxSinks)
         return fail(GDN_ERR_UNSUPPORTED, "sinks %d not built (at most %d)", d->sinks, kSwaMaxSinks);
-    if (!(std::isfinite(d->scale) && d->scale > 0.f)) return fail(GDN_ERR_UNSUPPORTED, "scale must be finite and > 0");
+    s = check_scale(d->scale);
+    if (s != GDN_OK) return s;
     // a block for each unit and key head, two where the backward pass splits its key side
     const SwaWorkspace w = swa_workspace_layout(swa_args(*d), bwd);
     if (std::max(w.row_units, 2 * w.key_units) * (int64_t)d->kv_heads >= INT32_MAX - 7)
@@ -269,7 +276,8 @@ gdn_status gdn_swa_step(const gdn_cache_desc *desc, int32_t num_seqs, int32_t he
     s = check_cache_type(d, dtype);
     if (s != GDN_OK) return s;
     if (dtype == GDN_FP32 && d.dim > 128) return fail(GDN_ERR_UNSUPPORTED, "dim %d not built with FP32", d.dim);
-    if (!(std::isfinite(scale) && scale > 0.f)) return fail(GDN_ERR_UNSUPPORTED, "scale must be finite and > 0");
+    s = check_scale(scale);
+    if (s != GDN_OK) return s;
     s = check_cache_seqs(d, num_seqs, slots, scales);
     if (s != GDN_OK) return s;
     SwaStepArgs a{};

@@ -613,7 +613,7 @@ gdn_status gdn_state_move(int32_t layers, int32_t slots, int64_t page_bytes, int
  *              Scores, maxima, sums and lse are fp32.  (The gradient takes its
  *              probabilities from lse: they are off by its rounding, 2^-23 |lse|
  *              relative, which matters for scores past 2^14 or so.)
- *   scale      finite and > 0
+ *   scale      > 0, at most 2^127
  *   flags      0
  * A sequence's queries are its last: the query i stands at position
  * i + (its keys) - (its queries), so that a prompt can go on behind keys that
@@ -792,7 +792,7 @@ gdn_status gdn_swa_step_workspace_size(const gdn_cache_desc *desc, int32_t num_s
  *
  *   heads      H, as for gdn_swa_fwd
  *   dtype      of q, k, v and o: the cache's, or any with E4M3 (FP32: d <= 128)
- *   scale      finite and > 0
+ *   scale      > 0, at most 2^127
  *   q          [N, H, d]   dtype
  *   k, v       [N, KV, d]  dtype
  *   o          [N, H, d]   dtype (written); zeros for a sequence that is left out
