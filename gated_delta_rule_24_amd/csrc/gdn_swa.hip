@@ -13,12 +13,15 @@
 // Only tiles that the mask cuts are masked; tiles that it hides are not visited.
 //
 // Measured (MI355X; a bf16 8192^3 product 1.23 PFLOP/s, a copy 5.35 TB/s): 50408 packed
-// tokens, 16 heads of 128, window 2048, bf16: 810 to 860 us from one GPU to another, 0.85
-// PFLOP/s of visible pairs.  The matrix cores are busy 42% of the time and the vector units about as
+// tokens, 16 heads of 128, window 2048, bf16: 810 to 865 us from one GPU to another, 0.85
+// PFLOP/s of visible pairs; fp16 905 to 935.  The matrix cores are busy 42% of the time and the vector units about as
 // long (per 64 keys and wave 32 products of 32 cycles, 127 vector instructions, 32
 // exponentials of 16 cycles): two waves a SIMD, all that the registers allow, overlap
 // the two in part.  Reads of LDS meet no bank twice (before the swizzle of gdn_swa.h:
 // 1245 us instead of 966).  256 sequences of 9 tokens behind 2052 keys: 202 us, 5.4 TB/s.
+// In fp32 6.84 ms (0.104 PFLOP/s of 0.14), 64-wide heads 3.11; 256-wide heads 2.04 ms in bf16
+// (0.70 PFLOP/s), 2.16 in fp16.  These hold 512 bytes and more of a row in several forms
+// and run one wave a SIMD: with two they spill, 7.53 ms in fp32 (128) and 3.84 in bf16 (256).
 // Tried and not kept: tiles of 32 keys (885 us instead of 835; three waves a SIMD
 // spill), raised wave priority in the products (845 to 850 instead of 839).
 #include "gdn_ops.h"
@@ -330,14 +333,12 @@ __global__ __launch_bounds__(1024) void swa_table_kernel(int N, int T, int Tk, c
     }
 }
 
-static int64_t far_tokens(const SwaArgs &a) { return swa_far_chunk(a.window); }
-
 hipError_t launch_swa_table(const SwaArgs &a, bool bwd, int tokens, int32_t *meta, int2 *rows, int2 *keys,
                             hipStream_t st) {
     ProfScope prof("gdn_swa_table", st);
     const SwaWorkspace w = swa_workspace_layout(a, bwd);
     swa_table_kernel<<<bwd ? 2 : 1, 1024, 0, st>>>(a.N, a.T, a.Tk, a.cu, a.cuk, tokens, a.window, a.sinks,
-                                                   (int)far_tokens(a), (int)w.row_units, (int)w.key_units, meta, rows,
+                                                   swa_far_chunk(a.window), (int)w.row_units, (int)w.key_units, meta, rows,
                                                    keys);
     return hipGetLastError();
 }
@@ -356,7 +357,7 @@ int swa_row_tile(const SwaArgs &a) {
 SwaWorkspace swa_workspace_layout(const SwaArgs &a, bool bwd) {
     SwaWorkspace w{};
     const int tokens = swa_row_tile(a) / (a.H / a.KV);
-    const int64_t T = (int64_t)a.B * a.T, Tk = (int64_t)a.B * a.Tk, far = far_tokens(a);
+    const int64_t T = (int64_t)a.B * a.T, Tk = (int64_t)a.B * a.Tk, far = swa_far_chunk(a.window);
     const bool table = a.B == 1;                  // a packed batch, or one sequence
     w.row_units = T / tokens + a.N;
     w.far_units = a.sinks ? Tk / far : 0;         // a sequence has keys / far at most

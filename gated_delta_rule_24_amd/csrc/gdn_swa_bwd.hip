@@ -16,9 +16,10 @@
 // gradients goes to the workspace in fp32, and a last kernel adds the parts.
 //
 // Measured (MI355X): 4 x 4096 tokens, 16 heads on 4 of 128, window 2048, 4 sinks, bf16: query
-// side 295 us (1.05 PFLOP/s over its three products, the matrix cores busy 44%), key side
-// 610 to 650 (0.82 over its five, busy 38%).  32768 tokens, 16 heads on 8 of 64, 16 sinks,
-// fp16: 435 and 665 to 715.  Both are bound by what two waves a SIMD overlap of products,
+// side 295 to 300 us (1.05 PFLOP/s over its three products, the matrix cores busy 52%), key side
+// 610 to 630 (0.82 over its five, busy 35%).  32768 tokens, 16 heads on 8 of 64, 16 sinks,
+// fp16: 456 to 468 and 695 to 740.  The first case in fp32: 3.0 and 5.8 ms with one wave a
+// SIMD, 3.4 and 6.75 with two, which spill; with 64-wide heads 1.27 and 2.19.  Both are bound by what two waves a SIMD overlap of products,
 // exponentials and LDS reads; the key side also has two or three times as many units
 // of unequal length as blocks fit.  Key side, of the same first case: far parts of the
 // sinks without masks 965 -> 757 us, no looks for values that are not finite in masked
@@ -237,7 +238,7 @@ __device__ __forceinline__ int64_t far_first(int64_t k0, int far) { return 2 * (
 // different blocks, the second with S once more (5 products instead of 4).
 // Measured, 4 x 4096 tokens, 16 heads on 4 of 128, window 2048, in bf16: different blocks
 // 1118 us, one block for both 3715 with two waves a SIMD (registers spill) and 1195 with
-// one; since then the split form has come to 610 to 650.  4096 tokens, 16 heads on 8 of 64,
+// one; since then the split form has come to 610 to 630.  4096 tokens, 16 heads on 8 of 64,
 // in fp32: 817 us split, 684 not.
 template <typename T, int D>
 constexpr bool kSplitKeySide = D == 128;
