@@ -19,9 +19,9 @@
 // side 295 to 300 us (1.05 PFLOP/s over its three products, the matrix cores busy 52%), key side
 // 610 to 630 (0.82 over its five, busy 35%).  32768 tokens, 16 heads on 8 of 64, 16 sinks,
 // fp16: 456 to 468 and 695 to 740.  The first case in fp32: 3.0 and 5.8 ms with one wave a
-// SIMD, 3.4 and 6.75 with two, which spill; with 64-wide heads 1.27 and 2.19.  Both are bound by what two waves a SIMD overlap of products,
-// exponentials and LDS reads; the key side also has two or three times as many units
-// of unequal length as blocks fit.  Key side, of the same first case: far parts of the
+// SIMD, 3.4 and 6.75 with two, which spill; with 64-wide heads 1.27 and 2.19.  Both are bound
+// by what two waves a SIMD overlap of products, exponentials and LDS reads; the key side
+// also has two or three times as many units of unequal length as blocks fit.  Key side, of the same first case: far parts of the
 // sinks without masks 965 -> 757 us, no looks for values that are not finite in masked
 // tiles 757 -> 614, reads in batches 650 -> 628 (another GPU).
 #include "gdn_ops.h"
@@ -542,8 +542,9 @@ __global__ __launch_bounds__(256, (Rows<T, D>::RB >= 512 ? 1 : 2)) void swa_dkv_
 // of lanes, which take the parts in turn and join in LDS, in a fixed order.
 constexpr int kSinkLanes = 32;
 template <typename T>
-__global__ __launch_bounds__(1024) void swa_sinks_kernel(SwaShape sh, int pairs, int far, int D, const float *__restrict__ share,
-                                                         T *__restrict__ dk, T *__restrict__ dv) {
+__global__ __launch_bounds__(1024) void swa_sinks_kernel(SwaShape sh, int pairs, int far, int D,
+                                                         const float *__restrict__ share, T *__restrict__ dk,
+                                                         T *__restrict__ dv) {
     __shared__ float sum[32][kSinkLanes + 1];
     if (sh.cu && sh.meta[1]) return;
     const int pair = (int)(blockIdx.z << kGridBits | blockIdx.x);   // sequence, key head

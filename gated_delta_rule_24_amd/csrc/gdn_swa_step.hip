@@ -15,10 +15,10 @@
 // Measured (MI355X, a copy 5.35 TB/s), 16 heads on 4 of 128: 256 sequences of 1029 to 2052
 // rows in 8 bits 99 to 103 us (515 MB, 5.1 TB/s), in bf16 181 (997 MB, 5.5); of up to 8192
 // rows in 8 bits 375 (2.05 GB, 5.5).  In fp32 372 (1.99 GB, 5.35), heads of 64 208 (0.997
-// GB, 4.8: some registers spill); 8-bit heads of 256 207 (1.01 GB, 4.9).  Two sequences of up to 65536 rows, fp16, 43 us and
-// 5 for the join (268 MB).  What is left are the first loads, behind those of slot and
-// length, and the last blocks.  128 registers, so that four blocks fit a CU: with 160
-// the bf16 case takes 205 us.
+// GB, 4.8: some registers spill); 8-bit heads of 256 207 (1.01 GB, 4.9).  Two sequences of
+// up to 65536 rows, fp16, 43 us and 5 for the join (268 MB).  What is left are the first
+// loads, behind those of slot and length, and the last blocks.  128 registers, so that four
+// blocks fit a CU: with 160 the bf16 case takes 205 us.
 #include "gdn_cache.h"
 #include "gdn_swa.h"
 
